@@ -781,6 +781,158 @@ moe_status_t moe_fc1_wgrad_tf32(const moe_mlp_desc_t* desc, const void* dh_t, co
                                 const int32_t* counts, const int32_t* padded_offsets,
                                 void* dw1p, cudaStream_t stream);
 
+/* ---------------------------------------------------------- residual block
+ * The norms around the routed-expert MLP in a residual block, fused with the
+ * block's gate and residual scale, forward and backward.  The pages name the
+ * MoE block and its memory-bound passes ([FK] "Overcoming training
+ * bottlenecks in the MoE block") but print none of these formulas:
+ *
+ *   pre norm    x  = N1(r)                                 the MLP's input
+ *   post norm   r' = res_scale*r + branch_scale * G (*) N2(y)
+ *               x' = N1(r')                    the next block's input, optional
+ *
+ * N(v) = xhat*(offset + w) + b, xhat = (v - mu)*rstd over the d channels:
+ *   MOE_NORM_RMS    mu = 0,       rstd = 1/sqrt(mean(v^2) + eps)
+ *   MOE_NORM_LAYER  mu = mean(v), rstd = 1/sqrt(mean((v-mu)^2) + eps)
+ *   MOE_NORM_NONE   N(v) = v (no weight, no bias)
+ * w = NULL: N(v) = xhat (+ b); b = NULL: no bias.  The gate G = act(gate) is
+ * 1 (MOE_GATE_NONE), a value per channel, per token, or per element.
+ * Everything is computed in fp32 (rows are read once; the squares of |v| up
+ * to about 1e18 do not overflow) and rounded once when stored: x' comes from
+ * the unrounded r'.  An Inf or NaN stays within its row (and reaches the
+ * parameter gradients).
+ *
+ * Row tensors are moe_rows_t: element (t, c) at p[t*ld + c], ld >= d in
+ * elements, any element alignment.  With d a multiple of 8 and every row
+ * 16-byte aligned the kernels move 16 bytes per thread, otherwise single
+ * elements. */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind_t;
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,  /* gate [d], param_dtype (ld unused) */
+  MOE_GATE_TOKEN = 2,    /* gate fp32, token t's at p[t*ld], ld >= 1 */
+  MOE_GATE_FULL = 3      /* gate [T,d], dtype */
+} moe_gate_kind_t;
+typedef enum { MOE_GATE_ACT_NONE = 0, MOE_GATE_ACT_SIGMOID = 1, MOE_GATE_ACT_TANH = 2 } moe_gate_act_t;
+
+typedef struct {
+  void* p;      /* device pointer (inputs are not written), NULL = absent */
+  int64_t ld;   /* elements from one row to the next */
+} moe_rows_t;
+
+typedef struct {
+  int32_t T;            /* tokens, >= 0 */
+  int32_t d;            /* channels, 1..16384 */
+  int32_t dtype;        /* x, y, full gates: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 */
+  int32_t res_dtype;    /* r, r' and their gradients: BF16 or FP32 (FP32 when
+                           dtype is FP32) */
+  int32_t param_dtype;  /* weights, biases, channel gate and their gradients */
+  int32_t pre_norm;     /* moe_norm_kind_t of N1 */
+  int32_t post_norm;    /* moe_norm_kind_t of N2 */
+  int32_t gate;         /* moe_gate_kind_t */
+  int32_t gate_act;     /* moe_gate_act_t */
+  float pre_eps, post_eps;        /* > 0 */
+  float pre_offset, post_offset;  /* added to the weights (1: stored around 0) */
+  float res_scale, branch_scale;
+} moe_block_norm_desc_t;
+
+/* Parameters, and (in the backward, written, each may be NULL) their
+ * gradients.  gate: see moe_gate_kind_t. */
+typedef struct {
+  void* pre_w;
+  void* pre_b;
+  void* post_w;
+  void* post_b;
+  moe_rows_t gate;
+} moe_block_params_t;
+
+/* The branch output given as routed expert rows: y[t] = sum_s topk_w[t,s] *
+ * Y[row_of[t,s]] (fp32 in slot order, as moe_unpermute_combine), Y the y
+ * argument with `capacity` rows.  y_out (optional, dtype): the combined rows,
+ * which the backward reads.  A row_of outside [0,capacity) sets
+ * MOE_DEV_BAD_OFFSETS and counts as a zero row. */
+typedef struct {
+  const int32_t* row_of;  /* [T,k] */
+  const float* topk_w;    /* [T,k] */
+  int32_t k;              /* 1..32 */
+  int32_t capacity;
+  moe_rows_t y_out;
+} moe_routed_rows_t;
+
+/* Bytes of the backward calls' workspace (partial sums of the parameter
+ * gradients). */
+moe_status_t moe_block_norm_workspace_size(const moe_block_norm_desc_t* desc, size_t* bytes);
+
+/* x = N1(res); uses desc's pre_* fields. */
+moe_status_t moe_block_pre_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows_t res,
+                                    const void* w, const void* b, moe_rows_t x,
+                                    cudaStream_t stream);
+
+/* Gradient of the pre norm joined to the residual's own:
+ *   dres = dres_scale*dres_in + N1^T(dx; res)
+ * (dres_in.p = NULL: without the first term; dres_scale is the block's
+ * res_scale where dres_in is the gradient of r'), dw [d] = sum_t dx*xhat,
+ * db [d] = sum_t dx (param_dtype, NULL = not wanted).  dres may be dres_in. */
+moe_status_t moe_block_pre_norm_bwd(const moe_block_norm_desc_t* desc, moe_rows_t dx,
+                                    moe_rows_t res, const void* w, moe_rows_t dres_in,
+                                    float dres_scale, moe_rows_t dres, void* dw, void* db,
+                                    void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* res_out = res_scale*res + branch_scale * G (*) N2(y), and where x.p is not
+ * NULL x = N1(res_out) (before its rounding).  res_out may be res.  routed
+ * (NULL = y holds the T rows themselves): see moe_routed_rows_t. */
+moe_status_t moe_block_post_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows_t res,
+                                     moe_rows_t y, const moe_block_params_t* params,
+                                     moe_rows_t res_out, moe_rows_t x,
+                                     const moe_routed_rows_t* routed, cudaStream_t stream);
+
+/* Gradient of moe_block_post_norm_fwd, the next norm's part included where
+ * dx.p is not NULL (then res_out is read):
+ *   D  = dres_scale*dres_in + N1^T(dx; res_out)
+ *   dy = N2^T(branch_scale * G (*) D; y)
+ * dres (optional): D, the gradient of res_out; the gradient of res itself is
+ * res_scale*D, which the pre norm's backward applies as its dres_scale.
+ * grads: the parameters' gradients over the T rows (written, not added to).
+ * At least one of dres_in, dx is given; dres may be dres_in. */
+moe_status_t moe_block_post_norm_bwd(const moe_block_norm_desc_t* desc, moe_rows_t dres_in,
+                                     float dres_scale, moe_rows_t dx, moe_rows_t res_out,
+                                     moe_rows_t y, const moe_block_params_t* params,
+                                     moe_rows_t dres, moe_rows_t dy,
+                                     const moe_block_params_t* grads, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream);
+
+/* ------------------------------------------- gradient norm and clipping
+ * A list of n gradient tensors (a HOST array, read before the call returns),
+ * each `rows` rows of `cols` elements, row r at grad + r*ld; rows = 1 for a
+ * contiguous tensor of any shape.  rows*cols may be 0. */
+typedef struct {
+  const void* grad;
+  void* out;           /* moe_clip_grads: may be grad itself (same type, ld) */
+  int64_t rows, cols;
+  int64_t ld, ld_out;  /* >= cols where rows > 1 */
+  int32_t dtype;       /* MOE_DTYPE_BF16 or MOE_DTYPE_FP32 */
+  int32_t out_dtype;
+} moe_grad_t;
+
+typedef enum { MOE_GRAD_NORM_L2 = 0, MOE_GRAD_NORM_INF = 1 } moe_grad_norm_t;
+
+/* Bytes of moe_grad_norm's workspace for a list of n tensors. */
+moe_status_t moe_grad_norm_workspace_size(int32_t n, size_t* bytes);
+
+/* norm[0] (fp32, device) = the list's 2-norm or largest magnitude; norms [n]
+ * (optional): each tensor's.  Squares are summed in fp32 over 32 elements
+ * and in fp64 beyond, and again in fp64 where the fp32 sum leaves its range,
+ * so any finite gradients have a finite sum; the order is fixed, so equal
+ * lists have equal norms.  Inf gives Inf, NaN NaN. */
+moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t n, int32_t norm_type, float* norm,
+                           float* norms, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* out = grad * min(1, max_norm / (norm[0] + eps)) for every tensor, norm read
+ * on the device.  A NaN norm gives NaN, an Inf norm a factor of 0.  Tensors
+ * clipped in place are not touched where the factor is 1. */
+moe_status_t moe_clip_grads(const moe_grad_t* grads, int32_t n, const float* norm, float max_norm,
+                            float eps, cudaStream_t stream);
+
 /* moe_route_permute for callers that cannot allocate device memory (for
  * example a host program whose device memory is all handed to its own fixed
  * pool, or a runtime that allows no allocation after start-up).  The pages

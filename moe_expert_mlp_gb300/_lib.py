@@ -45,8 +45,15 @@ EXPORTS = (
     "moe_fc2_dgrad_dglu_recompute_mx", "moe_route_permute_mx", "moe_unpermute_combine_bwd_mx",
     "moe_transpose_weights_tf32", "moe_transpose_rows_f32", "moe_fc1_glu_fwd_tf32",
     "moe_fc2_fwd_tf32", "moe_fc2_dgrad_dglu_tf32", "moe_fc2_wgrad_tf32", "moe_fc1_dgrad_tf32",
-    "moe_fc1_wgrad_tf32", "moe_selftest_grid_wait_timeout",
+    "moe_fc1_wgrad_tf32", "moe_selftest_grid_wait_timeout", "moe_block_norm_workspace_size",
+    "moe_block_pre_norm_fwd", "moe_block_pre_norm_bwd", "moe_block_post_norm_fwd",
+    "moe_block_post_norm_bwd", "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_clip_grads",
 )
+
+NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+GATES = {None: 0, "none": 0, "channel": 1, "token": 2, "full": 3}
+GATE_ACTS = {None: 0, "none": 0, "sigmoid": 1, "tanh": 2}
+GRAD_NORMS = {"l2": 0, "inf": 1}
 
 
 class MoeError(RuntimeError):
@@ -78,6 +85,35 @@ class moe_mx_weights_t(ctypes.Structure):
 
 class moe_nv_weights_t(ctypes.Structure):
     _fields_ = [("q", moe_mx_weights_t), ("amax", ctypes.c_void_p)]
+
+
+class moe_rows_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class moe_block_norm_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "d", "dtype", "res_dtype", "param_dtype", "pre_norm", "post_norm", "gate",
+                 "gate_act")]
+    _fields_ += [(n, ctypes.c_float) for n in
+                 ("pre_eps", "post_eps", "pre_offset", "post_offset", "res_scale",
+                  "branch_scale")]
+
+
+class moe_block_params_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pre_w", "pre_b", "post_w", "post_b")]
+    _fields_ += [("gate", moe_rows_t)]
+
+
+class moe_routed_rows_t(ctypes.Structure):
+    _fields_ = [("row_of", ctypes.c_void_p), ("topk_w", ctypes.c_void_p), ("k", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("y_out", moe_rows_t)]
+
+
+class moe_grad_t(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 def _nvw(w):
@@ -119,6 +155,21 @@ def make_desc(T, E, k, d, F, act="swiglu", alpha=1.0, limit=math.inf, linear_off
                           int(recompute_h))
 
 
+def make_block_norm_desc(T, d, dtype="bf16", res_dtype=None, param_dtype=None, pre_norm="rms",
+                         post_norm=None, pre_eps=1e-6, post_eps=1e-6, pre_offset=0.0,
+                         post_offset=0.0, gate=None, gate_act=None, res_scale=1.0,
+                         branch_scale=1.0):
+    """Descriptor of a residual block's norms (see include/moe.h): norms "rms",
+    "layer" or None; gate None, "channel", "token" or "full"; gate_act None,
+    "sigmoid" or "tanh"; types "bf16" or "fp32" (res_dtype and param_dtype
+    default to dtype)."""
+    dt = {"bf16": MOE_DTYPE_BF16, "fp32": MOE_DTYPE_FP32}
+    return moe_block_norm_desc_t(
+        T, d, dt[dtype], dt[res_dtype or dtype], dt[param_dtype or dtype], NORMS[pre_norm],
+        NORMS[post_norm], GATES[gate], GATE_ACTS[gate_act], pre_eps, post_eps, pre_offset,
+        post_offset, res_scale, branch_scale)
+
+
 _lib = None
 
 
@@ -131,6 +182,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P = ctypes.c_void_p
         D = ctypes.POINTER(moe_mlp_desc_t)
+        R = moe_rows_t
         sig = {
             "moe_fc1_padded_width": (ctypes.c_int32, [ctypes.c_int32]),
             "moe_workspace_size": (ctypes.c_int, [D, ctypes.POINTER(ctypes.c_size_t)]),
@@ -207,6 +259,19 @@ def lib():
             "moe_fc2_wgrad_tf32": (ctypes.c_int, [D] + [P] * 6),
             "moe_fc1_dgrad_tf32": (ctypes.c_int, [D] + [P] * 6),
             "moe_fc1_wgrad_tf32": (ctypes.c_int, [D] + [P] * 6),
+            "moe_block_norm_workspace_size": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_block_pre_norm_fwd": (ctypes.c_int, [P, R, P, P, R, P]),
+            "moe_block_pre_norm_bwd": (ctypes.c_int, [P, R, R, P, R, ctypes.c_float, R, P, P, P,
+                                                      ctypes.c_size_t, P]),
+            "moe_block_post_norm_fwd": (ctypes.c_int, [P, R, R, P, R, R, P, P]),
+            "moe_block_post_norm_bwd": (ctypes.c_int, [P, R, ctypes.c_float, R, R, R, P, R, R, P,
+                                                       P, ctypes.c_size_t, P]),
+            "moe_grad_norm_workspace_size": (ctypes.c_int, [ctypes.c_int32,
+                                                            ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_grad_norm": (ctypes.c_int, [P, ctypes.c_int32, ctypes.c_int32, P, P, P,
+                                             ctypes.c_size_t, P]),
+            "moe_clip_grads": (ctypes.c_int, [P, ctypes.c_int32, P, ctypes.c_float,
+                                              ctypes.c_float, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -644,3 +709,213 @@ def moe_fc1_dgrad_tf32(desc, dh, counts, padded_offsets, w1t, dx_perm, stream=No
 def moe_fc1_wgrad_tf32(desc, dh_t, x_t, counts, padded_offsets, dw1p, stream=None):
     _check(lib().moe_fc1_wgrad_tf32(ctypes.byref(desc), _p(dh_t), _p(x_t), _p(counts),
                                     _p(padded_offsets), _p(dw1p), _stream(stream)))
+
+
+# ------------------------------------------------- residual block's norms
+_TORCH = {MOE_DTYPE_BF16: torch.bfloat16, MOE_DTYPE_FP32: torch.float32}
+_NO_ROWS = moe_rows_t(None, 0)
+
+
+def _rows(t, n, d, dtype):
+    """A [n, d] tensor of the given type with unit stride along the channels
+    (any stride between rows) -> moe_rows_t."""
+    if t is None:
+        return _NO_ROWS
+    if t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"expected a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
+    if t.dim() != 2 or t.size(0) != n or t.size(1) != d:
+        raise ValueError(f"expected a tensor of shape {(n, d)}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if (step != 1 and d > 1) or (ld < d and n > 1):
+        raise ValueError(f"rows must be contiguous and apart, got strides {t.stride()}")
+    return moe_rows_t(t.data_ptr(), ld if n > 1 else max(ld, d))
+
+
+def _vector(t, d, dtype):
+    """A contiguous [d] parameter (or its gradient) -> pointer, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != d or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous {dtype} CUDA tensor of {d} values, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _block_params(desc, p):
+    """dict of optional tensors {pre_w, pre_b, post_w, post_b, gate} ->
+    moe_block_params_t."""
+    dt, d = _TORCH[desc.param_dtype], desc.d
+    g, gate = p.get("gate"), _NO_ROWS
+    if g is not None and desc.gate:
+        if desc.gate == 1:
+            gate = moe_rows_t(_vector(g, d, dt), 0)
+        elif desc.gate == 3:
+            gate = _rows(g, desc.T, d, _TORCH[desc.dtype])
+        else:
+            if g.dtype is not torch.float32 or not g.is_cuda or g.dim() != 1 or g.size(0) != desc.T:
+                raise ValueError(f"expected an fp32 CUDA gate of {desc.T} tokens, got {g.dtype} "
+                                 f"{tuple(g.shape)} on {g.device}")
+            if g.stride(0) < 1 and desc.T > 1:
+                raise ValueError("the tokens' gates must be apart")
+            gate = moe_rows_t(g.data_ptr(), max(g.stride(0), 1))
+    return moe_block_params_t(_vector(p.get("pre_w"), d, dt), _vector(p.get("pre_b"), d, dt),
+                              _vector(p.get("post_w"), d, dt), _vector(p.get("post_b"), d, dt),
+                              gate)
+
+
+def moe_block_norm_workspace_size(desc):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_block_norm_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_block_pre_norm_fwd(desc, res, w, b, x, stream=None):
+    """x = N1(res)."""
+    T, d, dt = desc.T, desc.d, _TORCH[desc.param_dtype]
+    _check(lib().moe_block_pre_norm_fwd(
+        ctypes.byref(desc), _rows(res, T, d, _TORCH[desc.res_dtype]), _vector(w, d, dt),
+        _vector(b, d, dt), _rows(x, T, d, _TORCH[desc.dtype]), _stream(stream)))
+
+
+def moe_block_pre_norm_bwd(desc, dx, res, w, dres_in, dres, dw, db, ws, dres_scale=1.0,
+                           stream=None):
+    """dres = dres_scale*dres_in + N1^T(dx); dw, db or None."""
+    T, d, dt = desc.T, desc.d, _TORCH[desc.param_dtype]
+    rt = _TORCH[desc.res_dtype]
+    _check(lib().moe_block_pre_norm_bwd(
+        ctypes.byref(desc), _rows(dx, T, d, _TORCH[desc.dtype]), _rows(res, T, d, rt),
+        _vector(w, d, dt), _rows(dres_in, T, d, rt), dres_scale, _rows(dres, T, d, rt),
+        _vector(dw, d, dt), _vector(db, d, dt), _p(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def moe_block_post_norm_fwd(desc, res, y, params, res_out, x=None, routed=None, stream=None):
+    """res_out = res_scale*res + branch_scale*G*N2(y), x = N1(res_out) or None.
+    params: dict {pre_w, pre_b, post_w, post_b, gate}; routed: dict {row_of,
+    topk_w, y_out} with y the expert rows [capacity, d]."""
+    T, d = desc.T, desc.d
+    at, rt = _TORCH[desc.dtype], _TORCH[desc.res_dtype]
+    rows = None
+    if routed is not None:
+        r, w = routed["row_of"], routed["topk_w"]
+        if (r.dtype is not torch.int32 or w.dtype is not torch.float32 or r.dim() != 2
+                or r.size(0) != T or r.shape != w.shape):
+            raise ValueError("row_of must be int32 [T,k] and topk_w fp32 [T,k]")
+        rows = ctypes.byref(moe_routed_rows_t(_p(r).value, _p(w).value, r.size(1), y.size(0),
+                                              _rows(routed.get("y_out"), T, d, at)))
+    _check(lib().moe_block_post_norm_fwd(
+        ctypes.byref(desc), _rows(res, T, d, rt), _rows(y, T if rows is None else y.size(0), d, at),
+        ctypes.byref(_block_params(desc, params)), _rows(res_out, T, d, rt), _rows(x, T, d, at),
+        rows, _stream(stream)))
+
+
+def moe_block_post_norm_bwd(desc, dres_in, dx, res_out, y, params, dres, dy, grads, ws,
+                            dres_scale=1.0, stream=None):
+    """dres = dres_scale*dres_in + N1^T(dx; res_out) (dx None: without the next
+    norm), dy = N2^T(branch_scale*G*dres; y) and the parameters' gradients
+    (grads: dict like params, each optional)."""
+    T, d = desc.T, desc.d
+    at, rt = _TORCH[desc.dtype], _TORCH[desc.res_dtype]
+    _check(lib().moe_block_post_norm_bwd(
+        ctypes.byref(desc), _rows(dres_in, T, d, rt), dres_scale, _rows(dx, T, d, at),
+        _rows(res_out, T, d, rt), _rows(y, T, d, at), ctypes.byref(_block_params(desc, params)),
+        _rows(dres, T, d, rt), _rows(dy, T, d, at), ctypes.byref(_block_params(desc, grads)),
+        _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------- gradient norm and clipping
+def _runs(t, out):
+    """(rows, cols, ld, ld_out) of a tensor whose elements lie in runs of equal
+    length and distance, in the memory order of t; out in the same order."""
+    if t.numel() == 0:
+        return (1, 0, 0, 0)
+    dims = sorted((i for i in range(t.dim()) if t.size(i) != 1), key=lambda i: -t.stride(i))
+    runs = []                                  # [size, stride, stride of out], outermost first
+    for i in dims:
+        n, s, so = t.size(i), t.stride(i), out.stride(i)
+        if runs and runs[-1][1] == n * s and runs[-1][2] == n * so:
+            runs[-1] = [runs[-1][0] * n, s, so]
+        else:
+            runs.append([n, s, so])
+    if not runs or runs[-1][1] != 1 or runs[-1][2] != 1:
+        runs.append([1, 1, 1])                 # no unit stride: rows of one element
+    cols = runs[-1][0]
+    if len(runs) == 1:
+        return (1, cols, cols, cols)
+    rows, ld, ld_out = runs[0]
+    if len(runs) > 2 or ld < cols or ld_out < cols:
+        raise ValueError(f"gradient of shape {tuple(t.shape)} and strides {t.stride()} (out: "
+                         f"{out.stride()}) is not rows at one distance")
+    return (rows, cols, ld, ld_out)
+
+
+class GradList:
+    """Gradient tensors (bf16 or fp32, contiguous or rows at one distance) and
+    where their clipped copies go (outs; default: in place), described for
+    moe_grad_norm and moe_clip_grads.  The list holds the tensors; one whose
+    memory was replaced or resized since (`tensor.data = ...`) is described
+    anew at the next call."""
+
+    def __init__(self, tensors, outs=None):
+        self.tensors = list(tensors)
+        self.outs = self.tensors if outs is None else list(outs)
+        if len(self.outs) != len(self.tensors):
+            raise ValueError(f"{len(self.tensors)} gradients and {len(self.outs)} outputs")
+        self.array = (moe_grad_t * max(len(self.tensors), 1))()
+        self._places = None
+        self.refresh()
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def refresh(self):
+        places = [t.data_ptr() for t in self.tensors] + [t.numel() for t in self.tensors]
+        if self.outs is not self.tensors:
+            places += [t.data_ptr() for t in self.outs]
+            places += [t.numel() for t in self.outs]
+        if places == self._places:
+            return
+        kinds = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
+        for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
+            if t.dtype not in kinds or o.dtype not in kinds or not t.is_cuda or not o.is_cuda:
+                raise ValueError(f"gradient {i}: expected bf16 or fp32 CUDA tensors, got {t.dtype} "
+                                 f"on {t.device} and {o.dtype} on {o.device}")
+            if t.shape != o.shape:
+                raise ValueError(f"gradient {i}: shapes {tuple(t.shape)} and {tuple(o.shape)}")
+            self.array[i] = moe_grad_t(t.data_ptr(), o.data_ptr(), *_runs(t, o), kinds[t.dtype],
+                                       kinds[o.dtype])
+        self._places = places
+
+
+def _grad_list(grads):
+    if not isinstance(grads, GradList):
+        return GradList(grads)
+    grads.refresh()
+    return grads
+
+
+def moe_grad_norm_workspace_size(n):
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_grad_norm_workspace_size(n, ctypes.byref(b)))
+    return int(b.value)
+
+
+def moe_grad_norm(grads, norm, norms, norm_type, ws, stream=None):
+    """Global norm of a GradList (or a list of tensors) into norm fp32 [1], and
+    each tensor's into norms fp32 [n] (or None); norm_type "l2" or "inf"."""
+    g = _grad_list(grads)
+    if norm.dtype is not torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one fp32 value")
+    if norms is not None and (norms.dtype is not torch.float32 or norms.numel() != len(g)):
+        raise ValueError(f"norms must be {len(g)} fp32 values")
+    _check(lib().moe_grad_norm(g.array, len(g), GRAD_NORMS[norm_type], _p(norm), _p(norms), _p(ws),
+                               ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_clip_grads(grads, norm, max_norm, eps=1e-6, stream=None):
+    """outs = grads * min(1, max_norm / (norm + eps)), norm fp32 [1] on the
+    device."""
+    g = _grad_list(grads)
+    if norm.dtype is not torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one fp32 value")
+    _check(lib().moe_clip_grads(g.array, len(g), _p(norm), max_norm, eps, _stream(stream)))

@@ -263,6 +263,15 @@ void fill_common(GemmArgs& a, const moe_mlp_desc_t* d, const DeviceInfo* di,
 }  // namespace moe
 
 namespace moe {
+moe_status_t current_device(int* sms, int** status) {
+  DeviceInfo* di;
+  const moe_status_t st = device_info(&di);
+  if (st != MOE_OK) return st;
+  *sms = di->sms;
+  *status = di->status;
+  return MOE_OK;
+}
+
 bool encode_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t row_bytes, uint64_t plane_bytes, uint32_t box0, uint32_t box1,
                    CUtensorMapSwizzle swizzle, CUtensorMapDataType dtype) {

@@ -16,6 +16,10 @@ constexpr int kMaxTopK = 32;
 constexpr int kAlign = 128;            // group alignment = GEMM tile rows
 constexpr int kGluHalf = 128;          // packed FC1 block: 128 gate + 128 linear rows
 
+// SM count and status word of the current device (moe_api.cu); MOE_ERR_ARCH
+// unless it is sm_103.
+moe_status_t current_device(int* sms, int** status);
+
 inline int fc1_pad(int F) { return (F + kGluHalf - 1) / kGluHalf * kGluHalf; }
 
 // ------------------------------------------------ memory-bound kernels
