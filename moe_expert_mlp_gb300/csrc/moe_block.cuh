@@ -22,6 +22,7 @@ namespace moe {
 constexpr int kBlockThreads = 512;   // threads of a block at most
 constexpr int kUnit = 8;             // channels of a unit
 constexpr int kBlockMaxD = 16384;    // 512 threads x 4 units
+constexpr int kFewRows = 2;          // rows an SM up to which a row's latency counts
 
 // Row tensor: element (t, c) at p[t * ld + c].
 struct BlockRows {
@@ -38,7 +39,7 @@ struct BlockNorm {
 
 struct BlockArgs {
   int T, d;
-  int tpr, nv;       // threads of a group, units of a thread
+  int tpr;           // threads of a group (the launchers')
   int vec;           // every row 16-byte aligned and d % 8 == 0
   int p32;           // parameters are fp32 (else bf16)
   int gate, gate_act;
@@ -59,24 +60,18 @@ struct BlockArgs {
   BlockRows dgate;   // token, full
 };
 
-// Channels of unit u of thread `lane` of its group.
-struct UnitMap {
-  int c0, step, n;
-};
-
-__device__ __forceinline__ UnitMap unit_map(const BlockArgs& p, int lane, int u) {
-  UnitMap m;
-  if (p.vec) {
-    m.c0 = (u * p.tpr + lane) * kUnit;
-    m.step = 1;
-    m.n = m.c0 < p.d ? kUnit : 0;
-  } else {
-    m.c0 = u * kUnit * p.tpr + lane;
-    m.step = p.tpr;
-    m.n = m.c0 < p.d ? min(kUnit, (p.d - m.c0 + p.tpr - 1) / p.tpr) : 0;
+// Channels of unit u of thread `lane` of its group: c0, c0 + step, ..., those
+// below d.  VEC: 8 neighbours, all or none.
+template <bool VEC>
+struct Unit {
+  int c0, d, tpr;
+  __device__ __forceinline__ Unit() {}
+  __device__ __forceinline__ Unit(const BlockArgs& p, int lane, int u) : d(p.d), tpr(p.tpr) {
+    c0 = VEC ? (u * p.tpr + lane) * kUnit : u * kUnit * p.tpr + lane;
   }
-  return m;
-}
+  __device__ __forceinline__ int at(int e) const { return VEC ? c0 + e : c0 + e * tpr; }
+  __device__ __forceinline__ bool has(int e) const { return VEC ? c0 < d : c0 + e * tpr < d; }
+};
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -89,44 +84,58 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  v[0] = bf16_lo(w.x);
-  v[1] = bf16_hi(w.x);
-  v[2] = bf16_lo(w.y);
-  v[3] = bf16_hi(w.y);
-  v[4] = bf16_lo(w.z);
-  v[5] = bf16_hi(w.z);
-  v[6] = bf16_lo(w.w);
-  v[7] = bf16_hi(w.w);
+// 16 bytes of a row, read once: they do not displace the parameters in L1.
+__device__ __forceinline__ uint4 load16_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
-// The unit's elements of one row, 0 past the row's end.
-template <typename T>
-__device__ __forceinline__ void load_unit(const T* row, const UnitMap& m, bool vec, float (&v)[8]) {
-  if (vec) {
-    if (m.n) {
-      if constexpr (sizeof(T) == 2) {
-        unpack8(*reinterpret_cast<const uint4*>(row + m.c0), v);
-      } else {
-        const float4 a = *reinterpret_cast<const float4*>(row + m.c0);
-        const float4 b = *reinterpret_cast<const float4*>(row + m.c0 + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// A unit's 8 elements as they lie in memory (VEC: 16 bytes in bf16, 32 in
+// fp32; else one register each), 0 past the row's end.
+template <typename T, bool VEC>
+struct Raw {
+  static constexpr int kWords = VEC ? 2 * sizeof(T) : 8;
+  uint32_t w[kWords];
+
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const T* row, const Unit<VEC>& m) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        const uint4* from = reinterpret_cast<const uint4*>(row + m.c0) + i;
+        if (m.has(0)) q = ONCE ? load16_once(from) : *from;
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      for (int e = 0; e < 8; ++e) w[e] = m.has(e) ? __float_as_uint(to_f32(row[m.at(e)])) : 0u;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < m.n ? to_f32(row[m.c0 + e * m.step]) : 0.0f;
   }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (VEC && sizeof(T) == 2)
+      return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    else
+      return __uint_as_float(w[e]);
+  }
+};
+
+// The unit's elements of one row: read once, past L1.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_row(const T* row, const Unit<VEC>& m, float (&v)[8]) {
+  Raw<T, VEC> r;
+  r.template load<true>(row, m);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = r.get(e);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_unit(T* row, const UnitMap& m, bool vec, const float (&v)[8]) {
-  if (vec) {
-    if (m.n) {
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_unit(T* row, const Unit<VEC>& m, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (m.has(0)) {
       if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<uint4*>(row + m.c0) =
             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
@@ -139,25 +148,29 @@ __device__ __forceinline__ void store_unit(T* row, const UnitMap& m, bool vec, c
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < m.n) row[m.c0 + e * m.step] = from_f32<T>(v[e]);
+      if (m.has(e)) row[m.at(e)] = from_f32<T>(v[e]);
   }
 }
 
-// The unit's elements of a parameter vector (bf16 or fp32), `absent` where
-// there is none.
-__device__ __forceinline__ void load_param(const void* w, const BlockArgs& p, const UnitMap& m,
+// The unit's elements of a parameter vector (bf16 or fp32) plus `off`,
+// `absent` where there is none.
+template <bool VEC>
+__device__ __forceinline__ void load_param(const void* w, const BlockArgs& p, const Unit<VEC>& m,
                                            float off, float absent, float (&v)[8]) {
   if (w == nullptr) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = absent;
-    return;
-  }
-  if (p.p32)
-    load_unit(static_cast<const float*>(w), m, p.vec, v);
-  else
-    load_unit(static_cast<const __nv_bfloat16*>(w), m, p.vec, v);
+  } else if (p.p32) {
+    Raw<float, VEC> r;
+    r.template load<false>(static_cast<const float*>(w), m);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] += off;
+    for (int e = 0; e < 8; ++e) v[e] = r.get(e) + off;
+  } else {
+    Raw<__nv_bfloat16, VEC> r;
+    r.template load<false>(static_cast<const __nv_bfloat16*>(w), m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = r.get(e) + off;
+  }
 }
 
 template <typename T>
@@ -242,8 +255,12 @@ struct BlockGrads {
   int acc, parts;                           // set by the launcher
 };
 
-cudaError_t launch_block_fwd(const BlockArgs& a, int dtype, int res_dtype, bool post,
-                             cudaStream_t s);
+// Forward (POST: the post norm), for one pair of activation and residual types.
+template <typename TA, typename TR>
+cudaError_t launch_block_fwd_types(BlockArgs a, bool post, int sms, cudaStream_t s);
+// Backward over the rows; sets o.parts.
+template <typename TA, typename TR>
+cudaError_t launch_block_bwd_types(BlockArgs a, BlockGrads& o, int sms, cudaStream_t s);
 cudaError_t launch_block_bwd(const BlockArgs& a, BlockGrads o, int dtype, int res_dtype, int sms,
                              cudaStream_t s);
 

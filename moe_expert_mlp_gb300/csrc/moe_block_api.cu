@@ -87,15 +87,10 @@ struct Checker {
   }
 };
 
-// How a row is spread over its group: the fewest units a thread (1, 2 or 4)
-// with which 512 threads hold it.
-void spread(BlockArgs& a, const moe_block_norm_desc_t* d, bool vec) {
-  const int units = (d->d + kUnit - 1) / kUnit;
+void fill(BlockArgs& a, const moe_block_norm_desc_t* d, bool vec) {
   a.T = d->T;
   a.d = d->d;
   a.vec = vec;
-  a.nv = units <= kBlockThreads ? 1 : units <= 2 * kBlockThreads ? 2 : 4;
-  a.tpr = ((units + a.nv - 1) / a.nv + 31) / 32 * 32;
   a.p32 = d->param_dtype == MOE_DTYPE_FP32;
   a.gate = d->gate;
   a.gate_act = d->gate_act;
@@ -106,6 +101,14 @@ void spread(BlockArgs& a, const moe_block_norm_desc_t* d, bool vec) {
 size_t bwd_ws_bytes(const moe_block_norm_desc_t* d) {
   const size_t parts = d->T < kBlockBwdMaxParts ? d->T : kBlockBwdMaxParts;
   return parts * 4 * d->d * sizeof(float) + 256;
+}
+
+cudaError_t launch_fwd(const moe_block_norm_desc_t* d, const BlockArgs& a, bool post, int sms,
+                       cudaStream_t s) {
+  if (d->dtype == MOE_DTYPE_FP32) return launch_block_fwd_types<float, float>(a, post, sms, s);
+  if (d->res_dtype == MOE_DTYPE_FP32)
+    return launch_block_fwd_types<__nv_bfloat16, float>(a, post, sms, s);
+  return launch_block_fwd_types<__nv_bfloat16, __nv_bfloat16>(a, post, sms, s);
 }
 
 moe_status_t to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -119,7 +122,7 @@ moe_status_t run_bwd(const moe_block_norm_desc_t* desc, Checker& c, BlockArgs& a
   int sms;
   const moe_status_t st = current_device(&sms, &a.status);
   if (st != MOE_OK) return st;
-  spread(a, desc, c.vec);
+  fill(a, desc, c.vec);
   a.part = static_cast<float*>(ws);
   return to_status(launch_block_bwd(a, o, desc->dtype, desc->res_dtype, sms, stream));
 }
@@ -155,8 +158,8 @@ moe_status_t moe_block_pre_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows_
   if (c.st != MOE_OK) return c.st;
   int sms;
   if ((st = current_device(&sms, &a.status)) != MOE_OK) return st;
-  spread(a, desc, c.vec);
-  return to_status(launch_block_fwd(a, desc->dtype, desc->res_dtype, false, stream));
+  fill(a, desc, c.vec);
+  return to_status(launch_fwd(desc, a, false, sms, stream));
 }
 
 moe_status_t moe_block_post_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows_t res,
@@ -193,8 +196,8 @@ moe_status_t moe_block_post_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows
   if (c.st != MOE_OK) return c.st;
   int sms;
   if ((st = current_device(&sms, &a.status)) != MOE_OK) return st;
-  spread(a, desc, c.vec);
-  return to_status(launch_block_fwd(a, desc->dtype, desc->res_dtype, true, stream));
+  fill(a, desc, c.vec);
+  return to_status(launch_fwd(desc, a, true, sms, stream));
 }
 
 moe_status_t moe_block_pre_norm_bwd(const moe_block_norm_desc_t* desc, moe_rows_t dx,
