@@ -22,6 +22,7 @@ namespace moe {
 constexpr int kBlockThreads = 512;   // threads of a block at most
 constexpr int kUnit = 8;             // channels of a unit
 constexpr int kBlockMaxD = 16384;    // 512 threads x 4 units
+constexpr int kBlockMaxT = 1 << 30;    // a few steps of the grid past it stay in 32 bits
 constexpr int kFewRows = 2;          // rows an SM up to which a row's latency counts
 
 // Row tensor: element (t, c) at p[t * ld + c].
@@ -59,6 +60,41 @@ struct BlockArgs {
   float* part;       // [blocks][accumulators][d]
   BlockRows dgate;   // token, full
 };
+
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float sum(F2 a) {
+  const float2 p = parts(a);
+  return p.x + p.y;
+}
 
 // Channels of unit u of thread `lane` of its group: c0, c0 + step, ..., those
 // below d.  VEC: 8 neighbours, all or none.
@@ -115,6 +151,13 @@ struct Raw {
       for (int e = 0; e < 8; ++e) w[e] = m.has(e) ? __float_as_uint(to_f32(row[m.at(e)])) : 0u;
     }
   }
+  // elements 2i, 2i + 1
+  __device__ __forceinline__ F2 pair(int i) const {
+    if constexpr (VEC && sizeof(T) == 2)
+      return f2(bf16_lo(w[i]), bf16_hi(w[i]));
+    else
+      return f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (VEC && sizeof(T) == 2)
       return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
@@ -152,6 +195,28 @@ __device__ __forceinline__ void store_unit(T* row, const Unit<VEC>& m, const flo
   }
 }
 
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_unit(T* row, const Unit<VEC>& m, const F2 (&v)[4]) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = parts(v[i]);
+    q[2 * i] = a.x, q[2 * i + 1] = a.y;
+  }
+  store_unit(row, m, q);
+}
+
+// v where the row has the elements, 0 past its end (VEC: units are skipped as
+// a whole there).
+template <bool VEC>
+__device__ __forceinline__ F2 within(const Unit<VEC>& m, int i, F2 v) {
+  if constexpr (VEC) return v;
+  const float2 a = parts(v);
+  return f2(m.has(2 * i) ? a.x : 0.0f, m.has(2 * i + 1) ? a.y : 0.0f);
+}
+template <bool VEC>
+__device__ __forceinline__ bool beyond(const Unit<VEC>& m) { return VEC && !m.has(0); }
+
 // The unit's elements of a parameter vector (bf16 or fp32) plus `off`,
 // `absent` where there is none.
 template <bool VEC>
@@ -173,6 +238,15 @@ __device__ __forceinline__ void load_param(const void* w, const BlockArgs& p, co
   }
 }
 
+template <bool VEC>
+__device__ __forceinline__ void load_param(const void* w, const BlockArgs& p, const Unit<VEC>& m,
+                                           float off, float absent, F2 (&v)[4]) {
+  float q[8];
+  load_param(w, p, m, off, absent, q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2(q[2 * i], q[2 * i + 1]);
+}
+
 template <typename T>
 __device__ __forceinline__ T* row_ptr(const BlockRows& r, int t) {
   return reinterpret_cast<T*>(r.p) + static_cast<long long>(t) * r.ld;
@@ -190,59 +264,180 @@ __device__ __forceinline__ float gate_slope(int act, float v) {
   return 1.0f;
 }
 
+// Applies the gate's activation to a unit, leaving the gate's value.
+__device__ __forceinline__ void gate_unit(int act, F2 (&v)[4]) {
+  if (act == MOE_GATE_ACT_NONE) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = parts(v[i]);
+    v[i] = f2(gate_act(act, a.x), gate_act(act, a.y));
+  }
+}
+
 // A thread's place: its group's row, its place in the group, and the group's
 // shared partials (two sets used in turn: a set is written again only behind
-// the other set's barrier, when every thread has read it).
+// the other set's barrier, when every thread has read it).  NAMED: a block
+// holds several groups of more than a warp, each with its own barrier; a
+// kernel with barriers chosen at run time reserves all sixteen, and four such
+// blocks fill an SM, so a kernel that shares its SM goes without.
+template <bool NAMED>
 struct Group {
   int lane;      // thread of the group
   int id;        // group of the block
-  int warps;     // warps of the group
-  float4* red;   // [2][warps]
+  int warps;     // warps of the group, at most 16
+  float* red;    // [2][warps][4]
   int turn;
 };
 
-__device__ __forceinline__ Group make_group(const BlockArgs& p, float4* red) {
-  Group g;
+constexpr int kRedFloats = 2 * kBlockThreads / 32 * 4;
+
+template <bool NAMED>
+__device__ __forceinline__ Group<NAMED> make_group(const BlockArgs& p, float* red) {
+  Group<NAMED> g;
   g.id = threadIdx.x / p.tpr;
   g.lane = threadIdx.x - g.id * p.tpr;
   g.warps = p.tpr / 32;
-  g.red = red + g.id * 2 * g.warps;
+  g.red = red + g.id * 2 * g.warps * 4;
   g.turn = 0;
   return g;
 }
 
-// Sums over the group, the same value in every thread of it.
-template <int N>
-__device__ __forceinline__ void group_sum(Group& g, float (&v)[N]) {
-  static_assert(N >= 1 && N <= 4, "one float4 of partials");
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-  if (g.warps == 1) return;
-  float4* set = g.red + g.turn * g.warps;
-  g.turn ^= 1;
-  if ((g.lane & 31) == 0) {
-    float4 w = make_float4(v[0], 0.0f, 0.0f, 0.0f);
-    if constexpr (N > 1) w.y = v[1];
-    if constexpr (N > 2) w.z = v[2];
-    if constexpr (N > 3) w.w = v[3];
-    set[g.lane >> 5] = w;
-  }
-  asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.warps * 32) : "memory");
+// Sums over the group, the same bits in every thread of it.  With 2 (or 3, 4)
+// values the warp's halves (quarters) take one value each as they fold, so
+// that the shuffles are 5 (6) instead of 10 (20); the lanes of a half (quarter)
+// then add the warps' partials of its value.
+template <int N, bool NAMED>
+__device__ __forceinline__ void group_sum(Group<NAMED>& g, float (&v)[N]) {
+  static_assert(N >= 1 && N <= 4, "four partials a warp");
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  constexpr int kParts = N == 1 ? 1 : N == 2 ? 2 : 4;   // values side by side in a warp
+  constexpr int kWide = 32 / kParts;                    // lanes of a value
   const int l = g.lane & 31;
-  const float4 w = l < g.warps ? set[l] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  v[0] = w.x;
-  if constexpr (N > 1) v[1] = w.y;
-  if constexpr (N > 2) v[2] = w.z;
-  if constexpr (N > 3) v[3] = w.w;
-  // at most 16 warps
+  float a;
+  if constexpr (N == 1) {
+    a = v[0];
+  } else {
+    float x = v[0], y = v[1];
+    if constexpr (N > 2) {
+      const bool up = l & 16;
+      const float z = N > 3 ? v[N - 1] : 0.0f;
+      x = (up ? v[2] : v[0]) + __shfl_xor_sync(kAll, up ? v[0] : v[2], 16);
+      y = (up ? z : v[1]) + __shfl_xor_sync(kAll, up ? v[1] : z, 16);
+    }
+    const bool up = l & kWide;
+    a = (up ? y : x) + __shfl_xor_sync(kAll, up ? x : y, kWide);
+  }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
+  for (int o = kWide / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
+  if (g.warps > 1) {
+    float* set = g.red + g.turn * g.warps * 4;
+    g.turn ^= 1;
+    const int value = l / kWide, at = l % kWide;
+    if (at == 0) set[(g.lane >> 5) * 4 + value] = a;
+    if constexpr (NAMED)
+      asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.warps * 32) : "memory");
+    else
+      __syncthreads();
+    a = at < g.warps ? set[at * 4 + value] : 0.0f;
+    if constexpr (kWide == 8) {
+      if (at + 8 < g.warps) a += set[(at + 8) * 4 + value];
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    for (int o = kWide < 16 ? kWide / 2 : 8; o > 0; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
+  }
+  if constexpr (N == 1) {
+    v[0] = __shfl_sync(kAll, a, 0);   // lanes 16.. hold no warp's partial
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, v[i], 0);
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, a, i * kWide);
+  }
+}
+
+__device__ __forceinline__ void copy16_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One row tensor of a row: a thread's units, in its places of the ring (VEC)
+// or in registers.
+template <typename T, int NV, bool VEC>
+struct RowPart {
+  static constexpr int kPieces = VEC ? NV * static_cast<int>(sizeof(T)) / 2 : 0;
+  Raw<T, VEC> held[VEC ? 1 : NV];
+  uint4* at;   // piece i at at[i * threads]
+
+  __device__ __forceinline__ void copy(const T* row, const Unit<VEC> (&m)[NV], int threads) {
+    if constexpr (VEC) {
+      constexpr int kHalves = sizeof(T) / 2;
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (m[u].has(0)) {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            copy16_async(at + (u * kHalves + h) * threads,
+                         reinterpret_cast<const uint4*>(row + m[u].c0) + h);
+        }
+    }
+  }
+  __device__ __forceinline__ void fetch(const T* row, const Unit<VEC> (&m)[NV]) {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) held[u].template load<true>(row, m[u]);
+    }
+  }
+  // (VEC: of a unit within the row)
+  __device__ __forceinline__ Raw<T, VEC> get(int u, int threads) const {
+    if constexpr (VEC) {
+      constexpr int kHalves = sizeof(T) / 2;
+      Raw<T, VEC> r;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const uint4 q = at[(u * kHalves + h) * threads];
+        r.w[4 * h] = q.x, r.w[4 * h + 1] = q.y, r.w[4 * h + 2] = q.z, r.w[4 * h + 3] = q.w;
+      }
+      return r;
+    } else {
+      return held[u];
+    }
+  }
+};
+
+// Parameters of a thread's units: in registers where they fit, else from L1.
+template <int NV, bool HELD>
+struct Weights {
+  F2 held[HELD ? NV : 1][4];
+  template <typename F>
+  __device__ __forceinline__ void fetch(F&& make) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) make(u, held[u]);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void get(F&& make, int u, F2 (&v)[4]) const {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = held[u][i];
+    } else {
+      make(u, v);
+    }
+  }
+};
+
+constexpr int kRing = 3;                    // rows of a group in the ring, at most
+constexpr size_t kBlockSmem = 220 * 1024;   // shared memory that the ring may take
+
+__device__ __forceinline__ void ring_wait(int ring) {
+  if (ring >= 3) copies_wait<2>();
+  else if (ring == 2) copies_wait<1>();
+  else copies_wait<0>();
 }
 
 // Blocks whose partial sums the backward's workspace has room for.

@@ -13,7 +13,7 @@ size_t type_bytes(int t) { return t == MOE_DTYPE_FP32 ? 4 : 2; }
 
 moe_status_t check_norm_desc(const moe_block_norm_desc_t* d) {
   if (!d) return MOE_ERR_NULL;
-  if (d->T < 0 || d->d < 1 || d->d > kBlockMaxD) return MOE_ERR_SHAPE;
+  if (d->T < 0 || d->T > kBlockMaxT || d->d < 1 || d->d > kBlockMaxD) return MOE_ERR_SHAPE;
   if (!is_float_type(d->dtype) || !is_float_type(d->res_dtype) || !is_float_type(d->param_dtype))
     return MOE_ERR_UNSUPPORTED;
   if (d->dtype == MOE_DTYPE_FP32 && d->res_dtype != MOE_DTYPE_FP32) return MOE_ERR_UNSUPPORTED;

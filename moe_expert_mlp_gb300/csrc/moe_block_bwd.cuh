@@ -32,86 +32,6 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ void copy16_async(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// One row tensor of a row: a thread's units, in its places of the ring (VEC)
-// or in registers.
-template <typename T, int NV, bool VEC>
-struct RowPart {
-  static constexpr int kPieces = VEC ? NV * static_cast<int>(sizeof(T)) / 2 : 0;
-  Raw<T, VEC> held[VEC ? 1 : NV];
-  uint4* at;   // piece i at at[i * threads]
-
-  __device__ __forceinline__ void copy(const T* row, const Unit<VEC> (&m)[NV], int threads) {
-    if constexpr (VEC) {
-      constexpr int kHalves = sizeof(T) / 2;
-#pragma unroll
-      for (int u = 0; u < NV; ++u)
-        if (m[u].has(0)) {
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            copy16_async(at + (u * kHalves + h) * threads,
-                         reinterpret_cast<const uint4*>(row + m[u].c0) + h);
-        }
-    }
-  }
-  __device__ __forceinline__ void fetch(const T* row, const Unit<VEC> (&m)[NV]) {
-    if constexpr (!VEC) {
-#pragma unroll
-      for (int u = 0; u < NV; ++u) held[u].template load<true>(row, m[u]);
-    }
-  }
-  __device__ __forceinline__ Raw<T, VEC> get(const Unit<VEC>& m, int u, int threads) const {
-    if constexpr (VEC) {
-      constexpr int kHalves = sizeof(T) / 2;
-      Raw<T, VEC> r;
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (m.has(0)) q = at[(u * kHalves + h) * threads];
-        r.w[4 * h] = q.x, r.w[4 * h + 1] = q.y, r.w[4 * h + 2] = q.z, r.w[4 * h + 3] = q.w;
-      }
-      return r;
-    } else {
-      return held[u];
-    }
-  }
-};
-
-// Weights of a thread's units: in registers where they fit, else from L1.
-template <int NV, bool VEC, bool HELD>
-struct Weights {
-  float held[HELD ? NV : 1][8];
-  template <typename F>
-  __device__ __forceinline__ void fetch(F&& make) {
-    if constexpr (HELD) {
-#pragma unroll
-      for (int u = 0; u < NV; ++u) make(u, held[u]);
-    }
-  }
-  template <typename F>
-  __device__ __forceinline__ void get(F&& make, int u, float (&v)[8]) const {
-    if constexpr (HELD) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = held[u][e];
-    } else {
-      make(u, v);
-    }
-  }
-};
-
-constexpr int kRing = 3;   // rows of a group in the ring, at most
-
 // Pieces of a ring row: the tensors that the kernel copies.
 template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST>
 __host__ __device__ constexpr int ring_pieces() {
@@ -127,9 +47,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   constexpr int kS1 = PRE ? (BIAS ? 2 : 1) : 0;        // the post norm's first sum
   constexpr bool kHeld = NV == 1 || (NV == 2 && !BIAS);
   constexpr int kPieces = ring_pieces<TA, TR, NV, VEC, PRE, POST>();
-  __shared__ float4 red[2 * kBlockThreads / 32];
+  __shared__ float red[kRedFloats];
   extern __shared__ uint4 dyn[];                 // the ring; then the groups' sums
-  Group g = make_group(p, red);
+  Group<true> g = make_group<true>(p, red);
   const int groups = blockDim.x / p.tpr, threads = blockDim.x;
   const float inv = 1.0f / static_cast<float>(p.d);
   const bool pre_layer = PRE && p.pre.kind == MOE_NORM_LAYER;
@@ -178,37 +98,37 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 
   // the pre norm's weights, and the post norm's times gate and scale where
   // neither changes from token to token
-  auto pre_weight = [&](int u, float (&v)[8]) { load_param(p.pre.w, p, m[u], p.pre.off, 1.0f, v); };
-  auto post_weight = [&](int u, float (&v)[8]) {
+  auto pre_weight = [&](int u, F2 (&v)[4]) { load_param(p.pre.w, p, m[u], p.pre.off, 1.0f, v); };
+  auto post_weight = [&](int u, F2 (&v)[4]) {
     load_param(p.post.w, p, m[u], p.post.off, 1.0f, v);
     if (p.gate == MOE_GATE_CHANNEL) {
-      float q[8];
+      F2 q[4];
       load_param(p.gate_rows.p, p, m[u], 0.0f, 1.0f, q);
+      gate_unit(p.gate_act, q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= p.branch_scale * gate_act(p.gate_act, q[e]);
-    } else if (p.gate == MOE_GATE_NONE) {
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * q[i];
+    }
+    if (!full && !token) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= p.branch_scale;
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * f2(p.branch_scale);
     }
   };
-  Weights<NV, VEC, kHeld> w1, w2;
+  Weights<NV, kHeld> w1, w2;
   if constexpr (PRE) w1.fetch(pre_weight);
   if constexpr (POST) w2.fetch(post_weight);
 
-  float acc[kAcc][NV][8];
+  F2 acc[kAcc][NV][4];
 #pragma unroll
   for (int a = 0; a < kAcc; ++a)
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[a][u][e] = 0.0f;
+      for (int i = 0; i < 4; ++i) acc[a][u][i] = f2(0.0f);
 
   int slot = 0;
   for (; t < p.T; t += step) {
     if constexpr (VEC) {
-      if (ring == 3) copies_wait<2>();
-      else if (ring == 2) copies_wait<1>();
-      else copies_wait<0>();
+      ring_wait(ring);
       place(slot);
     } else {
       if constexpr (PRE) {
@@ -222,173 +142,194 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     if (token) gt = gate_act(p.gate_act, *row_ptr<const float>(p.gate_rows, t));
     float mu1 = 0.0f, mu2 = 0.0f;
     if (pre_layer || post_layer) {
-      float s[2] = {0.0f, 0.0f};
+      F2 a1 = f2(0.0f), a2 = f2(0.0f);
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
         if constexpr (PRE) {
-          const Raw<TR, VEC> a = res.get(m[u], u, threads);
+          const Raw<TR, VEC> a = res.get(u, threads);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] += a.get(e);
+          for (int i = 0; i < 4; ++i) a1 = a1 + a.pair(i);
         }
         if constexpr (POST) {
-          const Raw<TA, VEC> a = y.get(m[u], u, threads);
+          const Raw<TA, VEC> a = y.get(u, threads);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[1] += a.get(e);
+          for (int i = 0; i < 4; ++i) a2 = a2 + a.pair(i);
         }
       }
+      float s[2] = {sum(a1), sum(a2)};
       group_sum(g, s);
       if (pre_layer) mu1 = s[0] * inv;
       if (post_layer) mu2 = s[1] * inv;
     }
 
-    // Sums over the row.  With a pre norm: its squares, dxh, dxh v and the
-    // post norm's squares; without: the post norm's own, as D is known.
-    float D[NV][8];
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto load_D = [&](int u) {
+    // Sums over the row.  With a pre norm: its squares, dxh, dxh (r' - mu) and
+    // the post norm's squares; without: the post norm's own, as D is known.
+    F2 D[NV][4];
+    const F2 zero = f2(0.0f);
+    auto load_D = [&](int u, F2 (&d)[4]) {
       if (p.dres_in.p != nullptr) {
-        const Raw<TR, VEC> a = dres_in.get(m[u], u, threads);
+        const Raw<TR, VEC> a = dres_in.get(u, threads);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) D[u][e] = p.dres_scale * a.get(e);
+        for (int i = 0; i < 4; ++i) d[i] = f2(p.dres_scale) * a.pair(i);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) D[u][e] = 0.0f;
+        for (int i = 0; i < 4; ++i) d[i] = zero;
       }
     };
-    // the post norm's sums of unit u: dxh, dxh (y - mu), D bias; dxh without
-    // the token's gate (and without the scale where there is a token or full
-    // gate), which the caller applies to the sums
-    auto post_sums = [&](int u, float& s1, float& s2, float& s3) {
-      const Raw<TA, VEC> a = y.get(m[u], u, threads);
-      float w[8];
+    // The post norm's sums: dxh, dxh (y - mu), D bias.  The token's gate, and
+    // the scale with a token or full gate, the caller applies to the sums.
+    // D is 0 past the row's end.
+    auto post_sums = [&](int u, F2& s1, F2& s2, F2& s3) {
+      const Raw<TA, VEC> a = y.get(u, threads);
+      F2 w[4];
       w2.get(post_weight, u, w);
       if (full) {
-        float q[8];
-        load_row(row_ptr<const TA>(p.gate_rows, t), m[u], q);
+        Raw<TA, VEC> r;
+        r.template load<true>(row_ptr<const TA>(p.gate_rows, t), m[u]);
+        F2 q[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] *= gate_act(p.gate_act, q[e]);
+        for (int i = 0; i < 4; ++i) q[i] = r.pair(i);
+        gate_unit(p.gate_act, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = w[i] * q[i];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float dxh = D[u][e] * w[e];
-        s1 += dxh;
-        s2 += dxh * (a.get(e) - mu2);            // D is 0 past the row's end
+      for (int i = 0; i < 4; ++i) {
+        const F2 dxh = D[u][i] * w[i];
+        s1 = s1 + dxh;
+        s2 = fma2(dxh, a.pair(i) + f2(-mu2), s2);
       }
       if (token && p.post.b != nullptr) {
-        float b[8];
+        F2 b[4];
         load_param(p.post.b, p, m[u], 0.0f, 0.0f, b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s3 += D[u][e] * b[e];
+        for (int i = 0; i < 4; ++i) s3 = fma2(D[u][i], b[i], s3);
       }
     };
-    auto post_squares = [&](int u, float& q) {
-      const Raw<TA, VEC> a = y.get(m[u], u, threads);
+    auto post_squares = [&](int u, F2& q) {
+      const Raw<TA, VEC> a = y.get(u, threads);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = !post_layer || m[u].has(e) ? a.get(e) - mu2 : 0.0f;
-        q += c * c;
+      for (int i = 0; i < 4; ++i) {
+        const F2 c = within(m[u], i, a.pair(i) + f2(-mu2));
+        q = fma2(c, c, q);
       }
     };
     float rstd2 = 1.0f;
     if constexpr (PRE) {
+      F2 s0 = zero, s1 = zero, s2 = zero, s3 = zero;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
-        const Raw<TR, VEC> a = res.get(m[u], u, threads);
-        const Raw<TA, VEC> b = dx.get(m[u], u, threads);
-        float w[8];
+        if (beyond(m[u])) continue;
+        const Raw<TR, VEC> a = res.get(u, threads);
+        const Raw<TA, VEC> b = dx.get(u, threads);
+        F2 w[4];
         w1.get(pre_weight, u, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float c = !pre_layer || m[u].has(e) ? a.get(e) - mu1 : 0.0f;
-          const float dxh = b.get(e) * w[e];
-          s[0] += c * c;
-          s[1] += dxh;
-          s[2] += dxh * c;
+        for (int i = 0; i < 4; ++i) {
+          const F2 c = within(m[u], i, a.pair(i) + f2(-mu1));
+          const F2 dxh = b.pair(i) * w[i];
+          s0 = fma2(c, c, s0);
+          s1 = s1 + dxh;
+          s2 = fma2(dxh, c, s2);
         }
-        if (normed) post_squares(u, s[3]);
+        if (normed) post_squares(u, s3);
       }
+      float s[4] = {sum(s0), sum(s1), sum(s2), sum(s3)};
       group_sum(g, s);
       const float rstd = 1.0f / sqrtf(s[0] * inv + p.pre.eps);
-      const float m0 = pre_layer ? s[1] * inv : 0.0f, m1 = s[2] * rstd * inv;
       if (normed) rstd2 = 1.0f / sqrtf(s[3] * inv + p.post.eps);
+      // rstd (dxh - m0 - xhat m1) = rstd dxh + k1 r' + k0
+      const float m1 = s[2] * inv * rstd, k1 = -(rstd * m1) * rstd;
+      const float k0 = (pre_layer ? -rstd * (s[1] * inv) : 0.0f) - k1 * mu1;
+      const F2 r2 = f2(rstd), c2 = f2(-mu1 * rstd), kk1 = f2(k1), kk0 = f2(k0);
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
-        load_D(u);
-        const Raw<TR, VEC> a = res.get(m[u], u, threads);
-        const Raw<TA, VEC> b = dx.get(m[u], u, threads);
-        float w[8];
+        if (beyond(m[u])) continue;
+        load_D(u, D[u]);
+        const Raw<TR, VEC> a = res.get(u, threads);
+        const Raw<TA, VEC> b = dx.get(u, threads);
+        F2 w[4];
         w1.get(pre_weight, u, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xh = (a.get(e) - mu1) * rstd;
-          acc[0][u][e] += b.get(e) * xh;         // dx is 0 past the row's end
-          if constexpr (BIAS) acc[1][u][e] += b.get(e);
-          D[u][e] += m[u].has(e) ? rstd * (b.get(e) * w[e] - m0 - xh * m1) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          const F2 v = a.pair(i), d = b.pair(i);
+          acc[0][u][i] = fma2(d, fma2(v, r2, c2), acc[0][u][i]);   // dx is 0 past the end
+          if constexpr (BIAS) acc[1][u][i] = acc[1][u][i] + d;
+          const F2 dv = fma2(d * w[i], r2, fma2(v, kk1, kk0));
+          D[u][i] = within(m[u], i, D[u][i] + dv);
         }
         if (p.dres.p != nullptr) store_unit(row_ptr<TR>(p.dres, t), m[u], D[u]);
       }
     } else {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
-        load_D(u);
+        if (beyond(m[u])) continue;
+        load_D(u, D[u]);
         if (p.dres.p != nullptr) store_unit(row_ptr<TR>(p.dres, t), m[u], D[u]);
       }
     }
 
     if constexpr (POST) {
-      float e1, e2, e3;
-      if constexpr (PRE) {
-        float q[3] = {0.0f, 0.0f, 0.0f};
-        if (normed || token) {
+      F2 s1 = zero, s2 = zero, s3 = zero;
+      float e1 = 0.0f, e2 = 0.0f, e3 = 0.0f;
+      if (normed || token) {
+        F2 s0 = zero;
 #pragma unroll
-          for (int u = 0; u < NV; ++u) post_sums(u, q[0], q[1], q[2]);
-          group_sum(g, q);
+        for (int u = 0; u < NV; ++u) {
+          if (beyond(m[u])) continue;
+          post_sums(u, s1, s2, s3);
+          if (!PRE && normed) post_squares(u, s0);
         }
-        e1 = q[0], e2 = q[1], e3 = q[2];
-      } else {
-        if (normed || token) {
-#pragma unroll
-          for (int u = 0; u < NV; ++u) {
-            post_sums(u, s[1], s[2], s[3]);
-            if (normed) post_squares(u, s[0]);
-          }
+        if constexpr (PRE) {
+          float s[3] = {sum(s1), sum(s2), sum(s3)};
           group_sum(g, s);
+          e1 = s[0], e2 = s[1], e3 = s[2];
+        } else {
+          float s[4] = {sum(s1), sum(s2), sum(s3), sum(s0)};
+          group_sum(g, s);
+          e1 = s[0], e2 = s[1], e3 = s[2];
+          if (normed) rstd2 = 1.0f / sqrtf(s[3] * inv + p.post.eps);
         }
-        if (normed) rstd2 = 1.0f / sqrtf(s[0] * inv + p.post.eps);
-        e1 = s[1], e2 = s[2], e3 = s[3];
       }
       if (token && p.dgate.p != nullptr && g.lane == 0)
         *row_ptr<float>(p.dgate, t) =
             p.branch_scale * (rstd2 * e2 + e3) * gate_slope(p.gate_act, gt);
+      // dy = rstd (scale D w - m0 - xhat m1) = k2 D w + k1 y + k0
       const float scale = token ? p.branch_scale * gt : full ? p.branch_scale : 1.0f;
-      const float m0 = post_layer ? scale * e1 * inv : 0.0f;
-      const float m1 = normed ? scale * e2 * rstd2 * inv : 0.0f;
-      const float out = normed ? rstd2 : 1.0f;
+      const float k2 = normed ? rstd2 * scale : scale;
+      const float m1 = scale * e2 * inv * rstd2, k1 = normed ? -(rstd2 * m1) * rstd2 : 0.0f;
+      const float k0 = (post_layer ? -rstd2 * (scale * e1 * inv) : 0.0f) - k1 * mu2;
+      const F2 r2 = f2(rstd2 * gt), c2 = f2(-mu2 * rstd2 * gt);   // xhat, with the token's gate
+      const F2 kk2 = f2(k2), kk1 = f2(k1), kk0 = f2(k0);
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
-        const Raw<TA, VEC> a = y.get(m[u], u, threads);
-        float w[8], dy[8];
+        if (beyond(m[u])) continue;
+        const Raw<TA, VEC> a = y.get(u, threads);
+        F2 w[4], dy[4];
         w2.get(post_weight, u, w);
         if (full) {
-          float q[8], dg[8], b[8];
-          load_row(row_ptr<const TA>(p.gate_rows, t), m[u], q);
+          Raw<TA, VEC> r;
+          r.template load<true>(row_ptr<const TA>(p.gate_rows, t), m[u]);
+          F2 b[4], dg[4];
           load_param(p.post.b, p, m[u], 0.0f, 0.0f, b);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float gv = gate_act(p.gate_act, q[e]);
-            const float n = (a.get(e) - mu2) * rstd2 * w[e] + b[e];
-            dg[e] = p.branch_scale * D[u][e] * n * gate_slope(p.gate_act, gv);
-            D[u][e] *= gv;                       // the gate joins the sums
+          for (int i = 0; i < 4; ++i) {
+            const F2 n = fma2(fma2(a.pair(i), r2, c2), w[i], b[i]);
+            const float2 q = parts(r.pair(i));
+            const float g0 = gate_act(p.gate_act, q.x), g1 = gate_act(p.gate_act, q.y);
+            dg[i] = f2(p.branch_scale) * D[u][i] * n *
+                    f2(gate_slope(p.gate_act, g0), gate_slope(p.gate_act, g1));
+            D[u][i] = D[u][i] * f2(g0, g1);      // the gate joins the sums
           }
           if (p.dgate.p != nullptr) store_unit(row_ptr<TA>(p.dgate, t), m[u], dg);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xh = (a.get(e) - mu2) * rstd2;
-          const float q = token ? D[u][e] * gt : D[u][e];
-          acc[kS1][u][e] += q * xh;              // D is 0 past the row's end
-          if constexpr (BIAS) acc[kS1 + 1][u][e] += q;
-          dy[e] = out * (scale * D[u][e] * w[e] - m0 - xh * m1);
+        for (int i = 0; i < 4; ++i) {
+          const F2 v = a.pair(i);                // D is 0 past the row's end
+          acc[kS1][u][i] = fma2(D[u][i], fma2(v, r2, c2), acc[kS1][u][i]);
+          if constexpr (BIAS) acc[kS1 + 1][u][i] = fma2(D[u][i], f2(gt), acc[kS1 + 1][u][i]);
+          dy[i] = fma2(D[u][i] * w[i], kk2, fma2(v, kk1, kk0));
         }
         store_unit(row_ptr<TA>(p.dy, t), m[u], dy);
       }
@@ -415,12 +356,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           if (m[u].has(e)) {
             const int c = m[u].at(e);
             const float before = i > 0 ? join[a * p.d + c] : 0.0f;
-            to[a * p.d + c] = before + acc[a][u][e];
+            const float2 mine = parts(acc[a][u][e / 2]);
+            to[a * p.d + c] = before + (e & 1 ? mine.y : mine.x);
           }
   }
 }
-
-constexpr size_t kBlockSmem = 220 * 1024;   // shared memory the ring may take
 
 template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST, bool BIAS>
 cudaError_t launch_kernel(const BlockArgs& a, int blocks, int groups, cudaStream_t s) {

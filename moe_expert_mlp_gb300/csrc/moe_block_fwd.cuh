@@ -4,15 +4,18 @@
 // expert rows.  Instantiated type by type in moe_block_fwd_*.cu.
 //
 // Bound by HBM: a few operations a channel against 4 to 16 bytes.  A row is
-// read once into registers, its sums are taken there, and what follows from
-// them is stored.  Groups are small (about 128 threads with up to 8 units
-// each) and blocks hold one row of a group at a time, so that several
-// independent blocks share an SM: while one waits at its sums others have
-// their loads in flight.  Parameters stay in L1, which the rows bypass.
+// read once, its sums are taken from registers, and what follows from them is
+// stored.
 //
-// With few rows (HOIST) nothing hides the latency of one row, so the group is
-// as large as the row allows and the parameters are fetched together with the
-// row instead of after its sums.
+// Many aligned rows: one block of up to 512 threads an SM (k_block_fwd_ring),
+// whose groups walk down the rows with their parameters in registers, while
+// each thread copies its own 16-byte pieces of the rows to come into its own
+// places of a ring in shared memory (cp.async) and waits for no one else's.
+//
+// Few rows, and rows that are not aligned: one group a row (k_block_fwd).  With
+// few rows nothing hides a row's latency, so the group is as large as the row
+// allows and the parameters are fetched together with the row instead of after
+// its sums.
 #pragma once
 
 #include "moe_block.cuh"
@@ -23,7 +26,7 @@ namespace {
 // Statistics of the row held in v: mean (layer norm) and 1/sqrt(. + eps).
 // The layer norm's variance sums squares about the mean, from registers.
 template <int NV, bool VEC>
-__device__ __forceinline__ void row_stats(const BlockArgs& p, const BlockNorm& n, Group& g,
+__device__ __forceinline__ void row_stats(const BlockArgs& p, const BlockNorm& n, Group<false>& g,
                                           const Unit<VEC> (&m)[NV], const float (&v)[NV][8],
                                           float& mu, float& rstd) {
   const float inv = 1.0f / static_cast<float>(p.d);
@@ -79,7 +82,7 @@ struct Params {
 
 // v = xhat * (off + w) + b
 template <int NV, bool VEC, bool HOIST>
-__device__ __forceinline__ void normalize(const BlockArgs& p, const BlockNorm& n, Group& g,
+__device__ __forceinline__ void normalize(const BlockArgs& p, const BlockNorm& n, Group<false>& g,
                                           const Unit<VEC> (&m)[NV],
                                           const Params<NV, VEC, HOIST>& pw,
                                           const Params<NV, VEC, HOIST>& pb, float (&v)[NV][8]) {
@@ -102,7 +105,7 @@ __device__ __forceinline__ void normalize(const BlockArgs& p, const BlockNorm& n
 
 // y[t] from the expert rows, fp32 in slot order; four rows' loads in flight.
 template <typename TA, int NV, bool VEC>
-__device__ __forceinline__ void combine_rows(const BlockArgs& p, int t, const Group& g,
+__device__ __forceinline__ void combine_rows(const BlockArgs& p, int t, const Group<false>& g,
                                              const Unit<VEC> (&m)[NV], float (&v)[NV][8]) {
 #pragma unroll
   for (int u = 0; u < NV; ++u)
@@ -146,8 +149,8 @@ enum FwdMode { kPre, kPost, kRouted };
 template <typename TA, typename TR, int NV, bool VEC, int MODE, bool HOIST>
 __global__ void __launch_bounds__(HOIST ? kBlockThreads : kBlockThreads / 2)
     k_block_fwd(const __grid_constant__ BlockArgs p) {
-  __shared__ float4 red[2 * kBlockThreads / 32];
-  Group g = make_group(p, red);
+  __shared__ float red[kRedFloats];
+  Group<false> g = make_group<false>(p, red);
   const int t = blockIdx.x * (blockDim.x / p.tpr) + g.id;
   if (t >= p.T) return;
   Unit<VEC> m[NV];
@@ -214,9 +217,296 @@ __global__ void __launch_bounds__(HOIST ? kBlockThreads : kBlockThreads / 2)
   for (int u = 0; u < NV; ++u) store_unit(row_ptr<TA>(p.x, t), m[u], v[u]);
 }
 
+// The routed branch's rows of a token, prefetched by lane: lane s of a warp
+// holds slot s's row (-1: not a row) and weight.
+struct Slots {
+  int row;
+  float w;
+  __device__ __forceinline__ void load(const BlockArgs& p, int t, int lane) {
+    const int s = lane & 31;
+    row = -1;
+    w = 0.0f;
+    if (t < p.T && s < p.k) {
+      const long long at = static_cast<long long>(t) * p.k + s;
+      row = __ldg(p.row_of + at);
+      w = __ldg(p.topk_w + at);
+      if (row < 0 || row >= p.capacity) {
+        if (lane < 32) atomicOr(p.status, MOE_DEV_BAD_OFFSETS);
+        row = -1;
+      }
+    }
+  }
+};
+
+template <typename TA, typename TR, int NV, int MODE, bool BIAS>
+__global__ void __launch_bounds__(kBlockThreads, 1)
+    k_block_fwd_ring(const __grid_constant__ BlockArgs p, int ring) {
+  constexpr bool kHeld = NV <= 2;
+  using Res = RowPart<TR, NV, true>;
+  using Act = RowPart<TA, NV, true>;
+  __shared__ float red[kRedFloats];
+  extern __shared__ uint4 dyn[];
+  Group<true> g = make_group<true>(p, red);
+  const int groups = blockDim.x / p.tpr, threads = blockDim.x;
+  const float inv = 1.0f / static_cast<float>(p.d);
+  const bool full = p.gate == MOE_GATE_FULL, token = p.gate == MOE_GATE_TOKEN;
+  const int slots = MODE == kRouted ? p.k : MODE == kPost ? 1 : 0;
+  const int pieces = Res::kPieces + slots * Act::kPieces;
+  Unit<true> m[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) m[u] = Unit<true>(p, g.lane, u);
+
+  const int step = gridDim.x * groups;
+  int t = blockIdx.x * groups + g.id;
+  Res res;
+  Act y;
+  auto place = [&](int slot) {
+    res.at = dyn + static_cast<size_t>(slot) * pieces * threads + threadIdx.x;
+    y.at = res.at + Res::kPieces * threads;
+  };
+  // copies row t (its expert rows given by s) into a slot of the ring
+  auto copy = [&](int row, int slot, const Slots& s) {
+    if (row < p.T) {
+      place(slot);
+      if constexpr (MODE == kPost) y.copy(row_ptr<const TA>(p.y, row), m, threads);
+      if constexpr (MODE == kRouted) {
+        for (int i = 0; i < slots; ++i) {
+          const int r = __shfl_sync(0xFFFFFFFFu, s.row, i);
+          if (r >= 0) y.copy(row_ptr<const TA>(p.y, r), m, threads);
+          y.at += Act::kPieces * threads;
+        }
+      }
+      res.copy(row_ptr<const TR>(p.res, row), m, threads);
+    }
+    copies_commit();   // one group a row, empty past the end
+  };
+  // routed: now, the rows in the ring behind it, and the one to copy next
+  Slots s0, s1, s2, next;
+  if constexpr (MODE == kRouted) {
+    s0.load(p, t, g.lane);
+    s1.load(p, t + step, g.lane);
+    s2.load(p, t + 2 * step, g.lane);
+    next.load(p, t + ring * step, g.lane);
+  }
+  copy(t, 0, s0);
+  if (ring > 1) copy(t + step, 1, s1);
+  if (ring > 2) copy(t + 2 * step, 2, s2);
+
+  // the parameters; the post norm's times gate and scale where neither changes
+  // from token to token
+  auto scaled = [&](int u, F2 (&v)[4]) {
+    if (p.gate == MOE_GATE_CHANNEL) {
+      F2 q[4];
+      load_param(p.gate_rows.p, p, m[u], 0.0f, 1.0f, q);
+      gate_unit(p.gate_act, q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * q[i];
+    }
+    if (!full && !token) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = v[i] * f2(p.branch_scale);
+    }
+  };
+  auto post_weight = [&](int u, F2 (&v)[4]) {
+    load_param(p.post.w, p, m[u], p.post.off, 1.0f, v);
+    scaled(u, v);
+  };
+  auto post_bias = [&](int u, F2 (&v)[4]) {
+    load_param(p.post.b, p, m[u], 0.0f, 0.0f, v);
+    scaled(u, v);
+  };
+  auto pre_weight = [&](int u, F2 (&v)[4]) { load_param(p.pre.w, p, m[u], p.pre.off, 1.0f, v); };
+  auto pre_bias = [&](int u, F2 (&v)[4]) { load_param(p.pre.b, p, m[u], 0.0f, 0.0f, v); };
+  Weights<NV, kHeld> w1, w2;
+  Weights<NV, kHeld && BIAS> b1, b2;
+  if constexpr (MODE != kPre) {
+    w2.fetch(post_weight);
+    if constexpr (BIAS) b2.fetch(post_bias);
+  }
+  if (p.x.p != nullptr) {
+    w1.fetch(pre_weight);
+    if constexpr (BIAS) b1.fetch(pre_bias);
+  }
+
+  const F2 zero = f2(0.0f);
+  F2 v[NV][4];
+  // mean and 1/sqrt(. + eps) of the row in v
+  auto stats = [&](const BlockNorm& n, float& mu, float& rstd) {
+    mu = 0.0f;
+    if (n.kind == MOE_NORM_LAYER) {
+      F2 a = zero;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = a + v[u][i];
+      }
+      float s[1] = {sum(a)};
+      group_sum(g, s);
+      mu = s[0] * inv;
+    }
+    F2 a = zero;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (beyond(m[u])) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 c = v[u][i] + f2(-mu);
+        a = fma2(c, c, a);
+      }
+    }
+    float s[1] = {sum(a)};
+    group_sum(g, s);
+    rstd = 1.0f / sqrtf(s[0] * inv + n.eps);
+  };
+
+  int slot = 0;
+  for (; t < p.T; t += step) {
+    float gt = 1.0f;
+    if (token) gt = gate_act(p.gate_act, *row_ptr<const float>(p.gate_rows, t));
+    ring_wait(ring);
+    place(slot);
+    Slots after = next;
+    if constexpr (MODE == kPre) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        const Raw<TR, true> a = res.get(u, threads);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = a.pair(i);
+      }
+      copy(t + ring * step, slot, next);   // the row is in registers
+    } else {
+      if constexpr (MODE == kPost) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          if (beyond(m[u])) continue;
+          const Raw<TA, true> a = y.get(u, threads);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = a.pair(i);
+        }
+      } else {
+        after.load(p, t + (ring + 1) * step, g.lane);
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = zero;
+        for (int s = 0; s < slots; ++s) {
+          const float w = __shfl_sync(0xFFFFFFFFu, s0.w, s);
+          const int r = __shfl_sync(0xFFFFFFFFu, s0.row, s);
+          if (r >= 0) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+              if (beyond(m[u])) continue;
+              const Raw<TA, true> a = y.get(u, threads);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[u][i] = fma2(f2(w), a.pair(i), v[u][i]);
+            }
+          }
+          y.at += Act::kPieces * threads;
+        }
+        if (p.y_out.p != nullptr) {
+#pragma unroll
+          for (int u = 0; u < NV; ++u) store_unit(row_ptr<TA>(p.y_out, t), m[u], v[u]);
+        }
+      }
+      float mu = 0.0f, rstd = 1.0f;
+      if (p.post.kind != MOE_NORM_NONE) stats(p.post, mu, rstd);
+      const float k = full || token ? p.branch_scale * gt : 1.0f;
+      const F2 k1 = f2(rstd * k), k0 = f2(-mu * rstd * k), a1 = f2(p.res_scale);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        const Raw<TR, true> r = res.get(u, threads);
+        F2 w[4];
+        w2.get(post_weight, u, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = fma2(v[u][i], k1, k0) * w[i];
+        if constexpr (BIAS) {
+          F2 b[4];
+          b2.get(post_bias, u, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = fma2(b[i], f2(k), v[u][i]);
+        }
+        if (full) {
+          Raw<TA, true> q;
+          q.template load<true>(row_ptr<const TA>(p.gate_rows, t), m[u]);
+          F2 gv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) gv[i] = q.pair(i);
+          gate_unit(p.gate_act, gv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = v[u][i] * gv[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = fma2(a1, r.pair(i), v[u][i]);
+        store_unit(row_ptr<TR>(p.res_out, t), m[u], v[u]);
+      }
+      copy(t + ring * step, slot, next);
+    }
+    if (p.x.p != nullptr) {
+      float mu, rstd;
+      stats(p.pre, mu, rstd);
+      const F2 k1 = f2(rstd), k0 = f2(-mu * rstd);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        F2 w[4], x[4];
+        w1.get(pre_weight, u, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fma2(v[u][i], k1, k0) * w[i];
+        if constexpr (BIAS) {
+          F2 b[4];
+          b1.get(pre_bias, u, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = x[i] + b[i];
+        }
+        store_unit(row_ptr<TA>(p.x, t), m[u], x);
+      }
+    }
+    slot = slot + 1 == ring ? 0 : slot + 1;
+    if constexpr (MODE == kRouted) {
+      s0 = ring > 1 ? s1 : next;
+      s1 = ring > 2 ? s2 : next;
+      s2 = next;
+      next = after;
+    }
+  }
+}
+
+// Launches the ring's kernel; `none` set where not one row fits the ring.
+template <typename TA, typename TR, int NV, int MODE>
+cudaError_t launch_ring(const BlockArgs& a, int sms, bool& none, cudaStream_t s) {
+  const int groups = kBlockThreads / a.tpr, threads = groups * a.tpr;
+  const int slots = MODE == kRouted ? a.k : MODE == kPost ? 1 : 0;
+  const size_t row = static_cast<size_t>(RowPart<TR, NV, true>::kPieces +
+                                         slots * RowPart<TA, NV, true>::kPieces) * threads * 16;
+  int ring = static_cast<int>(kBlockSmem / row);
+  none = ring == 0;
+  if (none) return cudaSuccess;
+  if (ring > kRing) ring = kRing;
+  const bool bias = a.post.b != nullptr || a.pre.b != nullptr;
+  auto* k = bias ? k_block_fwd_ring<TA, TR, NV, MODE, true> : k_block_fwd_ring<TA, TR, NV, MODE, false>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kBlockSmem));
+  if (e != cudaSuccess) return e;
+  int blocks = (a.T + groups - 1) / groups;
+  if (blocks > sms) blocks = sms;
+  k<<<blocks, threads, ring * row, s>>>(a, ring);
+  return cudaGetLastError();
+}
+
+template <typename TA, typename TR, int NV>
+cudaError_t launch_ring_mode(const BlockArgs& a, bool post, int sms, bool& none, cudaStream_t s) {
+  if (!post) return launch_ring<TA, TR, NV, kPre>(a, sms, none, s);
+  if (a.row_of == nullptr) return launch_ring<TA, TR, NV, kPost>(a, sms, none, s);
+  return launch_ring<TA, TR, NV, kRouted>(a, sms, none, s);
+}
+
 template <typename TA, typename TR, int NV, bool VEC, bool HOIST>
 cudaError_t launch_nv(const BlockArgs& a, bool post, cudaStream_t s) {
-  const int groups = max(1, 128 / a.tpr);
+  // several rows a block where a warp holds one, else one
+  const int groups = a.tpr == 32 ? 4 : 1;
   const int threads = groups * a.tpr, blocks = (a.T + groups - 1) / groups;
   if (!post)
     k_block_fwd<TA, TR, NV, VEC, kPre, HOIST><<<blocks, threads, 0, s>>>(a);
@@ -233,36 +523,25 @@ template <typename TA, typename TR>
 cudaError_t launch_block_fwd_types(BlockArgs a, bool post, int sms, cudaStream_t s) {
   const int units = (a.d + kUnit - 1) / kUnit;
   auto threads = [&](int nv) { return ((units + nv - 1) / nv + 31) / 32 * 32; };
-  if (!a.vec) {
-    const bool wide = units > 2 * kBlockThreads / 2;
-    a.tpr = threads(wide ? 8 : 2);
-    return wide ? launch_nv<TA, TR, 8, false, false>(a, post, s)
-                : launch_nv<TA, TR, 2, false, false>(a, post, s);
+  if (a.vec && a.T > kFewRows * sms) {
+    bool none = false;
+    const int nv = units <= 32 ? 1 : units <= 2 * kBlockThreads ? 2 : 4;
+    a.tpr = threads(nv);
+    const cudaError_t e = nv == 1   ? launch_ring_mode<TA, TR, 1>(a, post, sms, none, s)
+                          : nv == 2 ? launch_ring_mode<TA, TR, 2>(a, post, sms, none, s)
+                                    : launch_ring_mode<TA, TR, 4>(a, post, sms, none, s);
+    if (!none) return e;
   }
-  if (a.T <= kFewRows * sms && units <= 2 * kBlockThreads) {
+  if (a.vec && units <= 2 * kBlockThreads) {
     const bool one = units <= kBlockThreads;
     a.tpr = threads(one ? 1 : 2);
     return one ? launch_nv<TA, TR, 1, true, true>(a, post, s)
                : launch_nv<TA, TR, 2, true, true>(a, post, s);
   }
-  // units a thread: the count (of 1, 2, 3, 4, 7, 8) that leaves the fewest of
-  // the group's places empty with at most 160 threads
-  int nv = 8;
-  float best = 0.0f;
-  for (int n : {1, 2, 3, 4, 7, 8}) {
-    const int tpr = threads(n);
-    const float used = static_cast<float>(units) / (n * tpr);
-    if (tpr <= 160 && used > best + 0.02f) best = used, nv = n;
-  }
-  a.tpr = threads(nv);
-  switch (nv) {
-    case 1: return launch_nv<TA, TR, 1, true, false>(a, post, s);
-    case 2: return launch_nv<TA, TR, 2, true, false>(a, post, s);
-    case 3: return launch_nv<TA, TR, 3, true, false>(a, post, s);
-    case 4: return launch_nv<TA, TR, 4, true, false>(a, post, s);
-    case 7: return launch_nv<TA, TR, 7, true, false>(a, post, s);
-    default: return launch_nv<TA, TR, 8, true, false>(a, post, s);
-  }
+  const bool wide = units > 2 * kBlockThreads / 2;
+  a.tpr = threads(wide ? 8 : 2);
+  return wide ? launch_nv<TA, TR, 8, false, false>(a, post, s)
+              : launch_nv<TA, TR, 2, false, false>(a, post, s);
 }
 
 }  // namespace moe

@@ -32,7 +32,7 @@ def pre_fwd(m, desc, **over):
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(T=-1), SHAPE), (dict(d=0), SHAPE), (dict(d=16385), SHAPE),
+    (dict(T=-1), SHAPE), (dict(T=(1 << 30) + 1), SHAPE), (dict(d=0), SHAPE), (dict(d=16385), SHAPE),
     (dict(dtype=2), UNSUPPORTED), (dict(res_dtype=3), UNSUPPORTED),
     (dict(param_dtype=0), UNSUPPORTED), (dict(dtype=4, res_dtype=1), UNSUPPORTED),
     (dict(pre_norm=3), UNSUPPORTED), (dict(post_norm=-1), UNSUPPORTED), (dict(gate=4), UNSUPPORTED),
