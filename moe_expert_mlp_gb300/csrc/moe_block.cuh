@@ -371,9 +371,9 @@ template <typename T, int NV, bool VEC>
 struct RowPart {
   static constexpr int kPieces = VEC ? NV * static_cast<int>(sizeof(T)) / 2 : 0;
   Raw<T, VEC> held[VEC ? 1 : NV];
-  uint4* at;   // piece i at at[i * threads]
+  uint4* at;   // piece i at at[i * kBlockThreads]
 
-  __device__ __forceinline__ void copy(const T* row, const Unit<VEC> (&m)[NV], int threads) {
+  __device__ __forceinline__ void copy(const T* row, const Unit<VEC> (&m)[NV]) {
     if constexpr (VEC) {
       constexpr int kHalves = sizeof(T) / 2;
 #pragma unroll
@@ -381,7 +381,7 @@ struct RowPart {
         if (m[u].has(0)) {
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
-            copy16_async(at + (u * kHalves + h) * threads,
+            copy16_async(at + (u * kHalves + h) * kBlockThreads,
                          reinterpret_cast<const uint4*>(row + m[u].c0) + h);
         }
     }
@@ -393,13 +393,13 @@ struct RowPart {
     }
   }
   // (VEC: of a unit within the row)
-  __device__ __forceinline__ Raw<T, VEC> get(int u, int threads) const {
+  __device__ __forceinline__ Raw<T, VEC> get(int u) const {
     if constexpr (VEC) {
       constexpr int kHalves = sizeof(T) / 2;
       Raw<T, VEC> r;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        const uint4 q = at[(u * kHalves + h) * threads];
+        const uint4 q = at[(u * kHalves + h) * kBlockThreads];
         r.w[4 * h] = q.x, r.w[4 * h + 1] = q.y, r.w[4 * h + 2] = q.z, r.w[4 * h + 3] = q.w;
       }
       return r;
@@ -434,6 +434,9 @@ struct Weights {
 constexpr int kRing = 3;                    // rows of a group in the ring, at most
 constexpr size_t kBlockSmem = 220 * 1024;   // shared memory that the ring may take
 
+// Which of a ring kernel's two forms serves a call: PLAIN for RMS norms
+// without biases and no gate tensor, where the means and what depends on them
+// drop out of the arithmetic at compile time.
 __device__ __forceinline__ void ring_wait(int ring) {
   if (ring >= 3) copies_wait<2>();
   else if (ring == 2) copies_wait<1>();
@@ -441,7 +444,12 @@ __device__ __forceinline__ void ring_wait(int ring) {
 }
 
 // Blocks whose partial sums the backward's workspace has room for.
-constexpr int kBlockBwdMaxParts = 304;
+constexpr int kBlockBwdMaxParts = 160;
+
+// What a token's gate gives, read a row ahead of its use.
+__device__ __forceinline__ float token_gate(const BlockArgs& p, int t) {
+  return p.gate == MOE_GATE_TOKEN && t < p.T ? *row_ptr<const float>(p.gate_rows, t) : 1.0f;
+}
 
 struct BlockGrads {
   bool pre, post, bias;                     // sides present; bias sums kept

@@ -7,17 +7,26 @@ namespace moe {
 namespace {
 
 // Adds the blocks' partials channel by channel, and turns the sums into the
-// parameters' gradients.  32 channels a block, 8 rows of partials at a time.
-__global__ void __launch_bounds__(256) k_block_bwd_finish(const __grid_constant__ BlockArgs p,
-                                                          const __grid_constant__ BlockGrads o) {
-  __shared__ float sums[4][8][32];
+// parameters' gradients.  32 channels a block; its 32 warps share the partials
+// of each sum, and every thread has all of its own in flight at once.  Started
+// while the rows' kernel still runs (programmatic launch) it waits for its end.
+__global__ void __launch_bounds__(1024) k_block_bwd_finish(const __grid_constant__ BlockArgs p,
+                                                           const __grid_constant__ BlockGrads o) {
+  __shared__ float sums[4][32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kEach = (kBlockBwdMaxParts + 31) / 32;
   for (int a = 0; a < o.acc; ++a) {
-    float s = 0.0f;
-    if (c < p.d)
-      for (int i = warp; i < o.parts; i += 8)
-        s += p.part[(static_cast<long long>(i) * o.acc + a) * p.d + c];
+    float v[kEach], s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int i = warp + 32 * j;
+      v[j] = c < p.d && i < o.parts
+                 ? p.part[(static_cast<long long>(i) * o.acc + a) * p.d + c] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) s += v[j];
     sums[a][warp][lane] = s;
   }
   __syncthreads();
@@ -25,7 +34,7 @@ __global__ void __launch_bounds__(256) k_block_bwd_finish(const __grid_constant_
   float S[4];
   for (int a = 0; a < o.acc; ++a) {
     S[a] = 0.0f;
-    for (int i = 0; i < 8; ++i) S[a] += sums[a][i][lane];
+    for (int i = 0; i < 32; ++i) S[a] += sums[a][i][lane];
   }
   auto param = [&](const void* w, float absent) {
     if (w == nullptr) return absent;
@@ -74,8 +83,16 @@ cudaError_t launch_block_bwd(const BlockArgs& a, BlockGrads o, int dtype, int re
     e = launch_block_bwd_types<__nv_bfloat16, __nv_bfloat16>(a, o, sms, s);
   const bool any = o.dpre_w || o.dpre_b || o.dpost_w || o.dpost_b || o.dgate;
   if (e == cudaSuccess && any) {
-    k_block_bwd_finish<<<(a.d + 31) / 32, 256, 0, s>>>(a, o);
-    e = cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.d + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_block_bwd_finish, a, o);
   }
   return e;
 }

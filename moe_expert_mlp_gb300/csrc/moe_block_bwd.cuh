@@ -39,7 +39,7 @@ __host__ __device__ constexpr int ring_pieces() {
          RowPart<TA, NV, VEC>::kPieces * ((PRE ? 1 : 0) + (POST ? 1 : 0));
 }
 
-template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST, bool BIAS>
+template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST, bool BIAS, bool PLAIN>
 __global__ void __launch_bounds__(kBlockThreads, 1)
     k_block_bwd(const __grid_constant__ BlockArgs p, int ring) {
   constexpr int kSides = (PRE ? 1 : 0) + (POST ? 1 : 0);
@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   __shared__ float red[kRedFloats];
   extern __shared__ uint4 dyn[];                 // the ring; then the groups' sums
   Group<true> g = make_group<true>(p, red);
-  const int groups = blockDim.x / p.tpr, threads = blockDim.x;
+  const int groups = blockDim.x / p.tpr;
   const float inv = 1.0f / static_cast<float>(p.d);
-  const bool pre_layer = PRE && p.pre.kind == MOE_NORM_LAYER;
-  const bool normed = POST && p.post.kind != MOE_NORM_NONE;
-  const bool post_layer = POST && p.post.kind == MOE_NORM_LAYER;
-  const bool full = p.gate == MOE_GATE_FULL, token = p.gate == MOE_GATE_TOKEN;
+  const bool pre_layer = !PLAIN && PRE && p.pre.kind == MOE_NORM_LAYER;
+  const bool normed = POST && (PLAIN || p.post.kind != MOE_NORM_NONE);
+  const bool post_layer = !PLAIN && POST && p.post.kind == MOE_NORM_LAYER;
+  const bool full = !PLAIN && p.gate == MOE_GATE_FULL, token = p.gate == MOE_GATE_TOKEN;
   Unit<VEC> m[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) m[u] = Unit<VEC>(p, g.lane, u);
@@ -65,14 +65,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   RowPart<TA, NV, VEC> dx, y;
   auto place = [&](int slot) {
     if constexpr (VEC) {
-      uint4* at = dyn + static_cast<size_t>(slot) * kPieces * threads + threadIdx.x;
+      uint4* at = dyn + slot * kPieces * kBlockThreads + threadIdx.x;
       dres_in.at = at;
-      at += RowPart<TR, NV, VEC>::kPieces * threads;
+      at += RowPart<TR, NV, VEC>::kPieces * kBlockThreads;
       if constexpr (PRE) {
         res.at = at;
-        at += RowPart<TR, NV, VEC>::kPieces * threads;
+        at += RowPart<TR, NV, VEC>::kPieces * kBlockThreads;
         dx.at = at;
-        at += RowPart<TA, NV, VEC>::kPieces * threads;
+        at += RowPart<TA, NV, VEC>::kPieces * kBlockThreads;
       }
       y.at = at;
     }
@@ -82,11 +82,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       if (t < p.T) {
         place(slot);
         if constexpr (PRE) {
-          res.copy(row_ptr<const TR>(p.res, t), m, threads);
-          dx.copy(row_ptr<const TA>(p.dx, t), m, threads);
+          res.copy(row_ptr<const TR>(p.res, t), m);
+          dx.copy(row_ptr<const TA>(p.dx, t), m);
         }
-        if constexpr (POST) y.copy(row_ptr<const TA>(p.y, t), m, threads);
-        if (p.dres_in.p != nullptr) dres_in.copy(row_ptr<const TR>(p.dres_in, t), m, threads);
+        if constexpr (POST) y.copy(row_ptr<const TA>(p.y, t), m);
+        if (p.dres_in.p != nullptr) dres_in.copy(row_ptr<const TR>(p.dres_in, t), m);
       }
       copies_commit();   // one group a row, empty past the end
     }
@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[a][u][i] = f2(0.0f);
 
+  // v - mu of the row's elements
+  auto centred = [](F2 v, float mu) { return PLAIN ? v : v + f2(-mu); };
+  float next_gate = token_gate(p, t);
   int slot = 0;
   for (; t < p.T; t += step) {
     if constexpr (VEC) {
@@ -138,8 +141,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       if constexpr (POST) y.fetch(row_ptr<const TA>(p.y, t), m);
       if (p.dres_in.p != nullptr) dres_in.fetch(row_ptr<const TR>(p.dres_in, t), m);
     }
-    float gt = 1.0f;                             // the token's gate
-    if (token) gt = gate_act(p.gate_act, *row_ptr<const float>(p.gate_rows, t));
+    const float gt = token ? gate_act(p.gate_act, next_gate) : 1.0f;
+    next_gate = token_gate(p, t + step);
     float mu1 = 0.0f, mu2 = 0.0f;
     if (pre_layer || post_layer) {
       F2 a1 = f2(0.0f), a2 = f2(0.0f);
@@ -147,12 +150,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
         if constexpr (PRE) {
-          const Raw<TR, VEC> a = res.get(u, threads);
+          const Raw<TR, VEC> a = res.get(u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) a1 = a1 + a.pair(i);
         }
         if constexpr (POST) {
-          const Raw<TA, VEC> a = y.get(u, threads);
+          const Raw<TA, VEC> a = y.get(u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) a2 = a2 + a.pair(i);
         }
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     const F2 zero = f2(0.0f);
     auto load_D = [&](int u, F2 (&d)[4]) {
       if (p.dres_in.p != nullptr) {
-        const Raw<TR, VEC> a = dres_in.get(u, threads);
+        const Raw<TR, VEC> a = dres_in.get(u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = f2(p.dres_scale) * a.pair(i);
       } else {
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     // the scale with a token or full gate, the caller applies to the sums.
     // D is 0 past the row's end.
     auto post_sums = [&](int u, F2& s1, F2& s2, F2& s3) {
-      const Raw<TA, VEC> a = y.get(u, threads);
+      const Raw<TA, VEC> a = y.get(u);
       F2 w[4];
       w2.get(post_weight, u, w);
       if (full) {
@@ -197,10 +200,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const F2 dxh = D[u][i] * w[i];
-        s1 = s1 + dxh;
-        s2 = fma2(dxh, a.pair(i) + f2(-mu2), s2);
+        if (!PLAIN) s1 = s1 + dxh;
+        s2 = fma2(dxh, centred(a.pair(i), mu2), s2);
       }
-      if (token && p.post.b != nullptr) {
+      if (!PLAIN && token && p.post.b != nullptr) {
         F2 b[4];
         load_param(p.post.b, p, m[u], 0.0f, 0.0f, b);
 #pragma unroll
@@ -208,10 +211,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       }
     };
     auto post_squares = [&](int u, F2& q) {
-      const Raw<TA, VEC> a = y.get(u, threads);
+      const Raw<TA, VEC> a = y.get(u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const F2 c = within(m[u], i, a.pair(i) + f2(-mu2));
+        const F2 c = within(m[u], i, centred(a.pair(i), mu2));
         q = fma2(c, c, q);
       }
     };
@@ -221,24 +224,30 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
-        const Raw<TR, VEC> a = res.get(u, threads);
-        const Raw<TA, VEC> b = dx.get(u, threads);
+        const Raw<TR, VEC> a = res.get(u);
+        const Raw<TA, VEC> b = dx.get(u);
         F2 w[4];
         w1.get(pre_weight, u, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const F2 c = within(m[u], i, a.pair(i) + f2(-mu1));
+          const F2 c = within(m[u], i, centred(a.pair(i), mu1));
           const F2 dxh = b.pair(i) * w[i];
           s0 = fma2(c, c, s0);
-          s1 = s1 + dxh;
+          if (!PLAIN) s1 = s1 + dxh;
           s2 = fma2(dxh, c, s2);
         }
         if (normed) post_squares(u, s3);
       }
       float s[4] = {sum(s0), sum(s1), sum(s2), sum(s3)};
-      group_sum(g, s);
-      const float rstd = 1.0f / sqrtf(s[0] * inv + p.pre.eps);
-      if (normed) rstd2 = 1.0f / sqrtf(s[3] * inv + p.post.eps);
+      if constexpr (PLAIN && !POST) {
+        float q[2] = {s[0], s[2]};
+        group_sum(g, q);
+        s[0] = q[0], s[2] = q[1];
+      } else {
+        group_sum(g, s);
+      }
+      const float rstd = rsqrtf(s[0] * inv + p.pre.eps);
+      if (normed) rstd2 = rsqrtf(s[3] * inv + p.post.eps);
       // rstd (dxh - m0 - xhat m1) = rstd dxh + k1 r' + k0
       const float m1 = s[2] * inv * rstd, k1 = -(rstd * m1) * rstd;
       const float k0 = (pre_layer ? -rstd * (s[1] * inv) : 0.0f) - k1 * mu1;
@@ -247,17 +256,17 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
         load_D(u, D[u]);
-        const Raw<TR, VEC> a = res.get(u, threads);
-        const Raw<TA, VEC> b = dx.get(u, threads);
+        const Raw<TR, VEC> a = res.get(u);
+        const Raw<TA, VEC> b = dx.get(u);
         F2 w[4];
         w1.get(pre_weight, u, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F2 v = a.pair(i), d = b.pair(i);
-          acc[0][u][i] = fma2(d, fma2(v, r2, c2), acc[0][u][i]);   // dx is 0 past the end
-          if constexpr (BIAS) acc[1][u][i] = acc[1][u][i] + d;
-          const F2 dv = fma2(d * w[i], r2, fma2(v, kk1, kk0));
-          D[u][i] = within(m[u], i, D[u][i] + dv);
+          acc[0][u][i] = fma2(d, PLAIN ? v * r2 : fma2(v, r2, c2), acc[0][u][i]);
+          if constexpr (BIAS) acc[1][u][i] = acc[1][u][i] + d;     // dx is 0 past the end
+          const F2 join = PLAIN ? fma2(v, kk1, D[u][i]) : fma2(v, kk1, D[u][i] + kk0);
+          D[u][i] = within(m[u], i, fma2(d * w[i], r2, join));
         }
         if (p.dres.p != nullptr) store_unit(row_ptr<TR>(p.dres, t), m[u], D[u]);
       }
@@ -282,14 +291,25 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           if (!PRE && normed) post_squares(u, s0);
         }
         if constexpr (PRE) {
-          float s[3] = {sum(s1), sum(s2), sum(s3)};
+          if constexpr (PLAIN) {
+            float s[1] = {sum(s2)};
+            group_sum(g, s);
+            e2 = s[0];
+          } else {
+            float s[3] = {sum(s1), sum(s2), sum(s3)};
+            group_sum(g, s);
+            e1 = s[0], e2 = s[1], e3 = s[2];
+          }
+        } else if constexpr (PLAIN) {
+          float s[2] = {sum(s2), sum(s0)};
           group_sum(g, s);
-          e1 = s[0], e2 = s[1], e3 = s[2];
+          e2 = s[0];
+          rstd2 = rsqrtf(s[1] * inv + p.post.eps);
         } else {
           float s[4] = {sum(s1), sum(s2), sum(s3), sum(s0)};
           group_sum(g, s);
           e1 = s[0], e2 = s[1], e3 = s[2];
-          if (normed) rstd2 = 1.0f / sqrtf(s[3] * inv + p.post.eps);
+          if (normed) rstd2 = rsqrtf(s[3] * inv + p.post.eps);
         }
       }
       if (token && p.dgate.p != nullptr && g.lane == 0)
@@ -305,7 +325,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
-        const Raw<TA, VEC> a = y.get(u, threads);
+        const Raw<TA, VEC> a = y.get(u);
         F2 w[4], dy[4];
         w2.get(post_weight, u, w);
         if (full) {
@@ -327,9 +347,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F2 v = a.pair(i);                // D is 0 past the row's end
-          acc[kS1][u][i] = fma2(D[u][i], fma2(v, r2, c2), acc[kS1][u][i]);
+          acc[kS1][u][i] = fma2(D[u][i], PLAIN ? v * r2 : fma2(v, r2, c2), acc[kS1][u][i]);
           if constexpr (BIAS) acc[kS1 + 1][u][i] = fma2(D[u][i], f2(gt), acc[kS1 + 1][u][i]);
-          dy[i] = fma2(D[u][i] * w[i], kk2, fma2(v, kk1, kk0));
+          dy[i] = fma2(D[u][i] * w[i], kk2, PLAIN ? v * kk1 : fma2(v, kk1, kk0));
         }
         store_unit(row_ptr<TA>(p.dy, t), m[u], dy);
       }
@@ -362,52 +382,61 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   }
 }
 
-template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST, bool BIAS>
+template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST, bool BIAS, bool PLAIN>
 cudaError_t launch_kernel(const BlockArgs& a, int blocks, int groups, cudaStream_t s) {
-  const int threads = groups * a.tpr;
-  if constexpr (VEC && NV == 4) {
-    // the widest fp32 rows: not one fits the ring
-    if (static_cast<size_t>(ring_pieces<TA, TR, NV, VEC, PRE, POST>()) * threads * 16 > kBlockSmem)
-      return launch_kernel<TA, TR, NV, false, PRE, POST, BIAS>(a, blocks, groups, s);
-  }
   constexpr int kAcc = ((PRE ? 1 : 0) + (POST ? 1 : 0)) * (BIAS ? 2 : 1);
-  size_t row = static_cast<size_t>(ring_pieces<TA, TR, NV, VEC, PRE, POST>()) * threads * 16;
-  int ring = row == 0 ? 0 : static_cast<int>(kBlockSmem / row);
-  if (ring > kRing) ring = kRing;
-  size_t smem = ring * row;
-  if (groups > 1) {
-    const size_t join = static_cast<size_t>(kAcc) * a.d * sizeof(float);
-    if (join > smem) smem = join;
+  constexpr size_t kRow = static_cast<size_t>(ring_pieces<TA, TR, NV, VEC, PRE, POST>()) *
+                          kBlockThreads * 16;
+  if constexpr (VEC && kRow > kBlockSmem) {
+    // the widest fp32 rows: not one fits the ring
+    return launch_kernel<TA, TR, NV, false, PRE, POST, BIAS, false>(a, blocks, groups, s);
+  } else {
+    constexpr int kFit = kRow == 0 ? 0 : static_cast<int>(kBlockSmem / (kRow == 0 ? 1 : kRow));
+    constexpr int ring = kFit > kRing ? kRing : kFit;
+    size_t smem = ring * kRow;
+    if (groups > 1) {
+      const size_t join = static_cast<size_t>(kAcc) * a.d * sizeof(float);
+      if (join > smem) smem = join;
+    }
+    auto* k = k_block_bwd<TA, TR, NV, VEC, PRE, POST, BIAS, PLAIN>;
+    if (smem > 32 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    k<<<blocks, groups * a.tpr, smem, s>>>(a, ring);
+    return cudaGetLastError();
   }
-  auto* k = k_block_bwd<TA, TR, NV, VEC, PRE, POST, BIAS>;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+}
+
+template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST>
+cudaError_t launch_sides(const BlockArgs& a, const BlockGrads& o, int groups, cudaStream_t s) {
+  if constexpr (VEC && NV <= 2) {
+    const bool plain = !o.bias && (!PRE || a.pre.kind == MOE_NORM_RMS) &&
+                       (!POST || (a.post.kind == MOE_NORM_RMS && a.post.b == nullptr &&
+                                  a.gate != MOE_GATE_FULL));
+    if (plain) return launch_kernel<TA, TR, NV, true, PRE, POST, false, true>(a, o.parts, groups, s);
   }
-  k<<<blocks, threads, smem, s>>>(a, ring);
-  return cudaGetLastError();
+  return o.bias ? launch_kernel<TA, TR, NV, VEC, PRE, POST, true, false>(a, o.parts, groups, s)
+                : launch_kernel<TA, TR, NV, VEC, PRE, POST, false, false>(a, o.parts, groups, s);
 }
 
 template <typename TA, typename TR, int NV, bool VEC>
 cudaError_t launch_nv(const BlockArgs& a, const BlockGrads& o, int groups, cudaStream_t s) {
-  if (o.pre && o.post)
-    return o.bias ? launch_kernel<TA, TR, NV, VEC, true, true, true>(a, o.parts, groups, s)
-                  : launch_kernel<TA, TR, NV, VEC, true, true, false>(a, o.parts, groups, s);
-  if (o.pre)
-    return o.bias ? launch_kernel<TA, TR, NV, VEC, true, false, true>(a, o.parts, groups, s)
-                  : launch_kernel<TA, TR, NV, VEC, true, false, false>(a, o.parts, groups, s);
-  return o.bias ? launch_kernel<TA, TR, NV, VEC, false, true, true>(a, o.parts, groups, s)
-                : launch_kernel<TA, TR, NV, VEC, false, true, false>(a, o.parts, groups, s);
+  if (o.pre && o.post) return launch_sides<TA, TR, NV, VEC, true, true>(a, o, groups, s);
+  if (o.pre) return launch_sides<TA, TR, NV, VEC, true, false>(a, o, groups, s);
+  return launch_sides<TA, TR, NV, VEC, false, true>(a, o, groups, s);
 }
 
 }  // namespace
 
 template <typename TA, typename TR>
 cudaError_t launch_block_bwd_types(BlockArgs a, BlockGrads& o, int sms, cudaStream_t s) {
-  // the fewest units a thread (1, 2 or 4) with which 512 threads hold a row
+  // two units a thread where a row has them: more groups, whose sums wait apart
   const int units = (a.d + kUnit - 1) / kUnit;
-  const int nv = units <= kBlockThreads ? 1 : units <= 2 * kBlockThreads ? 2 : 4;
+  const int nv = units <= 32 || (!a.vec && units <= kBlockThreads) ? 1
+                 : units <= 2 * kBlockThreads                      ? 2
+                                                                   : 4;
   a.tpr = ((units + nv - 1) / nv + 31) / 32 * 32;
   const int groups = kBlockThreads / a.tpr;
   o.parts = (a.T + groups - 1) / groups;

@@ -54,7 +54,7 @@ __device__ __forceinline__ void row_stats(const BlockArgs& p, const BlockNorm& n
       for (int e = 0; e < 8; ++e) q[0] += v[u][e] * v[u][e];
   }
   group_sum(g, q);
-  rstd = 1.0f / sqrtf(q[0] * inv + n.eps);
+  rstd = rsqrtf(q[0] * inv + n.eps);
 }
 
 // Weight, bias and channel gate of a thread's units: fetched ahead (HOIST),
@@ -238,7 +238,7 @@ struct Slots {
   }
 };
 
-template <typename TA, typename TR, int NV, int MODE, bool BIAS>
+template <typename TA, typename TR, int NV, int MODE, bool BIAS, bool PLAIN>
 __global__ void __launch_bounds__(kBlockThreads, 1)
     k_block_fwd_ring(const __grid_constant__ BlockArgs p, int ring) {
   constexpr bool kHeld = NV <= 2;
@@ -247,9 +247,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   __shared__ float red[kRedFloats];
   extern __shared__ uint4 dyn[];
   Group<true> g = make_group<true>(p, red);
-  const int groups = blockDim.x / p.tpr, threads = blockDim.x;
+  const int groups = blockDim.x / p.tpr;
   const float inv = 1.0f / static_cast<float>(p.d);
-  const bool full = p.gate == MOE_GATE_FULL, token = p.gate == MOE_GATE_TOKEN;
+  const bool full = !PLAIN && p.gate == MOE_GATE_FULL, token = p.gate == MOE_GATE_TOKEN;
   const int slots = MODE == kRouted ? p.k : MODE == kPost ? 1 : 0;
   const int pieces = Res::kPieces + slots * Act::kPieces;
   Unit<true> m[NV];
@@ -261,22 +261,22 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   Res res;
   Act y;
   auto place = [&](int slot) {
-    res.at = dyn + static_cast<size_t>(slot) * pieces * threads + threadIdx.x;
-    y.at = res.at + Res::kPieces * threads;
+    res.at = dyn + slot * pieces * kBlockThreads + threadIdx.x;
+    y.at = res.at + Res::kPieces * kBlockThreads;
   };
   // copies row t (its expert rows given by s) into a slot of the ring
   auto copy = [&](int row, int slot, const Slots& s) {
     if (row < p.T) {
       place(slot);
-      if constexpr (MODE == kPost) y.copy(row_ptr<const TA>(p.y, row), m, threads);
+      if constexpr (MODE == kPost) y.copy(row_ptr<const TA>(p.y, row), m);
       if constexpr (MODE == kRouted) {
         for (int i = 0; i < slots; ++i) {
           const int r = __shfl_sync(0xFFFFFFFFu, s.row, i);
-          if (r >= 0) y.copy(row_ptr<const TA>(p.y, r), m, threads);
-          y.at += Act::kPieces * threads;
+          if (r >= 0) y.copy(row_ptr<const TA>(p.y, r), m);
+          y.at += Act::kPieces * kBlockThreads;
         }
       }
-      res.copy(row_ptr<const TR>(p.res, row), m, threads);
+      res.copy(row_ptr<const TR>(p.res, row), m);
     }
     copies_commit();   // one group a row, empty past the end
   };
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   // mean and 1/sqrt(. + eps) of the row in v
   auto stats = [&](const BlockNorm& n, float& mu, float& rstd) {
     mu = 0.0f;
-    if (n.kind == MOE_NORM_LAYER) {
+    if (!PLAIN && n.kind == MOE_NORM_LAYER) {
       F2 a = zero;
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
@@ -351,19 +351,20 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       if (beyond(m[u])) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const F2 c = v[u][i] + f2(-mu);
+        const F2 c = PLAIN ? v[u][i] : v[u][i] + f2(-mu);
         a = fma2(c, c, a);
       }
     }
     float s[1] = {sum(a)};
     group_sum(g, s);
-    rstd = 1.0f / sqrtf(s[0] * inv + n.eps);
+    rstd = rsqrtf(s[0] * inv + n.eps);
   };
 
+  float next_gate = token_gate(p, t);
   int slot = 0;
   for (; t < p.T; t += step) {
-    float gt = 1.0f;
-    if (token) gt = gate_act(p.gate_act, *row_ptr<const float>(p.gate_rows, t));
+    const float gt = token ? gate_act(p.gate_act, next_gate) : 1.0f;
+    next_gate = token_gate(p, t + step);
     ring_wait(ring);
     place(slot);
     Slots after = next;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
-        const Raw<TR, true> a = res.get(u, threads);
+        const Raw<TR, true> a = res.get(u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[u][i] = a.pair(i);
       }
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
           if (beyond(m[u])) continue;
-          const Raw<TA, true> a = y.get(u, threads);
+          const Raw<TA, true> a = y.get(u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[u][i] = a.pair(i);
         }
@@ -398,12 +399,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
               if (beyond(m[u])) continue;
-              const Raw<TA, true> a = y.get(u, threads);
+              const Raw<TA, true> a = y.get(u);
 #pragma unroll
               for (int i = 0; i < 4; ++i) v[u][i] = fma2(f2(w), a.pair(i), v[u][i]);
             }
           }
-          y.at += Act::kPieces * threads;
+          y.at += Act::kPieces * kBlockThreads;
         }
         if (p.y_out.p != nullptr) {
 #pragma unroll
@@ -411,17 +412,18 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         }
       }
       float mu = 0.0f, rstd = 1.0f;
-      if (p.post.kind != MOE_NORM_NONE) stats(p.post, mu, rstd);
+      if (PLAIN || p.post.kind != MOE_NORM_NONE) stats(p.post, mu, rstd);
       const float k = full || token ? p.branch_scale * gt : 1.0f;
       const F2 k1 = f2(rstd * k), k0 = f2(-mu * rstd * k), a1 = f2(p.res_scale);
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
-        const Raw<TR, true> r = res.get(u, threads);
+        const Raw<TR, true> r = res.get(u);
         F2 w[4];
         w2.get(post_weight, u, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[u][i] = fma2(v[u][i], k1, k0) * w[i];
+        for (int i = 0; i < 4; ++i)
+          v[u][i] = (PLAIN ? v[u][i] * k1 : fma2(v[u][i], k1, k0)) * w[i];
         if constexpr (BIAS) {
           F2 b[4];
           b2.get(post_bias, u, b);
@@ -454,7 +456,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         F2 w[4], x[4];
         w1.get(pre_weight, u, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fma2(v[u][i], k1, k0) * w[i];
+        for (int i = 0; i < 4; ++i)
+          x[i] = (PLAIN ? v[u][i] * k1 : fma2(v[u][i], k1, k0)) * w[i];
         if constexpr (BIAS) {
           F2 b[4];
           b1.get(pre_bias, u, b);
@@ -480,13 +483,18 @@ cudaError_t launch_ring(const BlockArgs& a, int sms, bool& none, cudaStream_t s)
   const int groups = kBlockThreads / a.tpr, threads = groups * a.tpr;
   const int slots = MODE == kRouted ? a.k : MODE == kPost ? 1 : 0;
   const size_t row = static_cast<size_t>(RowPart<TR, NV, true>::kPieces +
-                                         slots * RowPart<TA, NV, true>::kPieces) * threads * 16;
+                                         slots * RowPart<TA, NV, true>::kPieces) *
+                     kBlockThreads * 16;
   int ring = static_cast<int>(kBlockSmem / row);
   none = ring == 0;
   if (none) return cudaSuccess;
   if (ring > kRing) ring = kRing;
   const bool bias = a.post.b != nullptr || a.pre.b != nullptr;
-  auto* k = bias ? k_block_fwd_ring<TA, TR, NV, MODE, true> : k_block_fwd_ring<TA, TR, NV, MODE, false>;
+  const bool plain = !bias && (a.x.p == nullptr || a.pre.kind == MOE_NORM_RMS) &&
+                     (MODE == kPre || (a.post.kind == MOE_NORM_RMS && a.gate != MOE_GATE_FULL));
+  auto* k = plain  ? k_block_fwd_ring<TA, TR, NV, MODE, false, true>
+            : bias ? k_block_fwd_ring<TA, TR, NV, MODE, true, false>
+                   : k_block_fwd_ring<TA, TR, NV, MODE, false, false>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kBlockSmem));
   if (e != cudaSuccess) return e;

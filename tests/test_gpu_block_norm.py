@@ -104,7 +104,9 @@ SHAPES = [dict(T=1, d=64), dict(T=1, d=7168), dict(T=3, d=1), dict(T=5, d=7), di
           dict(T=130, d=2048), dict(T=9, d=1441), dict(T=4, d=4104), dict(T=3, d=8200),
           dict(T=2, d=16384), dict(T=2, d=16383), dict(T=300, d=256), dict(T=700, d=96),
           dict(T=37, d=520, pitch=8), dict(T=37, d=520, pitch=9, shift=3),
-          dict(T=33, d=4096, pitch=24, shift=8), dict(T=1000, d=72)]
+          dict(T=33, d=4096, pitch=24, shift=8), dict(T=1000, d=72),
+          dict(T=700, d=2048), dict(T=320, d=7168), dict(T=310, d=9000), dict(T=340, d=1448, pitch=8),
+          dict(T=600, d=1001)]
 KINDS = [dict(), dict(pre="layer", bias=True), dict(types="bf16/fp32/fp32", offset=1.0),
          dict(pre="layer", types="fp32/fp32/fp32"), dict(types="bf16/fp32/bf16", weights=False),
          dict(types="fp32/fp32/bf16", bias=True)]
