@@ -804,8 +804,8 @@ moe_status_t moe_fc1_wgrad_tf32(const moe_mlp_desc_t* desc, const void* dh_t, co
  *
  * Row tensors are moe_rows_t: element (t, c) at p[t*ld + c], ld >= d in
  * elements, any element alignment.  With d a multiple of 8 and every row
- * 16-byte aligned the kernels move 16 bytes per thread, otherwise single
- * elements. */
+ * aligned to 8 elements (16 bytes in bf16, 32 in fp32) the kernels move 8
+ * elements at a time, otherwise single ones. */
 typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind_t;
 typedef enum {
   MOE_GATE_NONE = 0,

@@ -41,7 +41,7 @@ struct BlockNorm {
 struct BlockArgs {
   int T, d;
   int tpr;           // threads of a group (the launchers')
-  int vec;           // every row 16-byte aligned and d % 8 == 0
+  int vec;           // every row aligned to a unit, and d % 8 == 0
   int p32;           // parameters are fp32 (else bf16)
   int gate, gate_act;
   float res_scale, branch_scale, dres_scale;
@@ -129,6 +129,21 @@ __device__ __forceinline__ uint4 load16_once(const void* p) {
   return v;
 }
 
+// 32 bytes at a time (an fp32 unit): whole sectors, where two 16-byte accesses
+// a thread would each touch every second half of the warp's sectors.
+__device__ __forceinline__ void load32_once(const void* p, uint32_t (&v)[8]) {
+  asm volatile(
+      "ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // A unit's 8 elements as they lie in memory (VEC: 16 bytes in bf16, 32 in
 // fp32; else one register each), 0 past the row's end.
 template <typename T, bool VEC>
@@ -138,7 +153,11 @@ struct Raw {
 
   template <bool ONCE>
   __device__ __forceinline__ void load(const T* row, const Unit<VEC>& m) {
-    if constexpr (VEC) {
+    if constexpr (VEC && ONCE && sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 0u;
+      if (m.has(0)) load32_once(row + m.c0, w);
+    } else if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
         uint4 q = make_uint4(0, 0, 0, 0);
@@ -184,8 +203,7 @@ __device__ __forceinline__ void store_unit(T* row, const Unit<VEC>& m, const flo
             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                        pack_bf16x2(v[6], v[7]));
       } else {
-        *reinterpret_cast<float4*>(row + m.c0) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(row + m.c0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        store32(row + m.c0, v);
       }
     }
   } else {
@@ -365,25 +383,35 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One row tensor of a row: a thread's units, in its places of the ring (VEC)
-// or in registers.
+// One row tensor of a row: a thread's units, in the ring (VEC) or in registers.
+// In the ring a unit of the block takes kBlockThreads places of 16 bytes (bf16:
+// each thread's own) or twice as many (fp32: a warp's 64 in the order of the
+// row, so that its copies move whole sectors; every second eight of them are
+// swapped in pairs, which keeps the threads' reads off each other's banks).
 template <typename T, int NV, bool VEC>
 struct RowPart {
-  static constexpr int kPieces = VEC ? NV * static_cast<int>(sizeof(T)) / 2 : 0;
+  static constexpr int kHalves = sizeof(T) / 2;
+  static constexpr int kPieces = VEC ? NV * kHalves : 0;   // kBlockThreads places each
   Raw<T, VEC> held[VEC ? 1 : NV];
-  uint4* at;   // piece i at at[i * kBlockThreads]
+  uint4* at;
 
   __device__ __forceinline__ void copy(const T* row, const Unit<VEC> (&m)[NV]) {
     if constexpr (VEC) {
-      constexpr int kHalves = sizeof(T) / 2;
+      const int l = threadIdx.x & 31;
 #pragma unroll
-      for (int u = 0; u < NV; ++u)
-        if (m[u].has(0)) {
+      for (int u = 0; u < NV; ++u) {
+        if constexpr (kHalves == 1) {
+          if (m[u].has(0)) copy16_async(at + u * kBlockThreads + threadIdx.x, row + m[u].c0);
+        } else {
+          uint4* to = at + u * 2 * kBlockThreads + 2 * (threadIdx.x - l);
+          const int c = m[u].c0 - l * kUnit;               // the warp's first channel
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            copy16_async(at + (u * kHalves + h) * kBlockThreads,
-                         reinterpret_cast<const uint4*>(row + m[u].c0) + h);
+          for (int h = 0; h < 2; ++h) {
+            const int q = h * 32 + l;
+            if (c + q * 4 < m[u].d) copy16_async(to + (q ^ ((q >> 3) & 1)), row + c + q * 4);
+          }
         }
+      }
     }
   }
   __device__ __forceinline__ void fetch(const T* row, const Unit<VEC> (&m)[NV]) {
@@ -395,12 +423,14 @@ struct RowPart {
   // (VEC: of a unit within the row)
   __device__ __forceinline__ Raw<T, VEC> get(int u) const {
     if constexpr (VEC) {
-      constexpr int kHalves = sizeof(T) / 2;
+      const int l = threadIdx.x & 31;
       Raw<T, VEC> r;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        const uint4 q = at[(u * kHalves + h) * kBlockThreads];
-        r.w[4 * h] = q.x, r.w[4 * h + 1] = q.y, r.w[4 * h + 2] = q.z, r.w[4 * h + 3] = q.w;
+        const int q = kHalves == 1 ? static_cast<int>(threadIdx.x)
+                                   : 2 * (threadIdx.x - l) + ((2 * l + h) ^ ((l >> 2) & 1));
+        const uint4 v = at[u * kHalves * kBlockThreads + q];
+        r.w[4 * h] = v.x, r.w[4 * h + 1] = v.y, r.w[4 * h + 2] = v.z, r.w[4 * h + 3] = v.w;
       }
       return r;
     } else {
@@ -441,6 +471,7 @@ __device__ __forceinline__ void ring_wait(int ring) {
   if (ring >= 3) copies_wait<2>();
   else if (ring == 2) copies_wait<1>();
   else copies_wait<0>();
+  __syncwarp();   // the warp's copies, its other threads' among them
 }
 
 // Blocks whose partial sums the backward's workspace has room for.

@@ -48,7 +48,8 @@ struct Checker {
     const size_t b = type_bytes(type);
     const uintptr_t at = reinterpret_cast<uintptr_t>(r.p);
     if (at % b || r.ld < 0 || (n_rows > 1 && r.ld < d->d)) fail(MOE_ERR_SHAPE);
-    if (at % 16 || (n_rows > 1 && (static_cast<size_t>(r.ld) * b) % 16)) vec = false;
+    const size_t whole = kUnit * b;   // a unit: 16 or 32 bytes
+    if (at % whole || (n_rows > 1 && (static_cast<size_t>(r.ld) * b) % whole)) vec = false;
     return {static_cast<char*>(r.p), static_cast<long long>(r.ld)};
   }
   BlockRows rows(const moe_rows_t& r, int type, bool required) {

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   RowPart<TA, NV, VEC> dx, y;
   auto place = [&](int slot) {
     if constexpr (VEC) {
-      uint4* at = dyn + slot * kPieces * kBlockThreads + threadIdx.x;
+      uint4* at = dyn + slot * kPieces * kBlockThreads;
       dres_in.at = at;
       at += RowPart<TR, NV, VEC>::kPieces * kBlockThreads;
       if constexpr (PRE) {
@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         store_unit(row_ptr<TA>(p.dy, t), m[u], dy);
       }
     }
+    __syncwarp();
     copy(t + ring * step, slot);
     slot = slot + 1 == ring ? 0 : slot + 1;
   }

@@ -241,7 +241,7 @@ struct Slots {
 template <typename TA, typename TR, int NV, int MODE, bool BIAS, bool PLAIN>
 __global__ void __launch_bounds__(kBlockThreads, 1)
     k_block_fwd_ring(const __grid_constant__ BlockArgs p, int ring) {
-  constexpr bool kHeld = NV <= 2;
+  constexpr bool kHeld = NV <= 2 || PLAIN;
   using Res = RowPart<TR, NV, true>;
   using Act = RowPart<TA, NV, true>;
   __shared__ float red[kRedFloats];
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   Res res;
   Act y;
   auto place = [&](int slot) {
-    res.at = dyn + slot * pieces * kBlockThreads + threadIdx.x;
+    res.at = dyn + slot * pieces * kBlockThreads;
     y.at = res.at + Res::kPieces * kBlockThreads;
   };
   // copies row t (its expert rows given by s) into a slot of the ring
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[u][i] = a.pair(i);
       }
+      __syncwarp();
       copy(t + ring * step, slot, next);   // the row is in registers
     } else {
       if constexpr (MODE == kPost) {
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         for (int i = 0; i < 4; ++i) v[u][i] = fma2(a1, r.pair(i), v[u][i]);
         store_unit(row_ptr<TR>(p.res_out, t), m[u], v[u]);
       }
+      __syncwarp();
       copy(t + ring * step, slot, next);
     }
     if (p.x.p != nullptr) {
@@ -477,6 +479,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   }
 }
 
+bool plain_fwd(const BlockArgs& a, bool post) {
+  return a.post.b == nullptr && a.pre.b == nullptr &&
+         (a.x.p == nullptr || a.pre.kind == MOE_NORM_RMS) &&
+         (!post || (a.post.kind == MOE_NORM_RMS && a.gate != MOE_GATE_FULL));
+}
+
 // Launches the ring's kernel; `none` set where not one row fits the ring.
 template <typename TA, typename TR, int NV, int MODE>
 cudaError_t launch_ring(const BlockArgs& a, int sms, bool& none, cudaStream_t s) {
@@ -490,8 +498,7 @@ cudaError_t launch_ring(const BlockArgs& a, int sms, bool& none, cudaStream_t s)
   if (none) return cudaSuccess;
   if (ring > kRing) ring = kRing;
   const bool bias = a.post.b != nullptr || a.pre.b != nullptr;
-  const bool plain = !bias && (a.x.p == nullptr || a.pre.kind == MOE_NORM_RMS) &&
-                     (MODE == kPre || (a.post.kind == MOE_NORM_RMS && a.gate != MOE_GATE_FULL));
+  const bool plain = plain_fwd(a, MODE != kPre);
   auto* k = plain  ? k_block_fwd_ring<TA, TR, NV, MODE, false, true>
             : bias ? k_block_fwd_ring<TA, TR, NV, MODE, true, false>
                    : k_block_fwd_ring<TA, TR, NV, MODE, false, false>;
@@ -533,7 +540,10 @@ cudaError_t launch_block_fwd_types(BlockArgs a, bool post, int sms, cudaStream_t
   auto threads = [&](int nv) { return ((units + nv - 1) / nv + 31) / 32 * 32; };
   if (a.vec && a.T > kFewRows * sms) {
     bool none = false;
-    const int nv = units <= 32 ? 1 : units <= 2 * kBlockThreads ? 2 : 4;
+    // two units a thread where a row has them, and four where their parameters
+    // still fit the registers: more groups, whose sums wait apart
+    const bool four = units > 2 * kBlockThreads || (units > 128 && plain_fwd(a, post));
+    const int nv = units <= 32 ? 1 : four ? 4 : 2;
     a.tpr = threads(nv);
     const cudaError_t e = nv == 1   ? launch_ring_mode<TA, TR, 1>(a, post, sms, none, s)
                           : nv == 2 ? launch_ring_mode<TA, TR, 2>(a, post, sms, none, s)
