@@ -292,8 +292,11 @@ def _p(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    # the current stream's handle without building a torch.cuda.Stream (0.3
+    # instead of 3 us a call)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(st):
@@ -723,7 +726,7 @@ def _rows(t, n, d, dtype):
         return _NO_ROWS
     if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"expected a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    if t.dim() != 2 or t.size(0) != n or t.size(1) != d:
+    if t.shape != (n, d):
         raise ValueError(f"expected a tensor of shape {(n, d)}, got {tuple(t.shape)}")
     ld, step = t.stride()
     if (step != 1 and d > 1) or (ld < d and n > 1):
@@ -745,22 +748,25 @@ def _block_params(desc, p):
     """dict of optional tensors {pre_w, pre_b, post_w, post_b, gate} ->
     moe_block_params_t."""
     dt, d = _TORCH[desc.param_dtype], desc.d
-    g, gate = p.get("gate"), _NO_ROWS
-    if g is not None and desc.gate:
-        if desc.gate == 1:
-            gate = moe_rows_t(_vector(g, d, dt), 0)
-        elif desc.gate == 3:
-            gate = _rows(g, desc.T, d, _TORCH[desc.dtype])
+    out = moe_block_params_t()
+    for n in ("pre_w", "pre_b", "post_w", "post_b"):
+        t = p.get(n)
+        if t is not None:
+            setattr(out, n, _vector(t, d, dt))
+    g, kind = p.get("gate"), desc.gate
+    if g is not None and kind:
+        if kind == 1:
+            out.gate = moe_rows_t(_vector(g, d, dt), 0)
+        elif kind == 3:
+            out.gate = _rows(g, desc.T, d, _TORCH[desc.dtype])
         else:
-            if g.dtype is not torch.float32 or not g.is_cuda or g.dim() != 1 or g.size(0) != desc.T:
+            if g.dtype is not torch.float32 or not g.is_cuda or g.shape != (desc.T,):
                 raise ValueError(f"expected an fp32 CUDA gate of {desc.T} tokens, got {g.dtype} "
                                  f"{tuple(g.shape)} on {g.device}")
             if g.stride(0) < 1 and desc.T > 1:
                 raise ValueError("the tokens' gates must be apart")
-            gate = moe_rows_t(g.data_ptr(), max(g.stride(0), 1))
-    return moe_block_params_t(_vector(p.get("pre_w"), d, dt), _vector(p.get("pre_b"), d, dt),
-                              _vector(p.get("post_w"), d, dt), _vector(p.get("post_b"), d, dt),
-                              gate)
+            out.gate = moe_rows_t(g.data_ptr(), max(g.stride(0), 1))
+    return out
 
 
 def moe_block_norm_workspace_size(desc):
@@ -853,8 +859,8 @@ class GradList:
     """Gradient tensors (bf16 or fp32, contiguous or rows at one distance) and
     where their clipped copies go (outs; default: in place), described for
     moe_grad_norm and moe_clip_grads.  The list holds the tensors; one whose
-    memory was replaced or resized since (`tensor.data = ...`) is described
-    anew at the next call."""
+    memory was replaced since (`tensor.data = ...`) is described anew at the
+    next call; shapes, strides and types stay as they were."""
 
     def __init__(self, tensors, outs=None):
         self.tensors = list(tensors)
@@ -862,18 +868,19 @@ class GradList:
         if len(self.outs) != len(self.tensors):
             raise ValueError(f"{len(self.tensors)} gradients and {len(self.outs)} outputs")
         self.array = (moe_grad_t * max(len(self.tensors), 1))()
-        self._places = None
+        self._here = self._there = None
         self.refresh()
 
     def __len__(self):
         return len(self.tensors)
 
-    def refresh(self):
-        places = [t.data_ptr() for t in self.tensors] + [t.numel() for t in self.tensors]
-        if self.outs is not self.tensors:
-            places += [t.data_ptr() for t in self.outs]
-            places += [t.numel() for t in self.outs]
-        if places == self._places:
+    def refresh(self, outs=True):
+        """Describes the tensors (and, if asked, the outputs) anew where their
+        memory is another than it was."""
+        here = list(map(torch.Tensor.data_ptr, self.tensors))
+        there = (here if self.outs is self.tensors else
+                 list(map(torch.Tensor.data_ptr, self.outs)) if outs else self._there)
+        if here == self._here and there == self._there:
             return
         kinds = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
         for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
@@ -884,13 +891,13 @@ class GradList:
                 raise ValueError(f"gradient {i}: shapes {tuple(t.shape)} and {tuple(o.shape)}")
             self.array[i] = moe_grad_t(t.data_ptr(), o.data_ptr(), *_runs(t, o), kinds[t.dtype],
                                        kinds[o.dtype])
-        self._places = places
+        self._here, self._there = here, there
 
 
-def _grad_list(grads):
+def _grad_list(grads, outs):
     if not isinstance(grads, GradList):
         return GradList(grads)
-    grads.refresh()
+    grads.refresh(outs)
     return grads
 
 
@@ -903,7 +910,7 @@ def moe_grad_norm_workspace_size(n):
 def moe_grad_norm(grads, norm, norms, norm_type, ws, stream=None):
     """Global norm of a GradList (or a list of tensors) into norm fp32 [1], and
     each tensor's into norms fp32 [n] (or None); norm_type "l2" or "inf"."""
-    g = _grad_list(grads)
+    g = _grad_list(grads, False)
     if norm.dtype is not torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be one fp32 value")
     if norms is not None and (norms.dtype is not torch.float32 or norms.numel() != len(g)):
@@ -915,7 +922,7 @@ def moe_grad_norm(grads, norm, norms, norm_type, ws, stream=None):
 def moe_clip_grads(grads, norm, max_norm, eps=1e-6, stream=None):
     """outs = grads * min(1, max_norm / (norm + eps)), norm fp32 [1] on the
     device."""
-    g = _grad_list(grads)
+    g = _grad_list(grads, True)
     if norm.dtype is not torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be one fp32 value")
     _check(lib().moe_clip_grads(g.array, len(g), _p(norm), max_norm, eps, _stream(stream)))

@@ -14,6 +14,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "moe_f2.cuh"
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -61,41 +64,6 @@ struct BlockArgs {
   BlockRows dgate;   // token, full
 };
 
-// Two fp32 values in one 64-bit register pair: one instruction for both.
-struct F2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
-__device__ __forceinline__ float2 parts(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ float sum(F2 a) {
-  const float2 p = parts(a);
-  return p.x + p.y;
-}
-
 // Channels of unit u of thread `lane` of its group: c0, c0 + step, ..., those
 // below d.  VEC: 8 neighbours, all or none.
 template <bool VEC>
@@ -127,21 +95,6 @@ __device__ __forceinline__ uint4 load16_once(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-
-// 32 bytes at a time (an fp32 unit): whole sectors, where two 16-byte accesses
-// a thread would each touch every second half of the warp's sectors.
-__device__ __forceinline__ void load32_once(const void* p, uint32_t (&v)[8]) {
-  asm volatile(
-      "ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7])
-      : "l"(p));
-}
-__device__ __forceinline__ void store32(void* p, const float (&v)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
-               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
 }
 
 // A unit's 8 elements as they lie in memory (VEC: 16 bytes in bf16, 32 in
@@ -472,6 +425,20 @@ __device__ __forceinline__ void ring_wait(int ring) {
   else if (ring == 2) copies_wait<1>();
   else copies_wait<0>();
   __syncwarp();   // the warp's copies, its other threads' among them
+}
+
+// Lets a kernel take the ring's shared memory, once for each device (`done`:
+// the kernel's own, a bit a device).
+inline cudaError_t allow_ring(const void* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kBlockSmem));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Blocks whose partial sums the backward's workspace has room for.

@@ -83,16 +83,7 @@ cudaError_t launch_block_bwd(const BlockArgs& a, BlockGrads o, int dtype, int re
     e = launch_block_bwd_types<__nv_bfloat16, __nv_bfloat16>(a, o, sms, s);
   const bool any = o.dpre_w || o.dpre_b || o.dpost_w || o.dpost_b || o.dgate;
   if (e == cudaSuccess && any) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.d + 31) / 32);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_block_bwd_finish, a, o);
+    e = launch_dependent(k_block_bwd_finish, (a.d + 31) / 32, 1024, s, a, o);
   }
   return e;
 }

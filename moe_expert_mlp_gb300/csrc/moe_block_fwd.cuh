@@ -502,8 +502,8 @@ cudaError_t launch_ring(const BlockArgs& a, int sms, bool& none, cudaStream_t s)
   auto* k = plain  ? k_block_fwd_ring<TA, TR, NV, MODE, false, true>
             : bias ? k_block_fwd_ring<TA, TR, NV, MODE, true, false>
                    : k_block_fwd_ring<TA, TR, NV, MODE, false, false>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kBlockSmem));
+  static std::atomic<uint64_t> done[3];
+  const cudaError_t e = allow_ring(reinterpret_cast<const void*>(k), done[plain ? 0 : bias ? 1 : 2]);
   if (e != cudaSuccess) return e;
   int blocks = (a.T + groups - 1) / groups;
   if (blocks > sms) blocks = sms;

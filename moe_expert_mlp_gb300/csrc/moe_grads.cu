@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include "moe_f2.cuh"
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -23,6 +24,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kTile = 16384;        // elements of a tile
 constexpr int kMaxList = 448;       // tensors of a launch: 28 KB of parameters
+constexpr int kResident = 2;        // blocks of an SM
 constexpr int kMaxBlocks = 608;
 
 struct Tensor {
@@ -56,6 +58,13 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_of(const Tensor& t, int i) {
   Tile r;
+  if (t.rows == 1) {   // without divisions
+    r.row = 0;
+    r.col = static_cast<long long>(i) * kTile;
+    r.rows = 1;
+    r.cols = static_cast<int>(min(static_cast<long long>(kTile), t.cols - r.col));
+    return r;
+  }
   const long long pieces = row_pieces(t.cols), many = tile_rows(t.cols);
   if (pieces > 1) {
     r.row = i / pieces;
@@ -82,101 +91,211 @@ __device__ __forceinline__ int tensor_of(const List<N>& l, int i) {
   return lo;
 }
 
-// Sum of the squares of 32 elements.  fp32 holds it unless it overflows or
-// squares have vanished; then it is taken in fp64 (elements that are all zero
-// need neither).
-__device__ __forceinline__ double squares32(const float (&v)[32]) {
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) s += v[e] * v[e];
-  if (s >= 1e-30f && s <= 3e38f) return s;
-  double d = 0.0;
-  uint32_t any = 0;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) any |= __float_as_uint(v[e]) << 1;
-  if (any != 0) {
-#pragma unroll 1
-    for (int e = 0; e < 32; ++e) d += static_cast<double>(v[e]) * v[e];
-  }
-  return d;
-}
-
-template <bool INF>
-struct Sum {
-  double sum = 0.0;
-  uint32_t top = 0;   // bits of the largest magnitude: NaN above Inf above the finite
-  __device__ __forceinline__ void add(const float (&v)[32]) {
-    if constexpr (INF) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-    } else {
-      sum += squares32(v);
-    }
-  }
-};
-
 __device__ __forceinline__ float element(const char* base, long long i, bool f32) {
   return f32 ? reinterpret_cast<const float*>(base)[i]
              : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i]);
 }
 
-// 8 elements from a 16-byte aligned place.
-__device__ __forceinline__ void eight(const char* base, long long i, bool f32, float* v) {
+// 8 elements as they lie in memory: 4 words of bf16, 8 of fp32.
+__device__ __forceinline__ void raw_eight(const char* base, int i, bool f32, uint32_t (&w)[8]) {
   if (f32) {
-    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    load32_once(base + i * 4LL, w);
   } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + i);
-    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
+    const uint4 q = *reinterpret_cast<const uint4*>(base + i * 2LL);
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
   }
 }
 
-// Whether rows are adjacent, so that a tile is one run of elements.
-__device__ __forceinline__ bool one_run(const Tile& t, long long ld) {
-  return t.rows == 1 || ld == t.cols;
+// Whether a tile is one run of elements that starts on 32 bytes.
+__device__ __forceinline__ bool wide_run(const Tile& t, const char* base, long long ld) {
+  return (t.rows == 1 || ld == t.cols) && (reinterpret_cast<uintptr_t>(base) & 31) == 0;
 }
 
-template <bool INF>
-__device__ __forceinline__ void add_tile(const Tensor& t, const Tile& q, Sum<INF>& s) {
-  const int bytes = t.in32 ? 4 : 2;
+// A thread's sum of squares over some tiles of a tensor, in eight fp32 chains
+// of at most 16 squares each (kFlush tiles); then it goes to fp64.  The chains
+// hold it unless they overflow or squares have vanished: then the caller takes
+// it from the tiles again in fp64 (elements that are all zero need no second
+// look).
+constexpr int kFlush = 4;
+
+struct Squares {
+  F2 s[4];
+  uint32_t any;   // the elements' bits but their signs
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = f2(0.0f);
+    any = 0;
+  }
+  __device__ __forceinline__ void add(const uint32_t (&w)[8], bool f32) {
+    if (f32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 v = f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        s[i] = fma2(v, v, s[i]);
+        any |= (w[2 * i] | w[2 * i + 1]) & 0x7FFFFFFFu;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 v = f2(bf16_lo(w[i]), bf16_hi(w[i]));
+        s[i] = fma2(v, v, s[i]);
+        any |= w[i] & 0x7FFF7FFFu;
+      }
+    }
+  }
+  __device__ __forceinline__ void add(const uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 v = f2(bf16_lo(w[i]), bf16_hi(w[i]));
+      s[i] = fma2(v, v, s[i]);
+      any |= w[i] & 0x7FFF7FFFu;
+    }
+  }
+  __device__ __forceinline__ void add(const uint32_t (&w)[8]) { add(w, true); }
+  __device__ __forceinline__ void add(int i, float v) {
+    const F2 q = i & 1 ? f2(0.0f, v) : f2(v, 0.0f);
+    s[i / 2] = fma2(q, q, s[i / 2]);
+    any |= __float_as_uint(v) & 0x7FFFFFFFu;
+  }
+  __device__ __forceinline__ float total() const { return sum((s[0] + s[1]) + (s[2] + s[3])); }
+};
+
+// The largest magnitude, as bits (NaN above Inf above the finite); bf16 pairs
+// side by side.
+struct Top {
+  uint32_t top, pair;
+  __device__ __forceinline__ void clear() { top = pair = 0; }
+  __device__ __forceinline__ void add(const uint32_t (&w)[8], bool f32) {
+    if (f32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, w[i] & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pair = __vmaxu2(pair, w[i] & 0x7FFF7FFFu);
+    }
+  }
+  __device__ __forceinline__ void add(int, float v) { top = max(top, __float_as_uint(v) & 0x7FFFFFFFu); }
+  __device__ __forceinline__ uint32_t total() const {
+    return max(top, max(pair << 16, pair & 0xFFFF0000u));
+  }
+};
+
+// Hands a thread its elements of a tile: 8 at a time, or single ones with the
+// chain they belong to.
+template <typename Sum>
+__device__ __forceinline__ void add_tile(const Tensor& t, const Tile& q, Sum& s) {
   const int n = q.rows * q.cols;
-  const char* base = t.in + (q.row * t.ld + q.col) * bytes;
-  if (one_run(q, t.ld) && (reinterpret_cast<uintptr_t>(base) & 15) == 0) {
-    for (int i = threadIdx.x * 8; i < n; i += kThreads * 32) {
-      float v[32];
+  const char* base = t.in + (q.row * t.ld + q.col) * (t.in32 ? 4 : 2);
+  if (wide_run(q, base, t.ld)) {
+    if (n == kTile) {
+      // all four loads in flight
+      uint32_t w[4][8];
+      if (t.in32) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int at = i + u * kThreads * 8;
-        if (at + 8 <= n) {
-          eight(base, at, t.in32, v + 8 * u);
-        } else {
+        for (int u = 0; u < 4; ++u) raw_eight(base, (u * kThreads + threadIdx.x) * 8, true, w[u]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * u + e] = at + e < n ? element(base, at + e, t.in32) : 0.0f;
-        }
+        for (int u = 0; u < 4; ++u) s.add(w[u], true);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) raw_eight(base, (u * kThreads + threadIdx.x) * 8, false, w[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s.add(w[u], false);
       }
-      s.add(v);
+      return;
     }
+    for (int at = threadIdx.x * 8; at < n; at += kThreads * 8) {
+      if (at + 8 <= n) {
+        uint32_t w[8];
+        raw_eight(base, at, t.in32, w);
+        s.add(w, t.in32);
+      } else {
+        for (int e = 0; at + e < n; ++e) s.add(e, element(base, at + e, t.in32));
+      }
+    }
+    return;
+  }
+  for (int at = threadIdx.x; at < n; at += kThreads) {
+    const int r = at / q.cols;
+    s.add((at / kThreads) & 7, element(base, r * t.ld + (at - r * q.cols), t.in32));
+  }
+}
+
+// kFlush whole tiles on end, 128 bytes of a thread in flight at a time (with 64
+// the loads' latency showed: 247 instead of 174 us over 1.1 GB of bf16).
+template <bool IN32>
+__device__ __forceinline__ void add_four(const char* base, Squares& s) {
+  constexpr int kBatch = IN32 ? 4 : 8;
+#pragma unroll
+  for (int b = 0; b < 4 * kFlush / kBatch; ++b) {
+    uint32_t w[kBatch][IN32 ? 8 : 4];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int at = ((b * kBatch + u) * kThreads + threadIdx.x) * 8;
+      if constexpr (IN32) {
+        load32_once(base + at * 4LL, w[u]);
+      } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(base + at * 2LL);
+        w[u][0] = q.x, w[u][1] = q.y, w[u][2] = q.z, w[u][3] = q.w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) s.add(w[u]);
+  }
+}
+
+// The squares of the same elements once more, in fp64 (out of the way: called
+// only where fp32 does not hold them).
+__device__ __noinline__ double squares_again(const Tensor& t, int from, int to) {
+  double d = 0.0;
+  for (int i = from; i < to; ++i) {
+    const Tile q = tile_of(t, i);
+    const int n = q.rows * q.cols;
+    const char* base = t.in + (q.row * t.ld + q.col) * (t.in32 ? 4 : 2);
+    const int step = wide_run(q, base, t.ld) ? 8 : 1;
+    for (int at = threadIdx.x * step; at < n; at += kThreads * step)
+      for (int e = 0; e < step && at + e < n; ++e) {
+        const int r = (at + e) / q.cols;
+        const double v = element(base, r * t.ld + (at + e - r * q.cols), t.in32);
+        d += v * v;
+      }
+  }
+  return d;
+}
+
+// A thread's part of tiles from .. to - 1 of a tensor: its squares, or the
+// bits of its largest magnitude (exact in fp64).
+template <bool INF>
+__device__ __forceinline__ double add_tiles(const Tensor& t, int from, int to) {
+  if constexpr (INF) {
+    Top s;
+    s.clear();
+    for (int i = from; i < to; ++i) add_tile(t, tile_of(t, i), s);
+    return static_cast<double>(s.total());
   } else {
-    for (int i = threadIdx.x; i < n; i += kThreads * 32) {
-      float v[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int at = i + e * kThreads;
-        const int r = at / q.cols;
-        v[e] = at < n ? element(base, r * t.ld + (at - r * q.cols), t.in32) : 0.0f;
-      }
-      s.add(v);
+    double d = 0.0;
+    const bool whole = t.rows == 1 && (reinterpret_cast<uintptr_t>(t.in) & 31) == 0;
+    for (int i = from; i < to; i += kFlush) {
+      const int stop = min(i + kFlush, to);
+      Squares s;
+      s.clear();
+      if (whole && (i + kFlush) * static_cast<long long>(kTile) <= t.cols && stop - i == kFlush)
+        t.in32 ? add_four<true>(t.in + i * (kTile * 4LL), s)
+               : add_four<false>(t.in + i * (kTile * 2LL), s);
+      else
+        for (int k = i; k < stop; ++k) add_tile(t, tile_of(t, k), s);
+      const float v = s.total();
+      if (v >= 1e-30f && v <= 3e38f)
+        d += v;
+      else if (s.any != 0)
+        d += squares_again(t, i, stop);
     }
+    return d;
   }
 }
 
 // Block sum (or maximum) of every thread's part, on thread 0.
 template <bool INF>
-__device__ __forceinline__ double block_total(const Sum<INF>& s, double* shared) {
-  double v = INF ? static_cast<double>(s.top) : s.sum;   // the bits, exact in fp64
+__device__ __forceinline__ double block_total(double v, double* shared) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const double w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -197,7 +316,7 @@ __device__ __forceinline__ int first_tile(int b, int blocks, int tiles) {
 }
 
 template <bool INF, int N>
-__global__ void __launch_bounds__(kThreads) k_grad_partials(const __grid_constant__ List<N> l,
+__global__ void __launch_bounds__(kThreads, kResident) k_grad_partials(const __grid_constant__ List<N> l,
                                                             double* __restrict__ part) {
   __shared__ double shared[kThreads / 32];
   const int begin = first_tile(blockIdx.x, gridDim.x, l.tiles);
@@ -207,10 +326,10 @@ __global__ void __launch_bounds__(kThreads) k_grad_partials(const __grid_constan
     part[blockIdx.x + j - 1] = 0.0;   // the walk came from (block - 1, j - 1)
   for (int i = begin; i < end;) {
     const int stop = j + 1 < l.n ? min(end, l.t[j + 1].first) : end;
-    Sum<INF> s;
-    for (; i < stop; ++i) add_tile(l.t[j], tile_of(l.t[j], i - l.t[j].first), s);
-    const double v = block_total(s, shared);
+    const double v = block_total<INF>(
+        add_tiles<INF>(l.t[j], i - l.t[j].first, stop - l.t[j].first), shared);
     if (threadIdx.x == 0) part[blockIdx.x + j] = v;
+    i = stop;
     ++j;
   }
 }
@@ -219,49 +338,61 @@ __device__ __forceinline__ float norm_of(double v, bool inf) {
   return inf ? __uint_as_float(static_cast<uint32_t>(v)) : static_cast<float>(sqrt(v));
 }
 
-// One block: each tensor's norm from its slots (a warp each), and the total
-// of this launch's slots into sums[at].
-template <bool INF, int N>
-__global__ void __launch_bounds__(1024) k_grad_join(const __grid_constant__ List<N> l, int blocks,
-                                                    const double* __restrict__ part,
-                                                    float* __restrict__ norms,
-                                                    double* __restrict__ sums, int at, bool last,
-                                                    float* __restrict__ norm) {
-  __shared__ double shared[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (norms != nullptr) {
-    for (int j = warp; j < l.n; j += 32) {
-      // blocks whose runs meet tiles first .. next - 1
-      const int first = l.t[j].first, next = j + 1 < l.n ? l.t[j + 1].first : l.tiles;
-      int b = static_cast<int>(static_cast<long long>(first) * blocks / l.tiles);
-      while (first_tile(b + 1, blocks, l.tiles) <= first) ++b;
-      int e = static_cast<int>(static_cast<long long>(next - 1) * blocks / l.tiles);
-      while (first_tile(e + 1, blocks, l.tiles) <= next - 1) ++e;
-      double v = 0.0;
-      for (int i = b + lane; i <= e; i += 32) v = INF ? fmax(v, part[i + j]) : v + part[i + j];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const double w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = INF ? fmax(v, w) : v + w;
-      }
-      if (lane == 0) norms[l.t[j].id] = norm_of(v, INF);
-    }
-  }
-  double v = 0.0;
-  const int slots = l.n > 0 ? blocks + l.n - 1 : 0;
-  for (int i = threadIdx.x; i < slots; i += 1024) v = INF ? fmax(v, part[i]) : v + part[i];
+template <bool INF>
+__device__ __forceinline__ double warp_total(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const double w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
     v = INF ? fmax(v, w) : v + w;
   }
+  return v;
+}
+
+// Block of tile i: the block b with first_tile(b) <= i < first_tile(b + 1).
+__device__ __forceinline__ int block_of(int i, int blocks, int tiles) {
+  int b = static_cast<int>(static_cast<long long>(i) * blocks / tiles);
+  while (first_tile(b + 1, blocks, tiles) <= i) ++b;
+  return b;
+}
+
+// Block 0: the total of this launch's slots into sums[0], added to the launches'
+// before it.  Blocks behind it: tensors' norms, a warp each.  Started while
+// k_grad_partials still runs (programmatic launch), waits for its end.
+template <bool INF, int N>
+__global__ void __launch_bounds__(1024) k_grad_join(const __grid_constant__ List<N> l, int blocks,
+                                                    const double* __restrict__ part,
+                                                    float* __restrict__ norms,
+                                                    double* __restrict__ sums, bool first,
+                                                    bool last, float* __restrict__ norm) {
+  __shared__ double shared[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x > 0) {
+    const int j = (blockIdx.x - 1) * 32 + warp;
+    if (j >= l.n) return;
+    const int next = j + 1 < l.n ? l.t[j + 1].first : l.tiles;
+    const int b = block_of(l.t[j].first, blocks, l.tiles);
+    const int e = block_of(next - 1, blocks, l.tiles);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    double v = 0.0;
+    for (int i = b + lane; i <= e; i += 32) v = INF ? fmax(v, part[i + j]) : v + part[i + j];
+    v = warp_total<INF>(v);
+    if (lane == 0) norms[l.t[j].id] = norm_of(v, INF);
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  double v = 0.0;
+  const int slots = l.n > 0 ? blocks + l.n - 1 : 0;
+  for (int i = threadIdx.x; i < slots; i += 1024) v = INF ? fmax(v, part[i]) : v + part[i];
+  v = warp_total<INF>(v);
   if (lane == 0) shared[warp] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double total = at > 0 ? sums[0] : 0.0;
-    for (int i = 0; i < 32; ++i) total = INF ? fmax(total, shared[i]) : total + shared[i];
-    sums[0] = total;
-    if (last) norm[0] = norm_of(total, INF);
+  if (warp == 0) {
+    v = warp_total<INF>(shared[lane]);
+    if (lane == 0) {
+      if (!first) v = INF ? fmax(sums[0], v) : sums[0] + v;
+      sums[0] = v;
+      if (last) norm[0] = norm_of(v, INF);
+    }
   }
 }
 
@@ -272,41 +403,66 @@ __device__ __forceinline__ void put(char* base, long long i, bool f32, float v) 
     reinterpret_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
 }
 
+// 8 elements, scaled.
+__device__ __forceinline__ void put_eight(char* out, int i, bool out32, const uint32_t (&w)[8],
+                                          bool in32, float scale) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = scale * (in32 ? __uint_as_float(w[e]) : e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]));
+  if (out32)
+    store32(out + i * 4LL, v);
+  else
+    *reinterpret_cast<uint4*>(out + i * 2LL) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+}
+
+template <bool IN32, bool OUT32>
+__device__ __forceinline__ void clip_whole_tile(const char* in, char* out, float scale) {
+  uint32_t w[4][8];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) raw_eight(in, (u * kThreads + threadIdx.x) * 8, IN32, w[u]);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    put_eight(out, (u * kThreads + threadIdx.x) * 8, OUT32, w[u], IN32, scale);
+}
+
+// The blocks take the runs of tiles that they take in k_grad_partials and walk
+// them backwards: what that kernel read last is read first, while L2 has it.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ List<N> l,
-                                                   const float* __restrict__ norm, float max_norm,
-                                                   float eps) {
+__global__ void __launch_bounds__(kThreads, kResident) k_clip(const __grid_constant__ List<N> l,
+                                                              const float* __restrict__ norm,
+                                                              float max_norm, float eps) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // programmatic launch: the norm is there
   float scale = max_norm / (*norm + eps);
   if (scale >= 1.0f) scale = 1.0f;       // a NaN stays
   const int begin = first_tile(blockIdx.x, gridDim.x, l.tiles);
   const int end = first_tile(blockIdx.x + 1, gridDim.x, l.tiles);
-  int j = tensor_of(l, begin);
-  for (int i = begin; i < end; ++i) {
-    while (j + 1 < l.n && l.t[j + 1].first <= i) ++j;
+  int j = tensor_of(l, end - 1);
+  for (int i = end - 1; i >= begin; --i) {
+    while (l.t[j].first > i) --j;
     const Tensor& t = l.t[j];
     if (scale == 1.0f && t.in == t.out) continue;
     const Tile q = tile_of(t, i - t.first);
     const int n = q.rows * q.cols;
     const char* in = t.in + (q.row * t.ld + q.col) * (t.in32 ? 4 : 2);
     char* out = t.out + (q.row * t.ld_out + q.col) * (t.out32 ? 4 : 2);
-    if (one_run(q, t.ld) && one_run(q, t.ld_out) &&
-        ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
-#pragma unroll 4
+    if (wide_run(q, in, t.ld) && wide_run(q, out, t.ld_out)) {
+      if (n == kTile) {
+        if (t.in32)
+          t.out32 ? clip_whole_tile<true, true>(in, out, scale)
+                  : clip_whole_tile<true, false>(in, out, scale);
+        else
+          t.out32 ? clip_whole_tile<false, true>(in, out, scale)
+                  : clip_whole_tile<false, false>(in, out, scale);
+        continue;
+      }
       for (int at = threadIdx.x * 8; at < n; at += kThreads * 8) {
-        float v[8];
         if (at + 8 <= n) {
-          eight(in, at, t.in32, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= scale;
-          if (t.out32) {
-            float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at);
-            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-            to[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + at) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-          }
+          uint32_t w[8];
+          raw_eight(in, at, t.in32, w);
+          put_eight(out, at, t.out32, w, t.in32, scale);
         } else {
           for (int e = 0; at + e < n; ++e)
             put(out, at + e, t.out32, element(in, at + e, t.in32) * scale);
@@ -388,10 +544,13 @@ cudaError_t norm_pass(const moe_grad_t* g, int n, float* norm, float* norms, dou
   do {
     const int start = from;
     from = fill(l, g, from, n);
-    const int blocks = min(l.tiles, min(4 * sms, kMaxBlocks));
+    const int blocks = min(l.tiles, min(kResident * sms, kMaxBlocks));
     if (blocks > 0) k_grad_partials<INF, N><<<blocks, kThreads, 0, s>>>(l, part);
-    k_grad_join<INF, N><<<1, 1024, 0, s>>>(l, blocks, part, norms, ws, start, from >= n, norm);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int joins = norms != nullptr ? 1 + (l.n + 31) / 32 : 1;
+    e = launch_dependent(k_grad_join<INF, N>, joins, 1024, s, l, blocks,
+                         static_cast<const double*>(part), norms, ws, start == 0, from >= n, norm);
     if (e != cudaSuccess) return e;
   } while (from < n);
   return cudaSuccess;
@@ -404,15 +563,16 @@ cudaError_t clip_pass(const moe_grad_t* g, int n, const float* norm, float max_n
   int from = 0;
   do {
     from = fill(l, g, from, n);
-    const int blocks = min(l.tiles, 4 * sms);
-    if (blocks > 0) k_clip<N><<<blocks, kThreads, 0, s>>>(l, norm, max_norm, eps);
-    const cudaError_t e = cudaGetLastError();
+    const int blocks = min(l.tiles, min(kResident * sms, kMaxBlocks));
+    if (blocks == 0) continue;
+    const cudaError_t e = launch_dependent(k_clip<N>, blocks, kThreads, s, l, norm, max_norm, eps);
     if (e != cudaSuccess) return e;
   } while (from < n);
   return cudaSuccess;
 }
 
-constexpr int kSmallList = 56;   // 3.6 KB of parameters
+// Lists of up to so many tensors: 3.6 and 10 KB of parameters.
+constexpr int kSmallList = 56, kMiddleList = 160;
 
 size_t norm_ws_bytes() { return (32 + kMaxBlocks + kMaxList) * sizeof(double); }
 
@@ -456,6 +616,9 @@ moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t n, int32_t norm_type
   if (n <= kSmallList)
     e = inf ? norm_pass<kSmallList, true>(grads, n, norm, norms, w, sms, stream)
             : norm_pass<kSmallList, false>(grads, n, norm, norms, w, sms, stream);
+  else if (n <= kMiddleList)
+    e = inf ? norm_pass<kMiddleList, true>(grads, n, norm, norms, w, sms, stream)
+            : norm_pass<kMiddleList, false>(grads, n, norm, norms, w, sms, stream);
   else
     e = inf ? norm_pass<kMaxList, true>(grads, n, norm, norms, w, sms, stream)
             : norm_pass<kMaxList, false>(grads, n, norm, norms, w, sms, stream);
@@ -477,8 +640,9 @@ moe_status_t moe_clip_grads(const moe_grad_t* grads, int32_t n, const float* nor
   const moe_status_t st = current_device(&sms, &status);
   if (st != MOE_OK) return st;
   const cudaError_t e =
-      n <= kSmallList ? clip_pass<kSmallList>(grads, n, norm, max_norm, eps, sms, stream)
-                      : clip_pass<kMaxList>(grads, n, norm, max_norm, eps, sms, stream);
+      n <= kSmallList    ? clip_pass<kSmallList>(grads, n, norm, max_norm, eps, sms, stream)
+      : n <= kMiddleList ? clip_pass<kMiddleList>(grads, n, norm, max_norm, eps, sms, stream)
+                         : clip_pass<kMaxList>(grads, n, norm, max_norm, eps, sms, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -22,6 +22,23 @@ moe_status_t current_device(int* sms, int** status);
 
 inline int fc1_pad(int F) { return (F + kGluHalf - 1) / kGluHalf * kGluHalf; }
 
+// Launches a kernel that may start while the one before it in the stream
+// still runs, and waits for its end itself (griddepcontrol.wait).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int blocks, int threads, cudaStream_t s,
+                             A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
 // ------------------------------------------------ memory-bound kernels
 cudaError_t launch_topk(const float* logits, const float* bias, int T, int E, int k,
                         int32_t* topk_idx, float* topk_w, int32_t* chunk_counts, int* status,
