@@ -31,4 +31,5 @@ from ._lib import (  # noqa: F401
     moe_unpermute_combine_bwd,
     moe_workspace_size,
 )
+from .block import MoEResidualBlock  # noqa: F401
 from .layer import MoEExpertMLP  # noqa: F401

@@ -140,6 +140,21 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       }
       if constexpr (POST) y.fetch(row_ptr<const TA>(p.y, t), m);
       if (p.dres_in.p != nullptr) dres_in.fetch(row_ptr<const TR>(p.dres_in, t), m);
+      // the next row into L2, a line a thread
+      if (t + step < p.T) {
+        const int at = g.lane * 128;
+        auto line = [&](const BlockRows& r, int size) {
+          if (r.p != nullptr && at < p.d * size)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(r.p + (t + step) * r.ld * size + at));
+        };
+        if constexpr (PRE) {
+          line(p.res, sizeof(TR));
+          line(p.dx, sizeof(TA));
+        }
+        if constexpr (POST) line(p.y, sizeof(TA));
+        line(p.dres_in, sizeof(TR));
+        if (full) line(p.gate_rows, sizeof(TA));
+      }
     }
     const float gt = token ? gate_act(p.gate_act, next_gate) : 1.0f;
     next_gate = token_gate(p, t + step);
