@@ -9,6 +9,8 @@ if libmoe.so is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
@@ -279,6 +281,29 @@ def lib():
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
+_binding = None
+
+
+def binding():
+    """The C module that marshals the smallest calls (csrc/moe_binding.c),
+    set up with the loaded library's functions."""
+    global _binding
+    if _binding is None:
+        L = lib()
+        if not os.path.exists(BINDING_PATH):
+            raise MoeError(f"{BINDING_PATH} is not built; run __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.setup(torch, *[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.moe_block_pre_norm_fwd, L.moe_block_pre_norm_bwd, L.moe_block_post_norm_fwd,
+            L.moe_block_post_norm_bwd, L.moe_grad_norm, L.moe_clip_grads)])
+        _binding = module
+    return _binding
 
 
 def _p(t):
@@ -715,60 +740,8 @@ def moe_fc1_wgrad_tf32(desc, dh_t, x_t, counts, padded_offsets, dw1p, stream=Non
 
 
 # ------------------------------------------------- residual block's norms
-_TORCH = {MOE_DTYPE_BF16: torch.bfloat16, MOE_DTYPE_FP32: torch.float32}
-_NO_ROWS = moe_rows_t(None, 0)
-
-
-def _rows(t, n, d, dtype):
-    """A [n, d] tensor of the given type with unit stride along the channels
-    (any stride between rows) -> moe_rows_t."""
-    if t is None:
-        return _NO_ROWS
-    if t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"expected a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    if t.shape != (n, d):
-        raise ValueError(f"expected a tensor of shape {(n, d)}, got {tuple(t.shape)}")
-    ld, step = t.stride()
-    if (step != 1 and d > 1) or (ld < d and n > 1):
-        raise ValueError(f"rows must be contiguous and apart, got strides {t.stride()}")
-    return moe_rows_t(t.data_ptr(), ld if n > 1 else max(ld, d))
-
-
-def _vector(t, d, dtype):
-    """A contiguous [d] parameter (or its gradient) -> pointer, or None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or not t.is_cuda or t.numel() != d or not t.is_contiguous():
-        raise ValueError(f"expected a contiguous {dtype} CUDA tensor of {d} values, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _block_params(desc, p):
-    """dict of optional tensors {pre_w, pre_b, post_w, post_b, gate} ->
-    moe_block_params_t."""
-    dt, d = _TORCH[desc.param_dtype], desc.d
-    out = moe_block_params_t()
-    for n in ("pre_w", "pre_b", "post_w", "post_b"):
-        t = p.get(n)
-        if t is not None:
-            setattr(out, n, _vector(t, d, dt))
-    g, kind = p.get("gate"), desc.gate
-    if g is not None and kind:
-        if kind == 1:
-            out.gate = moe_rows_t(_vector(g, d, dt), 0)
-        elif kind == 3:
-            out.gate = _rows(g, desc.T, d, _TORCH[desc.dtype])
-        else:
-            if g.dtype is not torch.float32 or not g.is_cuda or g.shape != (desc.T,):
-                raise ValueError(f"expected an fp32 CUDA gate of {desc.T} tokens, got {g.dtype} "
-                                 f"{tuple(g.shape)} on {g.device}")
-            if g.stride(0) < 1 and desc.T > 1:
-                raise ValueError("the tokens' gates must be apart")
-            out.gate = moe_rows_t(g.data_ptr(), max(g.stride(0), 1))
-    return out
-
-
+# Marshalled in C (binding()): tensors are [T,d] with unit stride along the
+# channels and any stride between rows, None where absent.
 def moe_block_norm_workspace_size(desc):
     n = ctypes.c_size_t(0)
     _check(lib().moe_block_norm_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
@@ -777,42 +750,21 @@ def moe_block_norm_workspace_size(desc):
 
 def moe_block_pre_norm_fwd(desc, res, w, b, x, stream=None):
     """x = N1(res)."""
-    T, d, dt = desc.T, desc.d, _TORCH[desc.param_dtype]
-    _check(lib().moe_block_pre_norm_fwd(
-        ctypes.byref(desc), _rows(res, T, d, _TORCH[desc.res_dtype]), _vector(w, d, dt),
-        _vector(b, d, dt), _rows(x, T, d, _TORCH[desc.dtype]), _stream(stream)))
+    _check((_binding or binding()).pre_norm_fwd(desc, res, w, b, x, stream))
 
 
 def moe_block_pre_norm_bwd(desc, dx, res, w, dres_in, dres, dw, db, ws, dres_scale=1.0,
                            stream=None):
     """dres = dres_scale*dres_in + N1^T(dx); dw, db or None."""
-    T, d, dt = desc.T, desc.d, _TORCH[desc.param_dtype]
-    rt = _TORCH[desc.res_dtype]
-    _check(lib().moe_block_pre_norm_bwd(
-        ctypes.byref(desc), _rows(dx, T, d, _TORCH[desc.dtype]), _rows(res, T, d, rt),
-        _vector(w, d, dt), _rows(dres_in, T, d, rt), dres_scale, _rows(dres, T, d, rt),
-        _vector(dw, d, dt), _vector(db, d, dt), _p(ws), ws.numel() * ws.element_size(),
-        _stream(stream)))
+    _check((_binding or binding()).pre_norm_bwd(desc, dx, res, w, dres_in, dres, dw, db, ws,
+                                                dres_scale, stream))
 
 
 def moe_block_post_norm_fwd(desc, res, y, params, res_out, x=None, routed=None, stream=None):
     """res_out = res_scale*res + branch_scale*G*N2(y), x = N1(res_out) or None.
     params: dict {pre_w, pre_b, post_w, post_b, gate}; routed: dict {row_of,
     topk_w, y_out} with y the expert rows [capacity, d]."""
-    T, d = desc.T, desc.d
-    at, rt = _TORCH[desc.dtype], _TORCH[desc.res_dtype]
-    rows = None
-    if routed is not None:
-        r, w = routed["row_of"], routed["topk_w"]
-        if (r.dtype is not torch.int32 or w.dtype is not torch.float32 or r.dim() != 2
-                or r.size(0) != T or r.shape != w.shape):
-            raise ValueError("row_of must be int32 [T,k] and topk_w fp32 [T,k]")
-        rows = ctypes.byref(moe_routed_rows_t(_p(r).value, _p(w).value, r.size(1), y.size(0),
-                                              _rows(routed.get("y_out"), T, d, at)))
-    _check(lib().moe_block_post_norm_fwd(
-        ctypes.byref(desc), _rows(res, T, d, rt), _rows(y, T if rows is None else y.size(0), d, at),
-        ctypes.byref(_block_params(desc, params)), _rows(res_out, T, d, rt), _rows(x, T, d, at),
-        rows, _stream(stream)))
+    _check((_binding or binding()).post_norm_fwd(desc, res, y, params, res_out, x, routed, stream))
 
 
 def moe_block_post_norm_bwd(desc, dres_in, dx, res_out, y, params, dres, dy, grads, ws,
@@ -820,13 +772,8 @@ def moe_block_post_norm_bwd(desc, dres_in, dx, res_out, y, params, dres, dy, gra
     """dres = dres_scale*dres_in + N1^T(dx; res_out) (dx None: without the next
     norm), dy = N2^T(branch_scale*G*dres; y) and the parameters' gradients
     (grads: dict like params, each optional)."""
-    T, d = desc.T, desc.d
-    at, rt = _TORCH[desc.dtype], _TORCH[desc.res_dtype]
-    _check(lib().moe_block_post_norm_bwd(
-        ctypes.byref(desc), _rows(dres_in, T, d, rt), dres_scale, _rows(dx, T, d, at),
-        _rows(res_out, T, d, rt), _rows(y, T, d, at), ctypes.byref(_block_params(desc, params)),
-        _rows(dres, T, d, rt), _rows(dy, T, d, at), ctypes.byref(_block_params(desc, grads)),
-        _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    _check((_binding or binding()).post_norm_bwd(desc, dres_in, dx, res_out, y, params, dres, dy,
+                                                 grads, ws, dres_scale, stream))
 
 
 # ------------------------------------------- gradient norm and clipping
@@ -868,20 +815,12 @@ class GradList:
         if len(self.outs) != len(self.tensors):
             raise ValueError(f"{len(self.tensors)} gradients and {len(self.outs)} outputs")
         self.array = (moe_grad_t * max(len(self.tensors), 1))()
-        self._here = self._there = None
-        self.refresh()
+        self.describe()
 
     def __len__(self):
         return len(self.tensors)
 
-    def refresh(self, outs=True):
-        """Describes the tensors (and, if asked, the outputs) anew where their
-        memory is another than it was."""
-        here = list(map(torch.Tensor.data_ptr, self.tensors))
-        there = (here if self.outs is self.tensors else
-                 list(map(torch.Tensor.data_ptr, self.outs)) if outs else self._there)
-        if here == self._here and there == self._there:
-            return
+    def describe(self):
         kinds = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
         for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
             if t.dtype not in kinds or o.dtype not in kinds or not t.is_cuda or not o.is_cuda:
@@ -891,7 +830,13 @@ class GradList:
                 raise ValueError(f"gradient {i}: shapes {tuple(t.shape)} and {tuple(o.shape)}")
             self.array[i] = moe_grad_t(t.data_ptr(), o.data_ptr(), *_runs(t, o), kinds[t.dtype],
                                        kinds[o.dtype])
-        self._here, self._there = here, there
+
+    def refresh(self, outs=True):
+        """Describes the tensors anew if one (or, if asked, an output) is no
+        longer where it was."""
+        other = None if self.outs is self.tensors or not outs else self.outs
+        if not (_binding or binding()).in_place(self.array, self.tensors, other):
+            self.describe()
 
 
 def _grad_list(grads, outs):
@@ -911,18 +856,12 @@ def moe_grad_norm(grads, norm, norms, norm_type, ws, stream=None):
     """Global norm of a GradList (or a list of tensors) into norm fp32 [1], and
     each tensor's into norms fp32 [n] (or None); norm_type "l2" or "inf"."""
     g = _grad_list(grads, False)
-    if norm.dtype is not torch.float32 or norm.numel() != 1:
-        raise ValueError("norm must be one fp32 value")
-    if norms is not None and (norms.dtype is not torch.float32 or norms.numel() != len(g)):
-        raise ValueError(f"norms must be {len(g)} fp32 values")
-    _check(lib().moe_grad_norm(g.array, len(g), GRAD_NORMS[norm_type], _p(norm), _p(norms), _p(ws),
-                               ws.numel() * ws.element_size(), _stream(stream)))
+    _check((_binding or binding()).grad_norm(g.array, len(g.tensors), GRAD_NORMS[norm_type], norm,
+                                             norms, ws, stream))
 
 
 def moe_clip_grads(grads, norm, max_norm, eps=1e-6, stream=None):
     """outs = grads * min(1, max_norm / (norm + eps)), norm fp32 [1] on the
     device."""
     g = _grad_list(grads, True)
-    if norm.dtype is not torch.float32 or norm.numel() != 1:
-        raise ValueError("norm must be one fp32 value")
-    _check(lib().moe_clip_grads(g.array, len(g), _p(norm), max_norm, eps, _stream(stream)))
+    _check((_binding or binding()).clip_grads(g.array, len(g.tensors), norm, max_norm, eps, stream))

@@ -2,7 +2,8 @@
 
 Each .cu translation unit under csrc/ is compiled in parallel, then linked
 into moe_expert_mlp_gb300/libmoe.so.  No cmake, no torch extension machinery:
-the library is a plain C-ABI shared object.
+the library is a plain C-ABI shared object.  csrc/moe_binding.c, the Python
+binding of the smallest calls, is compiled beside it into _binding.so.
 """
 from __future__ import annotations
 
@@ -11,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -56,6 +59,12 @@ def build_library(verbose: bool = False, ptxas_info: bool = False, force: bool =
         if force or _stale(obj, [src] + headers):
             cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append(cmd)
+    binding = os.path.join(CSRC, "moe_binding.c")
+    if force or _stale(BINDING, [binding, headers[-1]]):
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+        jobs.append([os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-shared", "-fPIC", "-Wall",
+                     "-Wextra", "-I", sysconfig.get_paths()["include"], "-I", cuda, "-I",
+                     os.path.join(ROOT, "include"), binding, "-o", BINDING])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -66,7 +75,7 @@ def build_library(verbose: bool = False, ptxas_info: bool = False, force: bool =
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed for " + cmd[-3])
+                raise RuntimeError("compilation failed for " + cmd[-3])
     if force or jobs or _stale(LIB, objs):
         cmd = [nvcc] + ARCH + ["-shared", "-o", LIB] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)
