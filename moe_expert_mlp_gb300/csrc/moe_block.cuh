@@ -26,7 +26,6 @@ constexpr int kBlockThreads = 512;   // threads of a block at most
 constexpr int kUnit = 8;             // channels of a unit
 constexpr int kBlockMaxD = 16384;    // 512 threads x 4 units
 constexpr int kBlockMaxT = 1 << 30;    // a few steps of the grid past it stay in 32 bits
-constexpr int kFewRows = 2;          // rows an SM up to which a row's latency counts
 
 // Row tensor: element (t, c) at p[t * ld + c].
 struct BlockRows {

@@ -534,11 +534,17 @@ cudaError_t launch_nv(const BlockArgs& a, bool post, cudaStream_t s) {
 
 }  // namespace
 
+// Channels an SM up to which the calls are few rows.  Measured, post norm with
+// the next norm in bf16, one group a row against the ring: 2048 channels, 608
+// tokens 5.6 and 6.8 us, 1216 tokens 8.2 and 7.0; 1024 channels, 608 tokens 3.5
+// and 4.5, 1216 tokens 5.5 and 4.7; 4096 channels, 456 tokens 8.2 and 7.0.
+constexpr long long kFewChannels = 8192;
+
 template <typename TA, typename TR>
 cudaError_t launch_block_fwd_types(BlockArgs a, bool post, int sms, cudaStream_t s) {
   const int units = (a.d + kUnit - 1) / kUnit;
   auto threads = [&](int nv) { return ((units + nv - 1) / nv + 31) / 32 * 32; };
-  if (a.vec && a.T > kFewRows * sms) {
+  if (a.vec && static_cast<long long>(a.T) * a.d > kFewChannels * sms) {
     bool none = false;
     // two units a thread where a row has them, and four where their parameters
     // still fit the registers: more groups, whose sums wait apart

@@ -105,8 +105,8 @@ SHAPES = [dict(T=1, d=64), dict(T=1, d=7168), dict(T=3, d=1), dict(T=5, d=7), di
           dict(T=2, d=16384), dict(T=2, d=16383), dict(T=300, d=256), dict(T=700, d=96),
           dict(T=37, d=520, pitch=8), dict(T=37, d=520, pitch=9, shift=3),
           dict(T=33, d=4096, pitch=24, shift=8), dict(T=1000, d=72),
-          dict(T=700, d=2048), dict(T=320, d=7168), dict(T=310, d=9000), dict(T=340, d=1448, pitch=8),
-          dict(T=600, d=1001)]
+          dict(T=700, d=2048), dict(T=320, d=7168), dict(T=310, d=9000), dict(T=900, d=1448, pitch=8),
+          dict(T=600, d=1001), dict(T=5200, d=256), dict(T=1300, d=1000)]
 KINDS = [dict(), dict(pre="layer", bias=True), dict(types="bf16/fp32/fp32", offset=1.0),
          dict(pre="layer", types="fp32/fp32/fp32"), dict(types="bf16/fp32/bf16", weights=False),
          dict(types="fp32/fp32/bf16", bias=True)]
@@ -194,7 +194,12 @@ def test_post_norm(shape, kind, next_norm):
     (1, dict(T=5, d=64), dict()), (4, dict(T=130, d=2880), dict(gate="channel")),
     (6, dict(T=33, d=2048), dict(post="layer", types="bf16/fp32/fp32", bias=True)),
     (3, dict(T=9, d=77), dict(types="fp32/fp32/fp32")), (32, dict(T=3, d=520, pitch=9, shift=1), dict()),
-    (2, dict(T=4, d=8200), dict(post=None, gate="token", act="sigmoid"))], ids=str)
+    (2, dict(T=4, d=8200), dict(post=None, gate="token", act="sigmoid")),
+    # many rows: the ring, and more expert rows a token than it holds
+    (4, dict(T=700, d=2880), dict()), (1, dict(T=700, d=2048), dict(gate="token", act="tanh")),
+    (8, dict(T=1300, d=1000), dict(types="bf16/fp32/bf16", gate="full", bias=True)),
+    (12, dict(T=400, d=4096), dict()), (2, dict(T=200, d=8200), dict(gate="channel", pre="layer")),
+    (6, dict(T=700, d=2048), dict(types="fp32/fp32/fp32", post="layer"))], ids=str)
 def test_post_norm_on_expert_rows(k, shape, kind):
     """The combined rows, and the same results as combining first; with and
     without the combined rows written."""
