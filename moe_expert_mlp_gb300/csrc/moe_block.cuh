@@ -27,10 +27,12 @@ constexpr int kUnit = 8;             // channels of a unit
 constexpr int kBlockMaxD = 16384;    // 512 threads x 4 units
 constexpr int kBlockMaxT = 1 << 30;    // a few steps of the grid past it stay in 32 bits
 
-// Row tensor: element (t, c) at p[t * ld + c].
+// Row tensor: element (t, c) at p[t * ld + c]; ld16: ld in 16-byte steps (rows
+// of an aligned call).
 struct BlockRows {
   char* p;
   long long ld;
+  uint32_t ld16;
 };
 
 struct BlockNorm {
@@ -222,6 +224,17 @@ __device__ __forceinline__ T* row_ptr(const BlockRows& r, int t) {
   return reinterpret_cast<T*>(r.p) + static_cast<long long>(t) * r.ld;
 }
 
+// A row of an aligned call: one wide multiplication.
+template <typename T>
+__device__ __forceinline__ T* row16(const BlockRows& r, int t) {
+  return reinterpret_cast<T*>(r.p + ((static_cast<uint64_t>(static_cast<uint32_t>(t)) * r.ld16) << 4));
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ T* row_at(const BlockRows& r, int t) {
+  if constexpr (VEC) return row16<T>(r, t);
+  return row_ptr<T>(r, t);
+}
+
 // Gate value and the derivative of its activation.
 __device__ __forceinline__ float gate_act(int act, float g) {
   if (act == MOE_GATE_ACT_SIGMOID) return 1.0f / (1.0f + expf(-g));
@@ -323,9 +336,8 @@ __device__ __forceinline__ void group_sum(Group<NAMED>& g, float (&v)[N]) {
   }
 }
 
-__device__ __forceinline__ void copy16_async(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
-               : "memory");
+__device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -344,23 +356,26 @@ template <typename T, int NV, bool VEC>
 struct RowPart {
   static constexpr int kHalves = sizeof(T) / 2;
   static constexpr int kPieces = VEC ? NV * kHalves : 0;   // kBlockThreads places each
+  static constexpr int kUnitBytes = kHalves * kBlockThreads * 16;
+  static constexpr int kPlaces = kPieces * kBlockThreads;
   Raw<T, VEC> held[VEC ? 1 : NV];
-  uint4* at;
+  uint4* at;     // its places in shared memory
 
   __device__ __forceinline__ void copy(const T* row, const Unit<VEC> (&m)[NV]) {
     if constexpr (VEC) {
       const int l = threadIdx.x & 31;
+      const uint32_t base = smem_u32(at);
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         if constexpr (kHalves == 1) {
-          if (m[u].has(0)) copy16_async(at + u * kBlockThreads + threadIdx.x, row + m[u].c0);
+          if (m[u].has(0)) copy16_async(base + u * kUnitBytes + threadIdx.x * 16, row + m[u].c0);
         } else {
-          uint4* to = at + u * 2 * kBlockThreads + 2 * (threadIdx.x - l);
+          const uint32_t to = base + u * kUnitBytes + (threadIdx.x - l) * 32;
           const int c = m[u].c0 - l * kUnit;               // the warp's first channel
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int q = h * 32 + l;
-            if (c + q * 4 < m[u].d) copy16_async(to + (q ^ ((q >> 3) & 1)), row + c + q * 4);
+            if (c + q * 4 < m[u].d) copy16_async(to + (q ^ ((q >> 3) & 1)) * 16, row + c + q * 4);
           }
         }
       }

@@ -43,14 +43,16 @@ struct Checker {
   BlockRows rows(const moe_rows_t& r, int type, bool required, long long n_rows) {
     if (!r.p) {
       if (required) fail(MOE_ERR_NULL);
-      return {nullptr, 0};
+      return {nullptr, 0, 0};
     }
     const size_t b = type_bytes(type);
     const uintptr_t at = reinterpret_cast<uintptr_t>(r.p);
     if (at % b || r.ld < 0 || (n_rows > 1 && r.ld < d->d)) fail(MOE_ERR_SHAPE);
     const size_t whole = kUnit * b;   // a unit: 16 or 32 bytes
     if (at % whole || (n_rows > 1 && (static_cast<size_t>(r.ld) * b) % whole)) vec = false;
-    return {static_cast<char*>(r.p), static_cast<long long>(r.ld)};
+    const size_t step = n_rows > 1 ? static_cast<size_t>(r.ld) * b / 16 : 0;
+    if (step > UINT32_MAX) vec = false;
+    return {static_cast<char*>(r.p), static_cast<long long>(r.ld), static_cast<uint32_t>(step)};
   }
   BlockRows rows(const moe_rows_t& r, int type, bool required) {
     return rows(r, type, required, d->T);
@@ -72,19 +74,19 @@ struct Checker {
     return n;
   }
   BlockRows gate(const moe_rows_t& r) {
-    if (d->gate == MOE_GATE_NONE) return {nullptr, 0};
+    if (d->gate == MOE_GATE_NONE) return {nullptr, 0, 0};
     if (d->gate == MOE_GATE_FULL) return rows(r, d->dtype, true);
     if (!r.p) {
       fail(MOE_ERR_NULL);
-      return {nullptr, 0};
+      return {nullptr, 0, 0};
     }
-    if (d->gate == MOE_GATE_CHANNEL) return {static_cast<char*>(vector(r.p)), 0};
+    if (d->gate == MOE_GATE_CHANNEL) return {static_cast<char*>(vector(r.p)), 0, 0};
     return token(r);
   }
   BlockRows token(const moe_rows_t& r) {
     if (r.p && (reinterpret_cast<uintptr_t>(r.p) % 4 || r.ld < 0 || (d->T > 1 && r.ld < 1)))
       fail(MOE_ERR_SHAPE);
-    return {static_cast<char*>(r.p), static_cast<long long>(r.ld)};
+    return {static_cast<char*>(r.p), static_cast<long long>(r.ld), 0};
   }
 };
 

@@ -67,12 +67,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     if constexpr (VEC) {
       uint4* at = dyn + slot * kPieces * kBlockThreads;
       dres_in.at = at;
-      at += RowPart<TR, NV, VEC>::kPieces * kBlockThreads;
+      at += RowPart<TR, NV, VEC>::kPlaces;
       if constexpr (PRE) {
         res.at = at;
-        at += RowPart<TR, NV, VEC>::kPieces * kBlockThreads;
+        at += RowPart<TR, NV, VEC>::kPlaces;
         dx.at = at;
-        at += RowPart<TA, NV, VEC>::kPieces * kBlockThreads;
+        at += RowPart<TA, NV, VEC>::kPlaces;
       }
       y.at = at;
     }
@@ -82,11 +82,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       if (t < p.T) {
         place(slot);
         if constexpr (PRE) {
-          res.copy(row_ptr<const TR>(p.res, t), m);
-          dx.copy(row_ptr<const TA>(p.dx, t), m);
+          res.copy(row_at<VEC, const TR>(p.res, t), m);
+          dx.copy(row_at<VEC, const TA>(p.dx, t), m);
         }
-        if constexpr (POST) y.copy(row_ptr<const TA>(p.y, t), m);
-        if (p.dres_in.p != nullptr) dres_in.copy(row_ptr<const TR>(p.dres_in, t), m);
+        if constexpr (POST) y.copy(row_at<VEC, const TA>(p.y, t), m);
+        if (p.dres_in.p != nullptr) dres_in.copy(row_at<VEC, const TR>(p.dres_in, t), m);
       }
       copies_commit();   // one group a row, empty past the end
     }
@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       place(slot);
     } else {
       if constexpr (PRE) {
-        res.fetch(row_ptr<const TR>(p.res, t), m);
-        dx.fetch(row_ptr<const TA>(p.dx, t), m);
+        res.fetch(row_at<VEC, const TR>(p.res, t), m);
+        dx.fetch(row_at<VEC, const TA>(p.dx, t), m);
       }
-      if constexpr (POST) y.fetch(row_ptr<const TA>(p.y, t), m);
-      if (p.dres_in.p != nullptr) dres_in.fetch(row_ptr<const TR>(p.dres_in, t), m);
+      if constexpr (POST) y.fetch(row_at<VEC, const TA>(p.y, t), m);
+      if (p.dres_in.p != nullptr) dres_in.fetch(row_at<VEC, const TR>(p.dres_in, t), m);
       // the next row into L2, a line a thread
       if (t + step < p.T) {
         const int at = g.lane * 128;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
       w2.get(post_weight, u, w);
       if (full) {
         Raw<TA, VEC> r;
-        r.template load<true>(row_ptr<const TA>(p.gate_rows, t), m[u]);
+        r.template load<true>(row_at<VEC, const TA>(p.gate_rows, t), m[u]);
         F2 q[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = r.pair(i);
@@ -283,14 +283,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           const F2 join = PLAIN ? fma2(v, kk1, D[u][i]) : fma2(v, kk1, D[u][i] + kk0);
           D[u][i] = within(m[u], i, fma2(d * w[i], r2, join));
         }
-        if (p.dres.p != nullptr) store_unit(row_ptr<TR>(p.dres, t), m[u], D[u]);
+        if (p.dres.p != nullptr) store_unit(row_at<VEC, TR>(p.dres, t), m[u], D[u]);
       }
     } else {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         if (beyond(m[u])) continue;
         load_D(u, D[u]);
-        if (p.dres.p != nullptr) store_unit(row_ptr<TR>(p.dres, t), m[u], D[u]);
+        if (p.dres.p != nullptr) store_unit(row_at<VEC, TR>(p.dres, t), m[u], D[u]);
       }
     }
 
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         w2.get(post_weight, u, w);
         if (full) {
           Raw<TA, VEC> r;
-          r.template load<true>(row_ptr<const TA>(p.gate_rows, t), m[u]);
+          r.template load<true>(row_at<VEC, const TA>(p.gate_rows, t), m[u]);
           F2 b[4], dg[4];
           load_param(p.post.b, p, m[u], 0.0f, 0.0f, b);
 #pragma unroll
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
                     f2(gate_slope(p.gate_act, g0), gate_slope(p.gate_act, g1));
             D[u][i] = D[u][i] * f2(g0, g1);      // the gate joins the sums
           }
-          if (p.dgate.p != nullptr) store_unit(row_ptr<TA>(p.dgate, t), m[u], dg);
+          if (p.dgate.p != nullptr) store_unit(row_at<VEC, TA>(p.dgate, t), m[u], dg);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           if constexpr (BIAS) acc[kS1 + 1][u][i] = fma2(D[u][i], f2(gt), acc[kS1 + 1][u][i]);
           dy[i] = fma2(D[u][i] * w[i], kk2, PLAIN ? v * kk1 : fma2(v, kk1, kk0));
         }
-        store_unit(row_ptr<TA>(p.dy, t), m[u], dy);
+        store_unit(row_at<VEC, TA>(p.dy, t), m[u], dy);
       }
     }
     __syncwarp();

@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "moe_f2.cuh"
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
@@ -39,6 +41,7 @@ struct Tensor {
 template <int N>
 struct List {
   int n, tiles;      // tensors with elements, their tiles
+  int each, more;    // tiles of a block; the first `more` blocks have one more
   Tensor t[N];
 };
 
@@ -304,23 +307,33 @@ __device__ __forceinline__ double block_total(double v, double* shared) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i)
-      v = INF ? fmax(v, shared[i]) : v + shared[i];
+  if (threadIdx.x >= 32) return 0.0;
+  v = threadIdx.x < kThreads / 32 ? shared[threadIdx.x] : 0.0;
+#pragma unroll
+  for (int o = kThreads / 64; o > 0; o >>= 1) {
+    const double w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = INF ? fmax(v, w) : v + w;
+  }
   return v;
 }
 
-__device__ __forceinline__ int first_tile(int b, int blocks, int tiles) {
-  return static_cast<int>(static_cast<long long>(b) * tiles / blocks);
+// The block's run of tiles, and the block of a tile.
+template <int N>
+__device__ __forceinline__ int first_tile(const List<N>& l, int b) {
+  return b * l.each + min(b, l.more);
+}
+template <int N>
+__device__ __forceinline__ int block_of(const List<N>& l, int i) {
+  const int wide = l.more * (l.each + 1);
+  return i < wide ? i / (l.each + 1) : l.more + (i - wide) / l.each;
 }
 
 template <bool INF, int N>
 __global__ void __launch_bounds__(kThreads, kResident) k_grad_partials(const __grid_constant__ List<N> l,
                                                             double* __restrict__ part) {
   __shared__ double shared[kThreads / 32];
-  const int begin = first_tile(blockIdx.x, gridDim.x, l.tiles);
-  const int end = first_tile(blockIdx.x + 1, gridDim.x, l.tiles);
+  const int begin = first_tile(l, blockIdx.x);
+  const int end = first_tile(l, blockIdx.x + 1);
   int j = tensor_of(l, begin);
   if (threadIdx.x == 0 && blockIdx.x > 0 && j > 0 && l.t[j].first == begin)
     part[blockIdx.x + j - 1] = 0.0;   // the walk came from (block - 1, j - 1)
@@ -348,13 +361,6 @@ __device__ __forceinline__ double warp_total(double v) {
   return v;
 }
 
-// Block of tile i: the block b with first_tile(b) <= i < first_tile(b + 1).
-__device__ __forceinline__ int block_of(int i, int blocks, int tiles) {
-  int b = static_cast<int>(static_cast<long long>(i) * blocks / tiles);
-  while (first_tile(b + 1, blocks, tiles) <= i) ++b;
-  return b;
-}
-
 // Block 0: the total of this launch's slots into sums[0], added to the launches'
 // before it.  Blocks behind it: tensors' norms, a warp each.  Started while
 // k_grad_partials still runs (programmatic launch), waits for its end.
@@ -370,8 +376,7 @@ __global__ void __launch_bounds__(1024) k_grad_join(const __grid_constant__ List
     const int j = (blockIdx.x - 1) * 32 + warp;
     if (j >= l.n) return;
     const int next = j + 1 < l.n ? l.t[j + 1].first : l.tiles;
-    const int b = block_of(l.t[j].first, blocks, l.tiles);
-    const int e = block_of(next - 1, blocks, l.tiles);
+    const int b = block_of(l, l.t[j].first), e = block_of(l, next - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     double v = 0.0;
     for (int i = b + lane; i <= e; i += 32) v = INF ? fmax(v, part[i + j]) : v + part[i + j];
@@ -437,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_clip(const __grid_const
   asm volatile("griddepcontrol.wait;" ::: "memory");   // programmatic launch: the norm is there
   float scale = max_norm / (*norm + eps);
   if (scale >= 1.0f) scale = 1.0f;       // a NaN stays
-  const int begin = first_tile(blockIdx.x, gridDim.x, l.tiles);
-  const int end = first_tile(blockIdx.x + 1, gridDim.x, l.tiles);
+  const int begin = first_tile(l, blockIdx.x);
+  const int end = first_tile(l, blockIdx.x + 1);
   int j = tensor_of(l, end - 1);
   for (int i = end - 1; i >= begin; --i) {
     while (l.t[j].first > i) --j;
@@ -535,6 +540,15 @@ int fill(List<N>& l, const moe_grad_t* g, int from, int n) {
   return i;
 }
 
+// Shares the tiles among the resident blocks; returns their number.
+template <int N>
+int share(List<N>& l, int sms) {
+  const int blocks = std::min(l.tiles, std::min(kResident * sms, kMaxBlocks));
+  l.each = blocks > 0 ? l.tiles / blocks : 0;
+  l.more = blocks > 0 ? l.tiles % blocks : 0;
+  return blocks;
+}
+
 template <int N, bool INF>
 cudaError_t norm_pass(const moe_grad_t* g, int n, float* norm, float* norms, double* ws, int sms,
                       cudaStream_t s) {
@@ -544,7 +558,7 @@ cudaError_t norm_pass(const moe_grad_t* g, int n, float* norm, float* norms, dou
   do {
     const int start = from;
     from = fill(l, g, from, n);
-    const int blocks = min(l.tiles, min(kResident * sms, kMaxBlocks));
+    const int blocks = share(l, sms);
     if (blocks > 0) k_grad_partials<INF, N><<<blocks, kThreads, 0, s>>>(l, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -563,7 +577,7 @@ cudaError_t clip_pass(const moe_grad_t* g, int n, const float* norm, float max_n
   int from = 0;
   do {
     from = fill(l, g, from, n);
-    const int blocks = min(l.tiles, min(kResident * sms, kMaxBlocks));
+    const int blocks = share(l, sms);
     if (blocks == 0) continue;
     const cudaError_t e = launch_dependent(k_clip<N>, blocks, kThreads, s, l, norm, max_norm, eps);
     if (e != cudaSuccess) return e;
