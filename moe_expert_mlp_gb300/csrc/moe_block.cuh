@@ -3,11 +3,10 @@
 // a group of threads, and sums over the group.
 //
 // A row of d channels belongs to a group of `tpr` threads (a multiple of 32),
-// each holding kUnit = 8 channels in each of NV units.  With 16-byte aligned
-// rows a unit is 8 neighbouring channels (one 16-byte access in bf16, two in
-// fp32); otherwise its channels lie tpr apart, so that the warp's single
-// elements are still neighbours.  A block holds several groups when rows are
-// short.
+// each holding kUnit = 8 channels in each of NV units.  With rows aligned to a
+// unit (16 bytes in bf16, 32 in fp32) a unit is 8 neighbouring channels;
+// otherwise its channels lie tpr apart, so that the warp's single elements are
+// still neighbours.  A block holds several groups when rows are short.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -10,7 +10,13 @@
 // Many aligned rows: one block of up to 512 threads an SM (k_block_fwd_ring),
 // whose groups walk down the rows with their parameters in registers, while
 // each thread copies its own 16-byte pieces of the rows to come into its own
-// places of a ring in shared memory (cp.async) and waits for no one else's.
+// places of a ring in shared memory (cp.async) and waits for no one else's (an
+// fp32 warp: for its own threads').  Measured: post norm with the next norm,
+// 16384 x 7168 over an fp32 residual, 224 us = 6.3 TB/s, 93 % of the rate of a
+// copy; on expert rows, 16384 x 2880, k = 4, 136 us = 5.6 TB/s (the ring holds
+// one token's rows there, so a group's loads and sums do not overlap, only the
+// five groups'); pre layer norm, 4096 x 2048, 9.4 us = 3.6 TB/s, of which about
+// 3 us are the first rows' way in and the last ones' out.
 //
 // Few rows, and rows that are not aligned: one group a row (k_block_fwd).  With
 // few rows nothing hides a row's latency, so the group is as large as the row
