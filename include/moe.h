@@ -798,7 +798,7 @@ moe_status_t moe_fc1_wgrad_tf32(const moe_mlp_desc_t* desc, const void* dh_t, co
  * w = NULL: N(v) = xhat (+ b); b = NULL: no bias.  The gate G = act(gate) is
  * 1 (MOE_GATE_NONE), a value per channel, per token, or per element.
  * Everything is computed in fp32 (rows are read once; the squares of |v| up
- * to about 1e18 do not overflow) and rounded once when stored: x' comes from
+ * to about 1e17 do not overflow) and rounded once when stored: x' comes from
  * the unrounded r'.  An Inf or NaN stays within its row (and reaches the
  * parameter gradients).
  *

@@ -222,22 +222,23 @@ def test_post_norm_on_expert_rows(k, shape, kind):
     assert c.m.moe_read_device_status() == 0
 
 
-def test_expert_rows_out_of_range_are_reported_and_zero():
+@pytest.mark.parametrize("T,d", [(6, 256), (1300, 1024)])
+def test_expert_rows_out_of_range_are_reported_and_zero(T, d):
     """A row index outside the buffer is not read: the status word says so, and
     the other tokens are as they should be."""
-    c = Case(T=6, d=256)
-    Y = c.randn(12, c.d).to(c.at).cuda()
-    row_of = torch.arange(12, dtype=torch.int32).view(6, 2).cuda()
-    w = torch.full((6, 2), 0.5, device="cuda")
+    c = Case(T=T, d=d)
+    Y = c.randn(2 * T, d).to(c.at).cuda()
+    row_of = torch.arange(2 * T, dtype=torch.int32).view(T, 2).cuda()
+    w = torch.full((T, 2), 0.5, device="cuda")
     res = c.rows(c.rt)
     good, bad = c.empty(c.rt), c.empty(c.rt)
     c.m.moe_block_post_norm_fwd(c.desc, res, Y, c.p, good, None, dict(row_of=row_of, topk_w=w))
     assert c.m.moe_read_device_status(clear=True) == 0
-    row_of[2, 1], row_of[4, 0] = 12, -1
+    row_of[2, 1], row_of[4, 0] = 2 * T, -1
     c.m.moe_block_post_norm_fwd(c.desc, res, Y, c.p, bad, None, dict(row_of=row_of, topk_w=w))
     torch.cuda.synchronize()
     assert c.m.moe_read_device_status(clear=True) == 0x1
-    rest = [0, 1, 3, 5]
+    rest = [0, 1, 3, *range(5, T)]
     assert torch.equal(good[rest], bad[rest])
     only = 0.5 * f64(Y)[4:5]
     r, mag = B.post_fwd(f64(res)[2:3], only, np.abs(only), c.post, c.q["post_w"], None,
@@ -292,10 +293,14 @@ def test_large_mean_under_a_layer_norm():
     check("x", x, ref, mag, 128)
 
 
-def test_in_place_and_on_another_stream_and_twice():
+@pytest.mark.parametrize("shape", [dict(T=515, d=1024, gate="token", act="sigmoid", bias=True),
+                                   dict(T=1700, d=1024, gate="token"),
+                                   dict(T=700, d=2049, gate="token", types="fp32/fp32/fp32"),
+                                   dict(T=700, d=2048, gate="token", types="bf16/fp32/fp32")], ids=str)
+def test_in_place_and_on_another_stream_and_twice(shape):
     """res_out may be res, dres may be dres_in; on a side stream; equal inputs
     give equal bits."""
-    c = Case(T=515, d=1024, gate="token", act="sigmoid", bias=True)
+    c = Case(**shape)
     res, y, dx, dres_in = c.rows(c.rt), c.rows(c.at), c.rows(c.at), c.rows(c.rt)
     out, x = c.empty(c.rt), c.empty(c.at)
     c.m.moe_block_post_norm_fwd(c.desc, res, y, c.p, out, x)
@@ -303,7 +308,7 @@ def test_in_place_and_on_another_stream_and_twice():
 
     def grads():
         return {n: torch.empty(c.T if n == "gate" else c.d, dtype=torch.float32 if n == "gate" else c.pt,
-                               device="cuda") for n in c.p}
+                               device="cuda") for n, p in c.p.items() if p is not None}
 
     g1, g2 = grads(), grads()
     c.m.moe_block_post_norm_bwd(c.desc, dres_in, dx, out, y, c.p, dres, dy, g1, c.ws, 0.75)
