@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   constexpr int kS1 = PRE ? (BIAS ? 2 : 1) : 0;        // the post norm's first sum
   constexpr bool kHeld = NV == 1 || (NV == 2 && !BIAS);
   constexpr int kPieces = ring_pieces<TA, TR, NV, VEC, PRE, POST>();
+  constexpr bool kPipe = PLAIN && PRE && POST && kPieces * kBlockThreads * 16 * 2 <= kBlockSmem;
   __shared__ float red[kRedFloats];
   extern __shared__ uint4 dyn[];                 // the ring; then the groups' sums
   Group<true> g = make_group<true>(p, red);
@@ -135,11 +136,115 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[a][u][i] = f2(0.0f);
 
+  if constexpr (kPipe) {
+    // Both sides in the plain form: this row's sum over the post norm and the
+    // next row's three sums meet in one, so that a row waits once.
+    float s[4];                                  // post norm's; squares, dxh v, y's squares
+    auto next_sums = [&]() {
+      F2 s1 = f2(0.0f), s2 = s1, s3 = s1;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        const Raw<TR, VEC> a = res.get(u);
+        const Raw<TA, VEC> b = dx.get(u), c = y.get(u);
+        F2 w[4];
+        w1.get(pre_weight, u, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 v = a.pair(i), q = c.pair(i);
+          s1 = fma2(v, v, s1);
+          s2 = fma2(b.pair(i) * w[i], v, s2);
+          s3 = fma2(q, q, s3);
+        }
+      }
+      s[1] = sum(s1), s[2] = sum(s2), s[3] = sum(s3);
+    };
+    float next_gate = token_gate(p, t);
+    int slot = 0;
+    if (t < p.T) {
+      ring_wait(ring);
+      place(0);
+      next_sums();
+      s[0] = 0.0f;
+      group_sum(g, s);
+    }
+    for (; t < p.T; t += step) {
+      const float rstd = rsqrtf(s[1] * inv + p.pre.eps);
+      const float rstd2 = rsqrtf(s[3] * inv + p.post.eps);
+      const float k1 = -(rstd * (s[2] * inv * rstd)) * rstd;
+      const float gt = token ? gate_act(p.gate_act, next_gate) : 1.0f;
+      next_gate = token_gate(p, t + step);
+      place(slot);
+      F2 D[NV][4], e = f2(0.0f);
+      const F2 r2 = f2(rstd), kk1 = f2(k1);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        if (p.dres_in.p != nullptr) {
+          const Raw<TR, VEC> q = dres_in.get(u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[u][i] = f2(p.dres_scale) * q.pair(i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[u][i] = f2(0.0f);
+        }
+        const Raw<TR, VEC> a = res.get(u);
+        const Raw<TA, VEC> b = dx.get(u), c = y.get(u);
+        F2 w[4], ww[4];
+        w1.get(pre_weight, u, w);
+        w2.get(post_weight, u, ww);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 v = a.pair(i), d = b.pair(i);
+          acc[0][u][i] = fma2(d, v * r2, acc[0][u][i]);
+          D[u][i] = fma2(d * w[i], r2, fma2(v, kk1, D[u][i]));
+          e = fma2(D[u][i] * ww[i], c.pair(i), e);
+        }
+        if (p.dres.p != nullptr) store_unit(row_at<VEC, TR>(p.dres, t), m[u], D[u]);
+      }
+      s[0] = sum(e);
+      s[1] = s[2] = s[3] = 0.0f;
+      const int behind = slot + 1 == ring ? 0 : slot + 1;
+      if (t + step < p.T) {
+        ring_wait(ring - 1);
+        slot = behind;
+        place(slot);
+        next_sums();
+        slot = behind == 0 ? ring - 1 : behind - 1;
+      }
+      group_sum(g, s);
+      const float e2 = s[0];
+      if (token && p.dgate.p != nullptr && g.lane == 0)
+        *row_ptr<float>(p.dgate, t) = p.branch_scale * rstd2 * e2 * gate_slope(p.gate_act, gt);
+      const float scale = token ? p.branch_scale * gt : 1.0f;
+      const F2 kk2 = f2(rstd2 * scale), ky = f2(-(rstd2 * (scale * e2 * inv * rstd2)) * rstd2);
+      const F2 rg = f2(rstd2 * gt);              // xhat, with the token's gate
+      place(slot);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        const Raw<TA, VEC> c = y.get(u);
+        F2 w[4], dy[4];
+        w2.get(post_weight, u, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 v = c.pair(i);
+          acc[kS1][u][i] = fma2(D[u][i], v * rg, acc[kS1][u][i]);
+          dy[i] = fma2(D[u][i] * w[i], kk2, v * ky);
+        }
+        store_unit(row_at<VEC, TA>(p.dy, t), m[u], dy);
+      }
+      __syncwarp();
+      copy(t + ring * step, slot);
+      slot = behind;
+    }
+  }
+
   // v - mu of the row's elements
   auto centred = [](F2 v, float mu) { return PLAIN ? v : v + f2(-mu); };
   float next_gate = token_gate(p, t);
   int slot = 0;
-  for (; t < p.T; t += step) {
+  for (; !kPipe && t < p.T; t += step) {
     if constexpr (VEC) {
       ring_wait(ring);
       place(slot);
