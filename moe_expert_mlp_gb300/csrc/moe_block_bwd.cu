@@ -15,7 +15,7 @@ __global__ void __launch_bounds__(1024) k_block_bwd_finish(const __grid_constant
   __shared__ float sums[4][32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   constexpr int kEach = (kBlockBwdMaxParts + 31) / 32;
   for (int a = 0; a < o.acc; ++a) {
     float v[kEach], s = 0.0f;

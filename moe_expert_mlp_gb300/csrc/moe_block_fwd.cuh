@@ -12,8 +12,8 @@
 // each thread copies its own 16-byte pieces of the rows to come into its own
 // places of a ring in shared memory (cp.async) and waits for no one else's (an
 // fp32 warp: for its own threads').  Measured: post norm with the next norm,
-// 16384 x 7168 over an fp32 residual, 224 us = 6.3 TB/s, 93 % of the rate of a
-// copy; on expert rows, 16384 x 2880, k = 4, 136 us = 5.6 TB/s (the ring holds
+// 16384 x 7168 over an fp32 residual, 218 us = 6.5 TB/s, 95 % of the rate of a
+// copy, all in bf16 165 us = 5.7 TB/s; on expert rows, 16384 x 2880, k = 4, 136 us = 5.6 TB/s (the ring holds
 // one token's rows there, so a group's loads and sums do not overlap, only the
 // five groups'); pre layer norm, 4096 x 2048, 9.4 us = 3.6 TB/s, of which about
 // 3 us are the first rows' way in and the last ones' out.
@@ -371,7 +371,76 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
 
   float next_gate = token_gate(p, t);
   int slot = 0;
-  for (; t < p.T; t += step) {
+  constexpr bool kPipe = MODE == kPost && PLAIN;
+  if constexpr (kPipe) {
+    // The squares of this row's r' and of the next row's y meet in one sum, so
+    // that a row waits once.
+    float s[2];                                  // r', y of the row behind
+    auto next_squares = [&]() {
+      F2 a = zero;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        const Raw<TA, true> q = y.get(u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = fma2(q.pair(i), q.pair(i), a);
+      }
+      s[1] = sum(a);
+    };
+    if (t < p.T) {
+      ring_wait(ring);
+      place(0);
+      next_squares();
+      s[0] = 0.0f;
+      group_sum(g, s);
+    }
+    for (; t < p.T; t += step) {
+      const float gt = token ? gate_act(p.gate_act, next_gate) : 1.0f;
+      next_gate = token_gate(p, t + step);
+      place(slot);
+      const float rstd = rsqrtf(s[1] * inv + p.post.eps);
+      const F2 k1 = f2(rstd * (token ? p.branch_scale * gt : 1.0f)), a1 = f2(p.res_scale);
+      F2 sq = zero;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        const Raw<TA, true> q = y.get(u);
+        const Raw<TR, true> r = res.get(u);
+        F2 w[4];
+        w2.get(post_weight, u, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[u][i] = fma2(a1, r.pair(i), q.pair(i) * k1 * w[i]);
+          sq = fma2(v[u][i], v[u][i], sq);
+        }
+        store_unit(row16<TR>(p.res_out, t), m[u], v[u]);
+      }
+      __syncwarp();
+      copy(t + ring * step, slot, next);
+      slot = slot + 1 == ring ? 0 : slot + 1;
+      const bool more = t + step < p.T;
+      s[0] = sum(sq);
+      s[1] = 0.0f;
+      if (more) {
+        ring_wait(ring);
+        place(slot);
+        next_squares();
+      }
+      if (more || p.x.p != nullptr) group_sum(g, s);
+      if (p.x.p == nullptr) continue;
+      const F2 k2 = f2(rsqrtf(s[0] * inv + p.pre.eps));
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        if (beyond(m[u])) continue;
+        F2 w[4], x[4];
+        w1.get(pre_weight, u, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = v[u][i] * k2 * w[i];
+        store_unit(row16<TA>(p.x, t), m[u], x);
+      }
+    }
+  }
+  for (; !kPipe && t < p.T; t += step) {
     const float gt = token ? gate_act(p.gate_act, next_gate) : 1.0f;
     next_gate = token_gate(p, t + step);
     ring_wait(ring);

@@ -56,4 +56,10 @@ __device__ __forceinline__ void store32(void* p, const float (&v)[8]) {
                : "memory");
 }
 
+// Programmatic launch: a kernel that was placed while the one before it in the
+// stream still ran waits for its end.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 }  // namespace moe

@@ -383,14 +383,14 @@ __global__ void __launch_bounds__(1024) k_grad_join(const __grid_constant__ List
     if (j >= l.n) return;
     const int next = j + 1 < l.n ? l.t[j + 1].first : l.tiles;
     const int b = block_of(l, l.t[j].first), e = block_of(l, next - 1);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     double v = 0.0;
     for (int i = b + lane; i <= e; i += 32) v = INF ? fmax(v, part[i + j]) : v + part[i + j];
     v = warp_total<INF>(v);
     if (lane == 0) norms[l.t[j].id] = norm_of(v, INF);
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   double v = 0.0;
   const int slots = l.n > 0 ? blocks + l.n - 1 : 0;
   for (int i = threadIdx.x; i < slots; i += 1024) v = INF ? fmax(v, part[i]) : v + part[i];
@@ -445,7 +445,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kResident) k_clip(const __grid_constant__ List<N> l,
                                                               const float* __restrict__ norm,
                                                               float max_norm, float eps) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // programmatic launch: the norm is there
+  wait_for_previous();                   // programmatic launch: the norm is there
   float scale = max_norm / (*norm + eps);
   if (scale >= 1.0f) scale = 1.0f;       // a NaN stays
   const int begin = first_tile(l, blockIdx.x);
