@@ -490,27 +490,47 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
     slot = slot + 1 == ring ? 0 : slot + 1;
   }
 
-  // the block's sums: its groups one after another
+  // the block's sums: each group's into shared memory where there are several,
+  // then channel by channel in the order of the groups
   if constexpr (VEC) copies_wait<0>();
-  float* join = reinterpret_cast<float*>(dyn);   // [kAcc][d], with several groups
   float* part = p.part + static_cast<long long>(blockIdx.x) * kAcc * p.d;
-  if (groups > 1) __syncthreads();               // the ring is read no more
-  for (int i = 0; i < groups; ++i) {
-    if (i > 0) __syncthreads();
-    if (g.id != i) continue;
-    float* to = i + 1 == groups ? part : join;
+  auto put = [&](float* to) {
 #pragma unroll
     for (int a = 0; a < kAcc; ++a)
 #pragma unroll
-      for (int u = 0; u < NV; ++u)
+      for (int u = 0; u < NV; ++u) {
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (m[u].has(e)) {
-            const int c = m[u].at(e);
-            const float before = i > 0 ? join[a * p.d + c] : 0.0f;
-            const float2 mine = parts(acc[a][u][e / 2]);
-            to[a * p.d + c] = before + (e & 1 ? mine.y : mine.x);
+        for (int i = 0; i < 4; ++i) {
+          const float2 q = parts(acc[a][u][i]);
+          v[2 * i] = q.x, v[2 * i + 1] = q.y;
+        }
+        if constexpr (VEC) {
+          if (m[u].has(0)) {
+            float4* at = reinterpret_cast<float4*>(to + a * p.d + m[u].c0);
+            at[0] = make_float4(v[0], v[1], v[2], v[3]);
+            at[1] = make_float4(v[4], v[5], v[6], v[7]);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (m[u].has(e)) to[a * p.d + m[u].at(e)] = v[e];
+        }
+      }
+  };
+  if (groups == 1) {
+    put(part);
+    return;
+  }
+  float* sums = reinterpret_cast<float*>(dyn);   // [groups][kAcc][d]
+  const int n = kAcc * p.d;
+  __syncthreads();                               // the ring is read no more
+  put(sums + g.id * n);
+  __syncthreads();
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    float v = 0.0f;
+    for (int i = 0; i < groups; ++i) v += sums[i * n + c];
+    part[c] = v;
   }
 }
 
@@ -527,7 +547,7 @@ cudaError_t launch_kernel(const BlockArgs& a, int blocks, int groups, cudaStream
     constexpr int ring = kFit > kRing ? kRing : kFit;
     size_t smem = ring * kRow;
     if (groups > 1) {
-      const size_t join = static_cast<size_t>(kAcc) * a.d * sizeof(float);
+      const size_t join = static_cast<size_t>(groups) * kAcc * a.d * sizeof(float);
       if (join > smem) smem = join;
     }
     auto* k = k_block_bwd<TA, TR, NV, VEC, PRE, POST, BIAS, PLAIN>;
