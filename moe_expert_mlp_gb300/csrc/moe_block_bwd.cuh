@@ -26,12 +26,12 @@
 // 16-byte pieces of the next rows into its own places of a ring in shared
 // memory (cp.async), and waits for no one else's (an fp32 warp: for its own
 // threads').  Measured: pre norm, 16384 x 4096 in bf16, 84 us = 6.4 TB/s, 94 % of
-// the rate of a copy; both norms, 16384 x 7168, 248 us = 5.7 TB/s (84 %), where
+// the rate of a copy; both norms, 16384 x 7168, 246 us = 5.7 TB/s (84 %), where
 // one group of 14 warps has the SM, about 700 instructions a row and warp (two
 // sums a row instead of one that meets the next row's took 270 us; 28 warps of
 // one unit a thread 339 us, as the sums wait for all of them; four units a
 // thread do not fit the registers);
-// post norm with a token gate, 4096 x 2048, 19 us = 2.6 TB/s, a quarter of it
+// post norm with a token gate, 4096 x 2048, 17 us = 3.0 TB/s, a fifth of it
 // the launch of the sums over blocks and most of the rest 27 rows an SM in
 // four groups, one after another.  Rows that are not aligned are read element by
 // element into registers, with the next row called into L2: 1001 x 1441 in fp32,

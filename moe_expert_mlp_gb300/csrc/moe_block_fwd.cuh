@@ -152,8 +152,17 @@ __device__ __forceinline__ void combine_rows(const BlockArgs& p, int t, const Gr
 
 enum FwdMode { kPre, kPost, kRouted };
 
+// Blocks that have to fit an SM.  Rows that are not aligned wait for many small
+// loads: with bf16 branches four blocks of 64 registers hide more of it than two
+// without spills (routed, k = 6, 4096 x 2047: 117 and 174 us; post norm,
+// 929 x 3361: 17 and 22), with fp32 ones and for the pre norm they do not
+// (routed, 4096 x 1441: 82 and 69 us; pre norm, 4096 x 2047: 16.2 and 15.7).
+template <typename TA, int NV, bool VEC, int MODE>
+constexpr int kResidentFwd = !VEC && NV == 2 && MODE != kPre && sizeof(TA) == 2 ? 4 : 1;
+
 template <typename TA, typename TR, int NV, bool VEC, int MODE, bool HOIST>
-__global__ void __launch_bounds__(HOIST ? kBlockThreads : kBlockThreads / 2)
+__global__ void __launch_bounds__(HOIST ? kBlockThreads : kBlockThreads / 2,
+                                  kResidentFwd<TA, NV, VEC, MODE>)
     k_block_fwd(const __grid_constant__ BlockArgs p) {
   __shared__ float red[kRedFloats];
   Group<false> g = make_group<false>(p, red);
