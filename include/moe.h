@@ -860,7 +860,8 @@ typedef struct {
 } moe_routed_rows_t;
 
 /* Bytes of the backward calls' workspace (partial sums of the parameter
- * gradients). */
+ * gradients), 16-byte aligned; its contents need not be set, and calls that may
+ * overlap on the GPU need one each. */
 moe_status_t moe_block_norm_workspace_size(const moe_block_norm_desc_t* desc, size_t* bytes);
 
 /* x = N1(res); uses desc's pre_* fields. */
@@ -916,7 +917,8 @@ typedef struct {
 
 typedef enum { MOE_GRAD_NORM_L2 = 0, MOE_GRAD_NORM_INF = 1 } moe_grad_norm_t;
 
-/* Bytes of moe_grad_norm's workspace for a list of n tensors. */
+/* Bytes of moe_grad_norm's workspace for a list of n tensors, 16-byte aligned,
+ * contents not set; calls that may overlap on the GPU need one each. */
 moe_status_t moe_grad_norm_workspace_size(int32_t n, size_t* bytes);
 
 /* norm[0] (fp32, device) = the list's 2-norm or largest magnitude; norms [n]
