@@ -430,9 +430,7 @@ struct Weights {
 constexpr int kRing = 3;                    // rows of a group in the ring, at most
 constexpr size_t kBlockSmem = 220 * 1024;   // shared memory that the ring may take
 
-// Which of a ring kernel's two forms serves a call: PLAIN for RMS norms
-// without biases and no gate tensor, where the means and what depends on them
-// drop out of the arithmetic at compile time.
+// Waits until the copies of the oldest of `ring` rows under way are there.
 __device__ __forceinline__ void ring_wait(int ring) {
   if (ring >= 3) copies_wait<2>();
   else if (ring == 2) copies_wait<1>();

@@ -562,6 +562,8 @@ cudaError_t launch_kernel(const BlockArgs& a, int blocks, int groups, cudaStream
 template <typename TA, typename TR, int NV, bool VEC, bool PRE, bool POST>
 cudaError_t launch_sides(const BlockArgs& a, const BlockGrads& o, int groups, cudaStream_t s) {
   if constexpr (VEC && NV <= 2) {
+    // the plain form: the means and what depends on them drop out at compile time
+    // (both norms, 16384 x 7168: 272 instead of 383 us)
     const bool plain = !o.bias && (!PRE || a.pre.kind == MOE_NORM_RMS) &&
                        (!POST || (a.post.kind == MOE_NORM_RMS && a.post.b == nullptr &&
                                   a.gate != MOE_GATE_FULL));

@@ -566,6 +566,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
   }
 }
 
+// The plain form (PLAIN): RMS norms without biases and no gate tensor, where the
+// means and what depends on them drop out of the arithmetic at compile time
+// (post norm over an fp32 residual, 16384 x 7168: 286 instead of 303 us).
 bool plain_fwd(const BlockArgs& a, bool post) {
   return a.post.b == nullptr && a.pre.b == nullptr &&
          (a.x.p == nullptr || a.pre.kind == MOE_NORM_RMS) &&
