@@ -821,7 +821,8 @@ typedef struct {
 } moe_rows_t;
 
 typedef struct {
-  int32_t T;            /* tokens, 0..2^30 */
+  int32_t T;            /* tokens, 0..2^30; with none, row tensors and token or
+                           full gates may be NULL */
   int32_t d;            /* channels, 1..16384 */
   int32_t dtype;        /* x, y, full gates: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 */
   int32_t res_dtype;    /* r, r' and their gradients: BF16 or FP32 (FP32 when

@@ -73,10 +73,11 @@ struct Checker {
     n.b = n.kind == MOE_NORM_NONE ? nullptr : vector(b);
     return n;
   }
+  // (without tokens a token or full gate has no values and may be absent)
   BlockRows gate(const moe_rows_t& r) {
     if (d->gate == MOE_GATE_NONE) return {nullptr, 0, 0};
-    if (d->gate == MOE_GATE_FULL) return rows(r, d->dtype, true);
-    if (!r.p) {
+    if (d->gate == MOE_GATE_FULL) return rows(r, d->dtype, d->T > 0);
+    if (!r.p && (d->gate == MOE_GATE_CHANNEL || d->T > 0)) {
       fail(MOE_ERR_NULL);
       return {nullptr, 0, 0};
     }
