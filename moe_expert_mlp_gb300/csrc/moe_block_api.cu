@@ -91,13 +91,14 @@ struct Checker {
   }
 };
 
-void fill(BlockArgs& a, const moe_block_norm_desc_t* d, bool vec) {
+// (the gate is the post norm's: a pre norm's call has no gate to read)
+void fill(BlockArgs& a, const moe_block_norm_desc_t* d, bool vec, bool post) {
   a.T = d->T;
   a.d = d->d;
   a.vec = vec;
   a.p32 = d->param_dtype == MOE_DTYPE_FP32;
-  a.gate = d->gate;
-  a.gate_act = d->gate_act;
+  a.gate = post ? d->gate : MOE_GATE_NONE;
+  a.gate_act = post ? d->gate_act : MOE_GATE_ACT_NONE;
   a.res_scale = d->res_scale;
   a.branch_scale = d->branch_scale;
 }
@@ -126,7 +127,7 @@ moe_status_t run_bwd(const moe_block_norm_desc_t* desc, Checker& c, BlockArgs& a
   int sms;
   const moe_status_t st = current_device(&sms, &a.status);
   if (st != MOE_OK) return st;
-  fill(a, desc, c.vec);
+  fill(a, desc, c.vec, o.post);
   a.part = static_cast<float*>(ws);
   return to_status(launch_block_bwd(a, o, desc->dtype, desc->res_dtype, sms, stream));
 }
@@ -162,7 +163,7 @@ moe_status_t moe_block_pre_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows_
   if (c.st != MOE_OK) return c.st;
   int sms;
   if ((st = current_device(&sms, &a.status)) != MOE_OK) return st;
-  fill(a, desc, c.vec);
+  fill(a, desc, c.vec, false);
   return to_status(launch_fwd(desc, a, false, sms, stream));
 }
 
@@ -200,7 +201,7 @@ moe_status_t moe_block_post_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows
   if (c.st != MOE_OK) return c.st;
   int sms;
   if ((st = current_device(&sms, &a.status)) != MOE_OK) return st;
-  fill(a, desc, c.vec);
+  fill(a, desc, c.vec, true);
   return to_status(launch_fwd(desc, a, true, sms, stream));
 }
 

@@ -21,3 +21,22 @@ def test_no_tokens_with_every_gate(gate):
     c.m.moe_block_post_norm_bwd(c.desc, none, none, none, none, c.p, none, none, grads, c.ws)
     for n, t in grads.items():
         assert torch.count_nonzero(t) == 0, n
+
+
+@pytest.mark.parametrize("gate", ["token", "full"])
+@pytest.mark.parametrize("T,d", [(6, 256), (1300, 1024), (40, 77)])
+def test_pre_norm_under_a_gated_descriptor(gate, T, d):
+    """A block has one descriptor for both norms: the pre norm's calls have no
+    gate, whatever it says of the post norm's."""
+    plain, gated = Case(T=T, d=d, bias=True), Case(T=T, d=d, bias=True, gate=gate, act="sigmoid")
+    res, dx, dres_in = plain.rows(plain.rt, 2.0), plain.rows(plain.at), plain.rows(plain.rt)
+    got = []
+    for c in (plain, gated):
+        x, dres = c.empty(c.at), c.empty(c.rt)
+        dw, db = torch.empty_like(plain.p["pre_w"]), torch.empty_like(plain.p["pre_b"])
+        c.m.moe_block_pre_norm_fwd(c.desc, res, plain.p["pre_w"], plain.p["pre_b"], x)
+        c.m.moe_block_pre_norm_bwd(c.desc, dx, res, plain.p["pre_w"], dres_in, dres, dw, db, c.ws,
+                                   0.75)
+        got.append((x, dres, dw, db))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
