@@ -805,37 +805,42 @@ def _runs(t, out):
 class GradList:
     """Gradient tensors (bf16 or fp32, contiguous or rows at one distance) and
     where their clipped copies go (outs; default: in place), described for
-    moe_grad_norm and moe_clip_grads.  The list holds the tensors; one whose
-    memory was replaced since (`tensor.data = ...`) is described anew at the
-    next call; shapes, strides and types stay as they were."""
+    moe_grad_norm and moe_clip_grads.  The list holds the tensors; one that has
+    other memory, strides, size or type since (`tensor.data = ...`) is described
+    anew at the next call."""
 
     def __init__(self, tensors, outs=None):
         self.tensors = list(tensors)
         self.outs = self.tensors if outs is None else list(outs)
-        if len(self.outs) != len(self.tensors):
-            raise ValueError(f"{len(self.tensors)} gradients and {len(self.outs)} outputs")
-        self.array = (moe_grad_t * max(len(self.tensors), 1))()
         self.describe()
 
     def __len__(self):
         return len(self.tensors)
 
     def describe(self):
+        if len(self.outs) != len(self.tensors):
+            raise ValueError(f"{len(self.tensors)} gradients and {len(self.outs)} outputs")
         kinds = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
+        array = (moe_grad_t * max(len(self.tensors), 1))()
+        layouts = []
         for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
             if t.dtype not in kinds or o.dtype not in kinds or not t.is_cuda or not o.is_cuda:
                 raise ValueError(f"gradient {i}: expected bf16 or fp32 CUDA tensors, got {t.dtype} "
                                  f"on {t.device} and {o.dtype} on {o.device}")
             if t.shape != o.shape:
                 raise ValueError(f"gradient {i}: shapes {tuple(t.shape)} and {tuple(o.shape)}")
-            self.array[i] = moe_grad_t(t.data_ptr(), o.data_ptr(), *_runs(t, o), kinds[t.dtype],
-                                       kinds[o.dtype])
+            array[i] = moe_grad_t(t.data_ptr(), o.data_ptr(), *_runs(t, o), kinds[t.dtype],
+                                  kinds[o.dtype])
+            dense = t.is_contiguous() and o.is_contiguous()
+            layouts.append((None, None) if dense else tuple((tuple(v.shape), v.stride())
+                                                            for v in (t, o)))
+        self.array, self.layouts = array, layouts
 
     def refresh(self, outs=True):
         """Describes the tensors anew if one (or, if asked, an output) is no
-        longer where it was."""
+        longer what it was."""
         other = None if self.outs is self.tensors or not outs else self.outs
-        if not (_binding or binding()).in_place(self.array, self.tensors, other):
+        if not (_binding or binding()).in_place(self.array, self.tensors, other, self.layouts):
             self.describe()
 
 

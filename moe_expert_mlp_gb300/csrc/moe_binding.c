@@ -351,32 +351,69 @@ static int get_grads(PyObject* o, Py_buffer* b, Py_ssize_t n) {
   return -1;
 }
 
-/* array, tensors, outs or None: whether every tensor lies where the array says. */
+/* Whether t is n contiguous elements (layout None), or has the shape and strides
+ * of the layout (a tuple of both); -1 on failure. */
+static int has_layout(PyObject* t, PyObject* layout, long long n) {
+  if (layout == Py_None) {
+    long long have;
+    if (call_long(py.numel, t, &have) < 0) return -1;
+    if (have != n) return 0;
+    PyObject* c = PyObject_Vectorcall(py.is_contiguous, &t, 1, NULL);
+    if (!c) return -1;
+    Py_DECREF(c);
+    return c == Py_True;
+  }
+  PyObject* shape = PyObject_GetAttr(t, py.s_shape);
+  if (!shape) return -1;
+  int same = PyObject_RichCompareBool(shape, PyTuple_GET_ITEM(layout, 0), Py_EQ);
+  Py_DECREF(shape);
+  if (same <= 0) return same;
+  PyObject* strides = PyObject_Vectorcall(py.stride, &t, 1, NULL);
+  if (!strides) return -1;
+  same = PyObject_RichCompareBool(strides, PyTuple_GET_ITEM(layout, 1), Py_EQ);
+  Py_DECREF(strides);
+  return same;
+}
+
+/* Whether t is still the tensor at p of the type and layout; -1 on failure. */
+static int is_still(PyObject* t, const void* p, int type, PyObject* layout, long long n) {
+  void* at;
+  if (address(t, &at) < 0) return -1;
+  if (at != p) return 0;
+  PyObject* dtype = PyObject_GetAttr(t, py.s_dtype);
+  if (!dtype) return -1;
+  const int same = dtype == dtype_of(type);
+  Py_DECREF(dtype);
+  return same ? has_layout(t, layout, n) : 0;
+}
+
+/* array, tensors, outs or None, layouts (pairs of None or (shape, strides), of
+ * the tensor and its out): whether every tensor is what the array says. */
 static PyObject* in_place(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Py_buffer b;
   (void)self;
-  if (want(n, 3) < 0) return NULL;
-  if (!PyList_Check(a[1]) || (a[2] != Py_None && !PyList_Check(a[2]))) {
-    PyErr_SetString(PyExc_TypeError, "expected lists of tensors");
+  if (want(n, 4) < 0) return NULL;
+  if (!PyList_Check(a[1]) || (a[2] != Py_None && !PyList_Check(a[2])) || !PyList_Check(a[3])) {
+    PyErr_SetString(PyExc_TypeError, "expected lists of tensors and layouts");
     return NULL;
   }
   const Py_ssize_t count = PyList_GET_SIZE(a[1]);
   const int outs = a[2] != Py_None;
-  if (outs && PyList_GET_SIZE(a[2]) != count) Py_RETURN_FALSE;
+  if ((outs && PyList_GET_SIZE(a[2]) != count) || PyList_GET_SIZE(a[3]) != count) Py_RETURN_FALSE;
   if (get_grads(a[0], &b, count) < 0) return NULL;
   const moe_grad_t* g = b.buf;
-  int same = 1, failed = 0;
-  for (Py_ssize_t i = 0; i < count && same && !failed; ++i) {
-    void* p;
-    failed = address(PyList_GET_ITEM(a[1], i), &p) < 0;
-    if (!failed) same = p == g[i].grad;
-    if (outs && same && !failed) {
-      failed = address(PyList_GET_ITEM(a[2], i), &p) < 0;
-      if (!failed) same = p == g[i].out;
-    }
+  int same = 1;
+  for (Py_ssize_t i = 0; i < count && same > 0; ++i) {
+    PyObject* pair = PyList_GET_ITEM(a[3], i);
+    const long long elements = (long long)(g[i].rows * g[i].cols);
+    same = is_still(PyList_GET_ITEM(a[1], i), g[i].grad, g[i].dtype, PyTuple_GET_ITEM(pair, 0),
+                    elements);
+    if (outs && same > 0)
+      same = is_still(PyList_GET_ITEM(a[2], i), g[i].out, g[i].out_dtype, PyTuple_GET_ITEM(pair, 1),
+                      elements);
   }
   PyBuffer_Release(&b);
-  if (failed) return NULL;
+  if (same < 0) return NULL;
   return PyBool_FromLong(same);
 }
 

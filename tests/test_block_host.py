@@ -4,6 +4,7 @@ behind them, and what the binding says of a list's tensors."""
 import ctypes
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -43,3 +44,57 @@ def test_no_tokens_need_no_gate_values(m, kind):
 def test_a_channel_gate_is_needed_without_tokens_too(m):
     assert post_bwd(m, 0, "channel", None) == NULL     # its gradient's parameters
     assert post_bwd(m, 0, "channel", AT) == WORKSPACE
+
+
+def described(m, g):
+    """The list's tensors and outs as its array has them."""
+    return [(a.grad, a.out, a.rows, a.cols, a.ld, a.ld_out, a.dtype, a.out_dtype)
+            for a in g.array[:len(g)]]
+
+
+BASE = dict(whole=lambda b: b[:48], shorter=lambda b: b[:20], longer=lambda b: b[:],
+            matrix=lambda b: b[:48].view(6, 8), rows=lambda b: b[:48].view(6, 8)[:, :5],
+            rows_wider_apart=lambda b: b.view(6, 16)[:, :5], columns=lambda b: b[:48].view(6, 8).t(),
+            every_other=lambda b: b[:48:2], other_type=lambda b: b.view(torch.bfloat16)[:48],
+            other_type_as_long=lambda b: b.view(torch.bfloat16)[:96], nothing=lambda b: b[:0])
+
+
+@pytest.mark.parametrize("before", list(BASE))
+@pytest.mark.parametrize("after", list(BASE))
+def test_a_tensor_changed_at_its_address_is_described_anew(m, monkeypatch, before, after):
+    """A list's description is the one that a new list of the same tensors has,
+    also where a tensor, or its out, changed under its address."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)     # described, not run
+    a, b, still = torch.zeros(96), torch.zeros(96), torch.zeros(7)
+    for outs in (False, True):
+        t, o = BASE[before](a), BASE[before](b)
+        g = m.GradList([still, t], [still, o] if outs else None)
+        t.data, o.data = BASE[after](a), BASE[after](b)
+        g.refresh(outs=True)
+        assert described(m, g) == described(m, m.GradList([still, t], [still, o] if outs else None))
+
+
+def test_a_changed_out_is_described_anew_when_it_is_written(m, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    t, wide = torch.zeros(6, 8), torch.zeros(6, 16)
+    o = wide.view(-1)[:48].view(6, 8)
+    g = m.GradList([t], [o])
+    o.data = wide[:, :8]
+    g.refresh(outs=True)
+    assert described(m, g) == described(m, m.GradList([t], [o]))
+    o.data = wide[:3, :8]
+    g.refresh(outs=False)               # the norm reads no out
+    with pytest.raises(ValueError):
+        g.refresh(outs=True)            # another shape
+
+
+def test_a_list_that_grew_is_described_anew(m, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    g = m.GradList([torch.zeros(3)])
+    g.tensors.append(torch.zeros(5))
+    g.refresh()
+    assert [a.cols for a in g.array] == [3, 5]
+    g = m.GradList([torch.zeros(3)], [torch.zeros(3)])
+    g.tensors.append(torch.zeros(5))
+    with pytest.raises(ValueError):
+        g.refresh()

@@ -1,0 +1,37 @@
+"""Lists of gradients on the GPU: what a list measures and writes when its
+tensors change.  Bound of a norm: see test_gpu_grad_clip.py."""
+import pytest
+import torch
+
+from tests.test_gpu_grad_clip import check_clipped, check_norms, measure
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+
+@pytest.mark.parametrize("change", [lambda b: b[:3000], lambda b: b.view(125, 40)[:, :24],
+                                    lambda b: b[:5000:2],
+                                    lambda b: b.view(torch.bfloat16)[:5000]],
+                         ids=["shorter", "rows", "every_other", "other_type"])
+def test_a_tensor_changed_at_its_address(change):
+    """Norm and clip are those of the tensor as it is now; nothing beside it is
+    written."""
+    g = torch.Generator().manual_seed(8)
+    base = torch.randn(5000, generator=g).to(torch.bfloat16).float().cuda()
+    still = torch.randn(300, generator=g).cuda()
+    t = base[:]
+    m, lst, norm, norms = measure([still, t])
+    t.data = change(base)
+    before, inside = [still.clone(), t.clone()], torch.zeros(5000, dtype=torch.bool)
+    view = change(torch.arange(5000, dtype=torch.float32))
+    if view.dtype == torch.float32:
+        inside[view.long().flatten()] = True
+    else:
+        inside[:2500] = True
+    ws = torch.empty(m.moe_grad_norm_workspace_size(2), dtype=torch.uint8, device="cuda")
+    m.moe_grad_norm(lst, norm, norms, "l2", ws)
+    check_norms([still, t], "l2", norm, norms)
+    whole = base.clone()
+    m.moe_clip_grads(lst, norm, 0.5)
+    check_clipped([still, t], before, norm, 0.5)
+    assert torch.equal(base[~inside.cuda()], whole[~inside.cuda()])
