@@ -925,8 +925,10 @@ moe_status_t moe_grad_norm_workspace_size(int32_t n, size_t* bytes);
 /* norm[0] (fp32, device) = the list's 2-norm or largest magnitude; norms [n]
  * (optional): each tensor's.  Squares are summed in fp32 in chains of at most
  * 17 and in fp64 beyond, and again in fp64 where the fp32 sum leaves its
- * range, so any finite gradients have a finite sum; the order is fixed, so
- * equal lists have equal norms.  Inf gives Inf, NaN NaN. */
+ * range, so any finite gradients have a finite sum; the order is fixed by the
+ * list's sizes and strides and by where its tensors lie in 32 bytes, so equal
+ * lists laid out alike have equal norms on one GPU.  out, ld_out and out_dtype
+ * are not read.  Inf gives Inf, NaN NaN. */
 moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t n, int32_t norm_type, float* norm,
                            float* norms, void* ws, size_t ws_bytes, cudaStream_t stream);
 

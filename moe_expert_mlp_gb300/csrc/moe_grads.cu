@@ -10,7 +10,8 @@
 // partial sums are one for each tensor it meets: (block, tensor) pairs walk a
 // staircase, pair (b, j) writes slot b + j, and a slot the walk jumps over is
 // zeroed by the block behind it.  A second kernel adds the slots in order.
-// Nothing is added by atomics: equal gradients give equal bits.
+// Nothing is added by atomics: equal gradients, laid out alike and starting alike
+// to 32 bytes, give equal bits on one GPU.
 //
 // Measured on 554 M bf16 gradients (64 experts of 2048 x 1408): norm 174 us =
 // 6.4 TB/s (94 % of the rate of a copy), clipped into fp32 530 us = 6.3 TB/s;
@@ -439,8 +440,9 @@ __device__ __forceinline__ void clip_whole_tile(const char* in, char* out, float
     put_eight(out, (u * kThreads + threadIdx.x) * 8, OUT32, w[u], IN32, scale);
 }
 
-// The blocks take the runs of tiles that they take in k_grad_partials and walk
-// them backwards: what that kernel read last is read first, while L2 has it.
+// The blocks take the runs of tiles that they take in k_grad_partials (other ones
+// where a contiguous gradient's out is not contiguous) and walk them backwards:
+// what that kernel read last is read first, while L2 has it.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kResident) k_clip(const __grid_constant__ List<N> l,
                                                               const float* __restrict__ norm,
@@ -510,16 +512,17 @@ moe_status_t check_grad(const moe_grad_t& g, bool clip) {
 }
 
 // Appends tensors from the list's place `from`; returns the place behind the
-// last one taken (the list is full, or its tiles would pass 32 bits).
+// last one taken (the list is full, or its tiles would pass 32 bits).  Without
+// `clip` nothing is asked of the outs, which the caller may not have set.
 template <int N>
-int fill(List<N>& l, const moe_grad_t* g, int from, int n) {
+int fill(List<N>& l, const moe_grad_t* g, int from, int n, bool clip) {
   l.n = 0;
   long long tiles = 0;
   int i = from;
   for (; i < n && l.n < N; ++i) {
     moe_grad_t q = g[i];
     if (q.rows == 0 || q.cols == 0) continue;
-    const bool packed = q.rows == 1 || (q.ld == q.cols && (q.out == nullptr || q.ld_out == q.cols));
+    const bool packed = q.rows == 1 || (q.ld == q.cols && (!clip || q.ld_out == q.cols));
     if (packed) {
       q.cols *= q.rows;
       q.rows = 1;
@@ -531,7 +534,7 @@ int fill(List<N>& l, const moe_grad_t* g, int from, int n) {
     if (tiles + count > 0x7FFFFFFFLL / 2) break;
     Tensor& t = l.t[l.n++];
     t.in = static_cast<const char*>(q.grad);
-    t.out = static_cast<char*>(q.out);
+    t.out = clip ? static_cast<char*>(q.out) : nullptr;
     t.rows = q.rows;
     t.cols = q.cols;
     t.ld = q.ld;
@@ -563,7 +566,7 @@ cudaError_t norm_pass(const moe_grad_t* g, int n, float* norm, float* norms, dou
   int from = 0;
   do {
     const int start = from;
-    from = fill(l, g, from, n);
+    from = fill(l, g, from, n, false);
     const int blocks = share(l, sms);
     if (blocks > 0) k_grad_partials<INF, N><<<blocks, kThreads, 0, s>>>(l, part);
     cudaError_t e = cudaGetLastError();
@@ -582,7 +585,7 @@ cudaError_t clip_pass(const moe_grad_t* g, int n, const float* norm, float max_n
   List<N> l;
   int from = 0;
   do {
-    from = fill(l, g, from, n);
+    from = fill(l, g, from, n, true);
     const int blocks = share(l, sms);
     if (blocks == 0) continue;
     const cudaError_t e = launch_dependent(k_clip<N>, blocks, kThreads, s, l, norm, max_norm, eps);

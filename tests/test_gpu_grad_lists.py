@@ -35,3 +35,24 @@ def test_a_tensor_changed_at_its_address(change):
     m.moe_clip_grads(lst, norm, 0.5)
     check_clipped([still, t], before, norm, 0.5)
     assert torch.equal(base[~inside.cuda()], whole[~inside.cuda()])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norms_do_not_depend_on_where_the_clipped_go(dtype):
+    """The same gradients have the same bits of norm in place, with outs in
+    wider buffers, and with a description whose out was never set."""
+    g = torch.Generator().manual_seed(9)
+    t = [torch.randn(400, 300, generator=g).to(dtype).cuda() for _ in range(40)]
+    _, lst, norm, norms = measure(t)
+    wide = [torch.empty(400, 308, device="cuda")[:, :300] for _ in t]
+    m, _, norm2, norms2 = measure(t, "l2", wide)
+    assert torch.equal(norm, norm2) and torch.equal(norms, norms2)
+    ws = torch.empty(m.moe_grad_norm_workspace_size(len(t)), dtype=torch.uint8, device="cuda")
+    for a in lst.array:
+        a.rows, a.cols, a.ld = 400, 300, 300
+    for out, ld_out, kind in ((None, 0, 0), (1 << 20, 12345, 77)):
+        for a in lst.array:
+            a.out, a.ld_out, a.out_dtype = out, ld_out, kind
+        norm2, norms2 = torch.empty_like(norm), torch.empty_like(norms)
+        m._lib.binding().grad_norm(lst.array, len(t), 0, norm2, norms2, ws, None)
+        assert torch.equal(norm, norm2) and torch.equal(norms, norms2)
