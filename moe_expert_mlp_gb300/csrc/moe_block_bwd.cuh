@@ -480,7 +480,16 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
           const F2 v = a.pair(i);                // D is 0 past the row's end
           acc[kS1][u][i] = fma2(D[u][i], PLAIN ? v * r2 : fma2(v, r2, c2), acc[kS1][u][i]);
           if constexpr (BIAS) acc[kS1 + 1][u][i] = fma2(D[u][i], f2(gt), acc[kS1 + 1][u][i]);
-          dy[i] = fma2(D[u][i] * w[i], kk2, PLAIN ? v * kk1 : fma2(v, kk1, kk0));
+        }
+        if (normed) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const F2 v = a.pair(i);
+            dy[i] = fma2(D[u][i] * w[i], kk2, PLAIN ? v * kk1 : fma2(v, kk1, kk0));
+          }
+        } else {   // y has no part in dy, not even 0 times an Inf
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dy[i] = D[u][i] * w[i] * kk2;
         }
         store_unit(row_at<VEC, TA>(p.dy, t), m[u], dy);
       }

@@ -40,3 +40,24 @@ def test_pre_norm_under_a_gated_descriptor(gate, T, d):
         got.append((x, dres, dw, db))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("gate", [None, "channel", "token", "full"])
+@pytest.mark.parametrize("shape", [dict(T=40, d=264), dict(T=1300, d=1024), dict(T=40, d=77)], ids=str)
+@pytest.mark.parametrize("next_norm", [True, False])
+def test_without_a_post_norm_dy_does_not_depend_on_y(gate, shape, next_norm):
+    """dy = b G D: what y holds, an Inf or NaN too, has no part in it."""
+    c = Case(**shape, post=None, gate=gate, act="tanh" if gate else None)
+    y, r, dres_in = c.rows(c.at), c.rows(c.rt), c.rows(c.rt)
+    dx = c.rows(c.at) if next_norm else None
+
+    def backward():
+        dres, dy = c.empty(c.rt), c.empty(c.at)
+        c.m.moe_block_post_norm_bwd(c.desc, dres_in, dx, r if next_norm else None, y, c.p, dres, dy,
+                                    {}, c.ws, 0.75)
+        return dres, dy
+
+    clean = backward()
+    y[3, 5], y[9, 0], y[20, c.d - 1], y[39] = float("inf"), float("-inf"), float("nan"), 1e30
+    for a, b in zip(clean, backward()):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
