@@ -13,6 +13,7 @@ import importlib.machinery
 import importlib.util
 import math
 import os
+import sysconfig
 
 import torch
 
@@ -283,7 +284,8 @@ def lib():
     return _lib
 
 
-BINDING_PATH = os.path.join(_HERE, "_binding.so")
+# the file is named for the Python that it was compiled for
+BINDING_PATH = os.path.join(_HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 _binding = None
 
 

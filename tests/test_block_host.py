@@ -1,7 +1,9 @@
 """Host side of the residual block's norms and of the gradient lists, without a
 GPU: calls whose arguments are in order reach the check of the workspace
-behind them, and what the binding says of a list's tensors."""
+behind them, what the binding says of a list's tensors, and how it is built."""
 import ctypes
+import os
+import sysconfig
 
 import pytest
 import torch
@@ -98,3 +100,32 @@ def test_a_list_that_grew_is_described_anew(m, monkeypatch):
     g.tensors.append(torch.zeros(5))
     with pytest.raises(ValueError):
         g.refresh()
+
+
+@pytest.mark.parametrize("compiler", ["false", "/nowhere/cc"])
+def test_the_library_stands_without_the_binding(m, monkeypatch, tmp_path, capfd, compiler):
+    """Where the binding cannot be compiled (no Python headers, no C compiler)
+    the library still builds; the calls that need the binding raise, and an
+    outdated one is not left to be loaded."""
+    from moe_expert_mlp_gb300 import build
+    L = m._lib
+    at = tmp_path / "_binding.so"
+    at.write_bytes(b"of another header")
+    os.utime(at, (0, 0))
+    monkeypatch.setattr(build, "BINDING", str(at))
+    monkeypatch.setattr(L, "BINDING_PATH", str(at))
+    monkeypatch.setattr(L, "_binding", None)
+    monkeypatch.setenv("CC", compiler)
+    assert build.build_library() == build.LIB
+    assert "binding is not built" in capfd.readouterr().err
+    assert list(tmp_path.iterdir()) == []
+    with pytest.raises(m.MoeError):
+        m.moe_block_pre_norm_fwd(m.make_block_norm_desc(4, 64), None, None, None, None)
+    assert m.moe_fc1_padded_width(2880) == 2944            # the others do not need it
+
+
+def test_the_binding_is_named_for_its_python(m):
+    from moe_expert_mlp_gb300 import build
+    assert build.BINDING == m._lib.BINDING_PATH
+    assert build.BINDING.endswith("_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+    assert m._lib.binding().__file__ == build.BINDING
