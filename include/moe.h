@@ -805,7 +805,9 @@ moe_status_t moe_fc1_wgrad_tf32(const moe_mlp_desc_t* desc, const void* dh_t, co
  * Row tensors are moe_rows_t: element (t, c) at p[t*ld + c], ld >= d in
  * elements, any element alignment.  With d a multiple of 8 and every row
  * aligned to 8 elements (16 bytes in bf16, 32 in fp32) the kernels move 8
- * elements at a time, otherwise single ones. */
+ * elements at a time, otherwise single ones; above 8192 channels single ones
+ * too in the forward of few rows (and of expert rows whose token does not fit
+ * the kernel's shared memory) and in the fp32 backward of both norms. */
 typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind_t;
 typedef enum {
   MOE_GATE_NONE = 0,
@@ -894,7 +896,8 @@ moe_status_t moe_block_post_norm_fwd(const moe_block_norm_desc_t* desc, moe_rows
  *   dy = N2^T(branch_scale * G (*) D; y)
  * dres (optional): D, the gradient of res_out; the gradient of res itself is
  * res_scale*D, which the pre norm's backward applies as its dres_scale.
- * grads: the parameters' gradients over the T rows (written, not added to).
+ * grads: the parameters' gradients over the T rows (written, not added to);
+ * pre_w and pre_b are the next norm's, written where dx is given, or T is 0.
  * At least one of dres_in, dx is given; dres may be dres_in. */
 moe_status_t moe_block_post_norm_bwd(const moe_block_norm_desc_t* desc, moe_rows_t dres_in,
                                      float dres_scale, moe_rows_t dx, moe_rows_t res_out,

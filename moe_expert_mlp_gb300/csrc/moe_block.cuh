@@ -1,5 +1,5 @@
 // Device functions shared by the forward and backward kernels of the residual
-// block's norms (moe_block_fwd.cu, moe_block_bwd.cu): how a row is spread over
+// block's norms (moe_block_fwd.cuh, moe_block_bwd.cuh): how a row is spread over
 // a group of threads, and sums over the group.
 //
 // A row of d channels belongs to a group of `tpr` threads (a multiple of 32),

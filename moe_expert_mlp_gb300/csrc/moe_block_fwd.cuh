@@ -16,9 +16,13 @@
 // copy, all in bf16 165 us = 5.7 TB/s; on expert rows, 16384 x 2880, k = 4, 136 us = 5.6 TB/s (the ring holds
 // one token's rows there, so a group's loads and sums do not overlap, only the
 // five groups'); pre layer norm, 4096 x 2048, 9.4 us = 3.6 TB/s, of which about
-// 3 us are the first rows' way in and the last ones' out.
+// 3 us are the first rows' way in and the last ones' out; RMS, 16384 x 4096,
+// 48 us = 5.5 TB/s.  The general form takes two or three sums a row one after
+// another: both layer norms with biases and a channel gate, 16384 x 7168, 234 us
+// = 4.0 TB/s; with a gate tensor, read past the ring, 395 us = 3.0 TB/s.
 //
-// Few rows, and rows that are not aligned: one group a row (k_block_fwd).  With
+// Few rows, rows that are not aligned, and tokens whose expert rows do not fit
+// the ring: one group a row (k_block_fwd).  With
 // few rows nothing hides a row's latency, so the group is as large as the row
 // allows and the parameters are fetched together with the row instead of after
 // its sums.
@@ -637,7 +641,11 @@ cudaError_t launch_block_fwd_types(BlockArgs a, bool post, int sms, cudaStream_t
   if (a.vec && static_cast<long long>(a.T) * a.d > kFewChannels * sms) {
     bool none = false;
     // two units a thread where a row has them, and four where their parameters
-    // still fit the registers: more groups, whose sums wait apart
+    // still fit the registers: more groups, whose sums wait apart.  k is not
+    // looked at, and four units halve the expert rows that the ring can take: 5
+    // a token in bf16, 4 over an fp32 residual, 2 in fp32 (two units: 12, 11, 5).
+    // Beyond that the few rows' kernel takes the call: 4096 x 2048, k = 6, 62 us
+    // in the plain form without the ring, 41 us in the general one with it
     const bool four = units > 2 * kBlockThreads || (units > 128 && plain_fwd(a, post));
     const int nv = units <= 32 ? 1 : four ? 4 : 2;
     a.tpr = threads(nv);

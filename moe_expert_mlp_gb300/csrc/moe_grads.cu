@@ -16,7 +16,7 @@
 // Measured on 554 M bf16 gradients (64 experts of 2048 x 1408): norm 174 us =
 // 6.4 TB/s (94 % of the rate of a copy), clipped into fp32 530 us = 6.3 TB/s;
 // one call after the other 701 us, 93 % of the rate over the bytes of both
-// passes.  Small lists wait for their launches and last tiles: 84 fp32 tensors,
+// passes.  The largest magnitude of the same list 163 us, its floor.  Small lists wait for their launches and last tiles: 84 fp32 tensors,
 // 151 MB, 83 us for both, 81 % over the bytes of both passes.
 #include <cuda_bf16.h>
 #include <math.h>

@@ -1,5 +1,7 @@
 """Lists of gradients on the GPU: what a list measures and writes when its
-tensors change.  Bound of a norm: see test_gpu_grad_clip.py."""
+tensors change.  Bound of a norm: chains of at most 17 squares and three joins in
+fp32 before fp64 are 21 roundings of the sum, 11.5 * 2^-24 of its root; the checks
+of test_gpu_grad_clip.py allow 18."""
 import pytest
 import torch
 
