@@ -937,7 +937,9 @@ moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t n, int32_t norm_type
 
 /* out = grad * min(1, max_norm / (norm[0] + eps)) for every tensor, norm read
  * on the device.  A NaN norm gives NaN, an Inf norm a factor of 0.  Tensors
- * clipped in place are not touched where the factor is 1. */
+ * clipped in place are not touched where the factor is 1.  An out shares no
+ * memory with another out or another tensor's grad: a tensor listed twice and
+ * clipped in place would be scaled once or twice, element by element. */
 moe_status_t moe_clip_grads(const moe_grad_t* grads, int32_t n, const float* norm, float max_norm,
                             float eps, cudaStream_t stream);
 

@@ -837,6 +837,12 @@ class GradList:
             layouts.append((None, None) if dense else tuple((tuple(v.shape), v.stride())
                                                             for v in (t, o)))
         self.array, self.layouts = array, layouts
+        # two gradients clipped into the same memory, if there are any: blocks
+        # would write it side by side (the norm may read one twice)
+        seen, self.shared = {}, None
+        for i, o in enumerate(self.outs):
+            if o.numel() and seen.setdefault(o.data_ptr(), i) != i:
+                self.shared = (seen[o.data_ptr()], i)
 
     def refresh(self, outs=True):
         """Describes the tensors anew if one (or, if asked, an output) is no
@@ -871,4 +877,6 @@ def moe_clip_grads(grads, norm, max_norm, eps=1e-6, stream=None):
     """outs = grads * min(1, max_norm / (norm + eps)), norm fp32 [1] on the
     device."""
     g = _grad_list(grads, True)
+    if g.shared:
+        raise ValueError("gradients {} and {} are clipped into the same memory".format(*g.shared))
     _check((_binding or binding()).clip_grads(g.array, len(g.tensors), norm, max_norm, eps, stream))

@@ -129,3 +129,22 @@ def test_the_binding_is_named_for_its_python(m):
     assert build.BINDING == m._lib.BINDING_PATH
     assert build.BINDING.endswith("_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
     assert m._lib.binding().__file__ == build.BINDING
+
+
+def test_two_gradients_are_not_clipped_into_the_same_memory(m, monkeypatch):
+    """A gradient listed twice (a tied weight's) would be scaled by two blocks at
+    once: refused before anything is enqueued.  Its norm may be taken."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    a, b, out = torch.zeros(3), torch.zeros(3), torch.zeros(3)
+    norm = torch.zeros(1)
+    for lst in ([a, b, a], m.GradList([a, b, a]), m.GradList([a, b], [out, out])):
+        with pytest.raises(ValueError, match="same memory"):
+            m.moe_clip_grads(lst, norm, 1.0)
+    wide = torch.zeros(4, 8)
+    for fine in (m.GradList([a, a], [b, out]), m.GradList([wide[:, :4], wide[:, 4:]]),
+                 m.GradList([a[:0], a[:0], a])):
+        assert fine.shared is None
+    g = m.GradList([a, b])
+    b.data = a                          # tied since
+    with pytest.raises(ValueError, match="same memory"):
+        m.moe_clip_grads(g, norm, 1.0)
