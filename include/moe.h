@@ -943,6 +943,111 @@ moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t n, int32_t norm_type
 moe_status_t moe_clip_grads(const moe_grad_t* grads, int32_t n, const float* norm, float max_norm,
                             float eps, cudaStream_t stream);
 
+/* ------------------------------------------------------- router's losses
+ * What keeps a router's experts evenly used and its logits small, with their
+ * gradient.  The pages name the router and its top-k ([FK] "Overcoming
+ * training bottlenecks in the MoE block") but print none of these formulas:
+ * with p = softmax(logits[t]) over all E experts, sequences s of N_s counted
+ * tokens, N of them in all, and c[s,e] (token, slot) pairs on expert e,
+ *   f[s,e] = E c[s,e] / (k N_s)      P[s,e] = 1/N_s sum_t p[t,e]
+ *   balance = sum_s N_s/N sum_e f[s,e] P[s,e]          (1 where all is even)
+ *   z       = 1/N sum_t logsumexp(logits[t])^2
+ *   loss    = balance_coef*balance + z_coef*z
+ * and, f held fixed as it is not differentiable,
+ *   dlogits[t,e] = dloss/N * p[t,e] * (balance_coef*(f[s,e] - sum_j f[s,j] p[t,j])
+ *                                      + 2*z_coef*logsumexp(logits[t])).
+ * Sequence s holds the tokens seq_offsets[s] .. seq_offsets[s+1]-1 (int32
+ * [S+1], ascending within [0,T]; NULL with one sequence: all T); tokens outside
+ * every sequence and those whose mask byte is 0 (mask [T], NULL: none) count
+ * nowhere and get no gradient from the losses.  A token without a logit above
+ * -inf has p = 0 and adds nothing to either loss.  An empty sequence has P = 0;
+ * without counted tokens the losses are 0.  NaN and +Inf logits reach the
+ * losses, P of their sequence and their token's gradient.  Sums over tokens are
+ * fp32 within a block and added in one order, those over the batch fp64: equal
+ * inputs give equal results on one GPU. */
+typedef struct {
+  int32_t T;          /* tokens, 0..2^28 */
+  int32_t E;          /* experts, 1..256 */
+  int32_t k;          /* experts per token, 1..min(E,32) */
+  int32_t sequences;  /* S, 1..65535 */
+  float balance_coef, z_coef;
+} moe_router_loss_desc_t;
+
+/* Bytes of the forward's workspace, 16-byte aligned; its contents need not be
+ * set, and calls that may overlap on the GPU need one each. */
+moe_status_t moe_router_loss_workspace_size(const moe_router_loss_desc_t* desc, size_t* bytes);
+
+/* logits fp32 [T,E] and topk_idx i32 [T,k] as moe_route_permute reads and writes
+ * them -> counts i32 [S,E] (c), tokens i32 [S+1] (N_s, then N), probs fp32
+ * [S,E] (P), loss fp32 [3]: loss, balance, z.  An expert outside [0,E) sets
+ * MOE_DEV_BAD_EXPERT and is not counted; offsets that do not ascend within [0,T]
+ * set MOE_DEV_BAD_OFFSETS, with unspecified results. */
+moe_status_t moe_router_loss_fwd(const moe_router_loss_desc_t* desc, const float* logits,
+                                 const int32_t* topk_idx, const uint8_t* mask,
+                                 const int32_t* seq_offsets, int32_t* counts, int32_t* tokens,
+                                 float* probs, float* loss, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream);
+
+/* dlogits fp32 [T,E] (written, all T rows) = the losses' gradient, dloss fp32
+ * [1] on the device (NULL: 1) the gradient of loss[0]; and where dw is not NULL
+ * joined to moe_route_bwd's, in the same pass:
+ *   + [e = idx[t,i]] w[t,i] (dw[t,i] - sum_j w[t,j] dw[t,j])
+ * for every token, counted or not; an expert outside [0,E) sets
+ * MOE_DEV_BAD_EXPERT and gets nothing.  counts and tokens as the forward wrote them
+ * (or summed over the ranks that share a batch, N with them).  dlogits shares no
+ * memory with an input. */
+moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float* logits,
+                                 const uint8_t* mask, const int32_t* seq_offsets,
+                                 const int32_t* counts, const int32_t* tokens, const float* dloss,
+                                 const float* dw, const float* topk_w, const int32_t* topk_idx,
+                                 float* dlogits, cudaStream_t stream);
+
+/* ------------------------------------------------- orthogonalised updates
+ * The direction in which a weight matrix is moved, made of its gradient by
+ * Newton-Schulz steps, which bring all its singular values near one (the pages
+ * have no counterpart):
+ *   m' = momentum*m + (1-dampening)*g          (without a momentum: U = g)
+ *   U  = m', or with nesterov (1-dampening)*g + momentum*m'
+ *   X  = U / (|U|_F + eps);  `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X
+ *   out = scale * X
+ * for each of `batch` matrices of rows x cols.  The products run on the tensor
+ * cores with fp16 operands and fp32 accumulation, the state X is kept in 32 bits
+ * and out rounded once to bf16.  Up to eight of the default steps the 2-norm of
+ * out's error is below 1e-2 of out's (5 steps on matrices with sides of 64 and
+ * more: below 5e-3, rounding included).  (a, b, c) with which a singular value in
+ * [0,1] could reach 2 within the steps, or |b| s^2 + |c| s^4 could pass 16, are
+ * refused with MOE_ERR_UNSUPPORTED.  A zero matrix stays zero; an Inf or NaN
+ * reaches its own matrix only. */
+typedef struct {
+  void* p;        /* element (i, r, c) at p[i*plane + r*ld + c]; inputs are not written */
+  int64_t ld;     /* elements from one row to the next */
+  int64_t plane;  /* from one matrix to the next */
+} moe_matrices_t;
+
+typedef struct {
+  int32_t batch;       /* matrices, 0..65535 */
+  int32_t rows, cols;  /* 1..16384 each */
+  int32_t grad_dtype;  /* g: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 */
+  int32_t steps;       /* 1..16 */
+  int32_t nesterov;
+  float a, b, c;
+  float eps;           /* > 0 */
+  float momentum, dampening;
+  float scale;
+} moe_orthogonalize_desc_t;
+
+/* Bytes of the workspace, 256-byte aligned; its contents need not be set, and
+ * calls that may overlap on the GPU need one each. */
+moe_status_t moe_orthogonalize_workspace_size(const moe_orthogonalize_desc_t* desc, size_t* bytes);
+
+/* grad (grad_dtype), mom and mom_out (fp32; all NULL with momentum 0: no
+ * momentum is kept) -> out (bf16).  Any strides with ld >= cols and, of what is
+ * written, matrices apart.  mom_out may be mom, and out may be grad of the same
+ * strides; otherwise a written tensor shares no memory with another. */
+moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrices_t grad,
+                               moe_matrices_t mom, moe_matrices_t mom_out, moe_matrices_t out,
+                               void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* moe_route_permute for callers that cannot allocate device memory (for
  * example a host program whose device memory is all handed to its own fixed
  * pool, or a runtime that allows no allocation after start-up).  The pages

@@ -51,6 +51,8 @@ EXPORTS = (
     "moe_fc1_wgrad_tf32", "moe_selftest_grid_wait_timeout", "moe_block_norm_workspace_size",
     "moe_block_pre_norm_fwd", "moe_block_pre_norm_bwd", "moe_block_post_norm_fwd",
     "moe_block_post_norm_bwd", "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_clip_grads",
+    "moe_router_loss_workspace_size", "moe_router_loss_fwd", "moe_router_loss_bwd",
+    "moe_orthogonalize_workspace_size", "moe_orthogonalize",
 )
 
 NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
@@ -113,6 +115,22 @@ class moe_routed_rows_t(ctypes.Structure):
                 ("capacity", ctypes.c_int32), ("y_out", moe_rows_t)]
 
 
+class moe_router_loss_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "sequences")]
+    _fields_ += [(n, ctypes.c_float) for n in ("balance_coef", "z_coef")]
+
+
+class moe_matrices_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("ld", ctypes.c_int64), ("plane", ctypes.c_int64)]
+
+
+class moe_orthogonalize_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "rows", "cols", "grad_dtype", "steps", "nesterov")]
+    _fields_ += [(n, ctypes.c_float) for n in
+                 ("a", "b", "c", "eps", "momentum", "dampening", "scale")]
+
+
 class moe_grad_t(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("ld_out", ctypes.c_int64),
@@ -171,6 +189,22 @@ def make_block_norm_desc(T, d, dtype="bf16", res_dtype=None, param_dtype=None, p
         T, d, dt[dtype], dt[res_dtype or dtype], dt[param_dtype or dtype], NORMS[pre_norm],
         NORMS[post_norm], GATES[gate], GATE_ACTS[gate_act], pre_eps, post_eps, pre_offset,
         post_offset, res_scale, branch_scale)
+
+
+def make_router_loss_desc(T, E, k, sequences=1, balance_coef=1e-2, z_coef=0.0):
+    """Descriptor of the router's losses (see include/moe.h) over T tokens in
+    `sequences` sequences."""
+    return moe_router_loss_desc_t(T, E, k, sequences, balance_coef, z_coef)
+
+
+def make_orthogonalize_desc(batch, rows, cols, grad_dtype="bf16", steps=5,
+                            coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, momentum=0.0,
+                            dampening=0.0, nesterov=False, scale=1.0):
+    """Descriptor of orthogonalised updates (see include/moe.h) of `batch`
+    matrices; grad_dtype "bf16" or "fp32"."""
+    dt = {"bf16": MOE_DTYPE_BF16, "fp32": MOE_DTYPE_FP32}[grad_dtype]
+    return moe_orthogonalize_desc_t(batch, rows, cols, dt, steps, int(bool(nesterov)),
+                                    *coefficients, eps, momentum, dampening, scale)
 
 
 _lib = None
@@ -275,6 +309,13 @@ def lib():
                                              ctypes.c_size_t, P]),
             "moe_clip_grads": (ctypes.c_int, [P, ctypes.c_int32, P, ctypes.c_float,
                                               ctypes.c_float, P]),
+            "moe_router_loss_workspace_size": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_router_loss_fwd": (ctypes.c_int, [P] * 10 + [ctypes.c_size_t, P]),
+            "moe_router_loss_bwd": (ctypes.c_int, [P] * 12),
+            "moe_orthogonalize_workspace_size": (ctypes.c_int,
+                                                 [P, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_orthogonalize": (ctypes.c_int, [P] + [moe_matrices_t] * 4 +
+                                  [P, ctypes.c_size_t, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -880,3 +921,111 @@ def moe_clip_grads(grads, norm, max_norm, eps=1e-6, stream=None):
     if g.shared:
         raise ValueError("gradients {} and {} are clipped into the same memory".format(*g.shared))
     _check((_binding or binding()).clip_grads(g.array, len(g.tensors), norm, max_norm, eps, stream))
+
+
+# ------------------------------------------------------- router's losses
+def _array(t, shape, dtype, name):
+    """Address of a contiguous tensor of the shape and type on the current
+    device; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor of shape {shape}, got "
+                         f"{t.dtype} of shape {tuple(t.shape)} on {t.device}")
+    _on_device(t, name)
+    return t.data_ptr()
+
+
+def _on_device(t, name):
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"{torch.cuda.current_device()}")
+
+
+def _mask(mask, T):
+    if mask is not None and mask.dtype is torch.uint8:
+        return _array(mask, (T,), torch.uint8, "mask")
+    return _array(mask, (T,), torch.bool, "mask")
+
+
+def _workspace(ws):
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous CUDA tensor")
+    _on_device(ws, "ws")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_router_loss_workspace_size(desc):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_router_loss_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_router_loss_fwd(desc, logits, topk_idx, mask, seq_offsets, counts, tokens, probs, loss, ws,
+                        stream=None):
+    """counts, tokens, probs and loss (fp32 [3]: loss, balance, z) of a batch's
+    routing; mask (bool or uint8 [T]) and seq_offsets (int32 [S+1]) or None."""
+    T, E, k, S = desc.T, desc.E, desc.k, desc.sequences
+    f32, i32 = torch.float32, torch.int32
+    _check(lib().moe_router_loss_fwd(
+        ctypes.byref(desc), _array(logits, (T, E), f32, "logits"),
+        _array(topk_idx, (T, k), i32, "topk_idx"), _mask(mask, T),
+        _array(seq_offsets, (S + 1,), i32, "seq_offsets"), _array(counts, (S, E), i32, "counts"),
+        _array(tokens, (S + 1,), i32, "tokens"), _array(probs, (S, E), f32, "probs"),
+        _array(loss, (3,), f32, "loss"), *_workspace(ws), _stream(stream)))
+
+
+def moe_router_loss_bwd(desc, logits, mask, seq_offsets, counts, tokens, dloss, routed, dlogits,
+                        stream=None):
+    """dlogits = the losses' gradient (dloss fp32 [1] or None: 1), joined to that
+    of the selected weights where routed is a dict {dw, topk_w, topk_idx}."""
+    T, E, k, S = desc.T, desc.E, desc.k, desc.sequences
+    f32, i32 = torch.float32, torch.int32
+    dw = w = idx = None
+    if routed is not None:
+        dw = _array(routed["dw"], (T, k), f32, "dw")
+        w = _array(routed["topk_w"], (T, k), f32, "topk_w")
+        idx = _array(routed["topk_idx"], (T, k), i32, "topk_idx")
+    _check(lib().moe_router_loss_bwd(
+        ctypes.byref(desc), _array(logits, (T, E), f32, "logits"), _mask(mask, T),
+        _array(seq_offsets, (S + 1,), i32, "seq_offsets"), _array(counts, (S, E), i32, "counts"),
+        _array(tokens, (S + 1,), i32, "tokens"), _array(dloss, (1,), f32, "dloss"), dw, w, idx,
+        _array(dlogits, (T, E), f32, "dlogits"), _stream(stream)))
+
+
+# ------------------------------------------------- orthogonalised updates
+def moe_orthogonalize_workspace_size(desc):
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_orthogonalize_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _matrices(t, desc, dtype, name):
+    """[batch, rows, cols] (or one [rows, cols]) with unit stride along a row."""
+    if t is None:
+        return moe_matrices_t(None, 0, 0)
+    shape = (desc.batch, desc.rows, desc.cols)
+    if t.dtype is not dtype or not t.is_cuda or (
+            tuple(t.shape) != shape and (desc.batch != 1 or tuple(t.shape) != shape[1:])):
+        raise ValueError(f"{name}: expected a {dtype} CUDA tensor of shape {shape}, got {t.dtype} "
+                         f"of shape {tuple(t.shape)} on {t.device}")
+    _on_device(t, name)
+    if desc.cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: rows must have unit stride, got strides {t.stride()}")
+    # (strides along a dimension of one are whatever torch left there)
+    ld = t.stride(-2) if desc.rows > 1 else desc.cols
+    plane = t.stride(0) if desc.batch > 1 else ld * desc.rows
+    return moe_matrices_t(t.data_ptr(), ld, plane)
+
+
+def moe_orthogonalize(desc, grad, out, ws, mom=None, mom_out=None, stream=None):
+    """out (bf16) = scale times the orthogonalised update of each matrix of grad;
+    mom, mom_out (fp32): the momentum before and after (mom_out None: in place)."""
+    if mom is not None and mom_out is None:
+        mom_out = mom
+    g = torch.float32 if desc.grad_dtype == MOE_DTYPE_FP32 else torch.bfloat16
+    _check(lib().moe_orthogonalize(
+        ctypes.byref(desc), _matrices(grad, desc, g, "grad"),
+        _matrices(mom, desc, torch.float32, "mom"),
+        _matrices(mom_out, desc, torch.float32, "mom_out"),
+        _matrices(out, desc, torch.bfloat16, "out"), *_workspace(ws), _stream(stream)))

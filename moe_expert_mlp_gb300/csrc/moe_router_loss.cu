@@ -1,0 +1,581 @@
+// The router's losses and their gradient (see include/moe.h for the formulas).
+//
+// Both passes are one read of the logits: a token's row lies in the registers
+// of a group of 8 or 32 lanes, whose shuffles give its maximum, its sum of
+// exponentials and, in the backward, <f, p>.  What they cannot do without is
+// that read (and the backward's write); the arithmetic, one exponential an
+// element, is below it.
+//
+// Forward: the tokens are cut into chunks of equal length, one block each, and
+// a chunk at the ends of sequences into segments.  Chunks and sequences both
+// ascend, so the segment of chunk c and sequence s has the number c + s to
+// itself.  A block writes its segments' sums of p, counts and squares; a second
+// launch adds the segments of a sequence up in ascending order, so the result
+// does not depend on the order in which blocks ran.
+#include <math.h>
+
+#include "moe_internal.h"
+#include "moe_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kLossThreads = 256;
+constexpr int kLossMaxLanes = 32;
+
+struct LossArgs {
+  const float* logits;
+  const int32_t* topk_idx;
+  const uint8_t* mask;         // [T] or null: every token counts
+  const int32_t* seq_offsets;  // [S+1] or null: one sequence of all tokens
+  int32_t* counts;             // [S,E]
+  int32_t* tokens;             // [S+1]
+  float* probs;                // [S,E]
+  float* loss;                 // [3]
+  const float* dloss;          // backward: null = 1
+  const float* dw;             // backward: null = no share of the weights
+  const float* topk_w;
+  float* dlogits;
+  // workspace: per segment, and per (sequence, 32 experts)
+  float* seg_p;                // [segments, E]
+  int32_t* seg_count;          // [segments, E]
+  float* seg_z;                // [segments]
+  int32_t* seg_tokens;         // [segments]
+  double* term;                // [S, e_blocks]: N_s * sum f P over 32 experts
+  unsigned int* done;
+  int* status;
+  int T, E, k, S, chunk, chunks;
+  float balance, z;
+};
+
+// Element j, i of a lane's share of a row: VEC consecutive experts at a time.
+template <int LANES, int VEC>
+__device__ __forceinline__ int expert_of(int lane, int j) {
+  return (j * LANES + lane) * VEC;
+}
+
+// Softmax of one row over the group's lanes, in place: x becomes p.  Returns
+// logsumexp.  A row without a logit above -inf has p = 0 and gives 0.
+template <int LANES, int N>
+__device__ __forceinline__ float row_softmax(float (&x)[N], uint32_t group_mask) {
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = x[i] > top || x[i] != x[i] ? x[i] : top;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    const float other = __shfl_xor_sync(group_mask, top, o);
+    top = other > top || other != other ? other : top;
+  }
+  if (top == -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = 0.0f;
+    return 0.0f;
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = expf(x[i] - top);
+    sum += x[i];
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group_mask, sum, o);
+  const float inv = 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] *= inv;
+  return top + logf(sum);
+}
+
+// A lane's share of a row of floats; `fill` past the experts.
+template <int LANES, int N, int VEC>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float fill,
+                                         float (&x)[N]) {
+#pragma unroll
+  for (int j = 0; j < N / VEC; ++j) {
+    const int e = expert_of<LANES, VEC>(lane, j);
+    if constexpr (VEC == 4) {
+      const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
+                             : make_float4(fill, fill, fill, fill);
+      x[4 * j] = v.x;
+      x[4 * j + 1] = v.y;
+      x[4 * j + 2] = v.z;
+      x[4 * j + 3] = v.w;
+    } else {
+      x[j] = e < E ? __ldg(row + e) : fill;
+    }
+  }
+}
+
+// First sequence whose end lies behind token t (S when none does).
+__device__ __forceinline__ int sequence_of(const LossArgs& a, int t) {
+  if (a.seq_offsets == nullptr) return t < a.T ? 0 : a.S;
+  int lo = 0, hi = a.S;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.seq_offsets + mid + 1) > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void sequence_span(const LossArgs& a, int s, int* begin, int* end) {
+  if (a.seq_offsets == nullptr) {
+    *begin = 0;
+    *end = a.T;
+    return;
+  }
+  *begin = max(__ldg(a.seq_offsets + s), 0);
+  *end = min(__ldg(a.seq_offsets + s + 1), a.T);
+}
+
+template <int LANES, int N, int VEC>
+__global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) {
+  constexpr int kGroups = kLossThreads / LANES;
+  __shared__ float s_p[kGroups * LANES * N];   // a row of each group
+  __shared__ int s_count[kMaxExperts];
+  __shared__ float s_z[kGroups];
+  __shared__ int s_n[kGroups];
+  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+  const uint32_t group_mask =
+      LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+  const int c = blockIdx.x;
+  const int t0 = c * a.chunk, t1 = min(t0 + a.chunk, a.T);
+  if (c == 0 && threadIdx.x == 0) *a.done = 0;
+  for (int s = sequence_of(a, t0); s < a.S; ++s) {
+    int begin, end;
+    sequence_span(a, s, &begin, &end);
+    if (begin >= t1) break;
+    begin = max(begin, t0);
+    end = min(end, t1);
+    if (begin >= end) continue;
+    for (int e = threadIdx.x; e < a.E; e += kLossThreads) s_count[e] = 0;
+    float acc[N], z = 0.0f;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    for (int t = begin + group; t < end; t += kGroups) {
+      if (a.mask != nullptr && a.mask[t] == 0) continue;
+      float x[N];
+      load_row<LANES, N, VEC>(a.logits + static_cast<long long>(t) * a.E, a.E, lane, -INFINITY, x);
+      const float lse = row_softmax<LANES, N>(x, group_mask);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += x[i];
+      z += lse * lse;
+      ++n;
+    }
+#pragma unroll
+    for (int j = 0; j < N / VEC; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        s_p[group * (LANES * N) + expert_of<LANES, VEC>(lane, j) + i] = acc[j * VEC + i];
+    if (lane == 0) {
+      s_z[group] = z;
+      s_n[group] = n;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < (end - begin) * a.k; i += kLossThreads) {
+      const int t = begin + i / a.k;
+      if (a.mask != nullptr && a.mask[t] == 0) continue;
+      const int e = __ldg(a.topk_idx + static_cast<long long>(begin) * a.k + i);
+      if (e < 0 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
+      else atomicAdd(&s_count[e], 1);
+    }
+    __syncthreads();
+    const long long seg = static_cast<long long>(c) + s;
+    for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
+      float p = 0.0f;
+      for (int g = 0; g < kGroups; ++g) p += s_p[g * (LANES * N) + e];
+      a.seg_p[seg * a.E + e] = p;
+      a.seg_count[seg * a.E + e] = s_count[e];
+    }
+    if (threadIdx.x == 0) {
+      float zz = 0.0f;
+      int nn = 0;
+      for (int g = 0; g < kGroups; ++g) {
+        zz += s_z[g];
+        nn += s_n[g];
+      }
+      a.seg_z[seg] = zz;
+      a.seg_tokens[seg] = nn;
+    }
+    __syncthreads();
+  }
+}
+
+// One block: 32 experts of one sequence, its segments over 32 warps.  The last
+// block to end joins the sequences' terms.
+__global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
+  __shared__ float s_p[32][33];
+  __shared__ int s_c[32][33];
+  __shared__ int s_n[32];
+  __shared__ bool s_last;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  int begin, end;
+  sequence_span(a, s, &begin, &end);
+  const int c0 = begin / a.chunk, c1 = end > begin ? (end - 1) / a.chunk + 1 : c0;
+  float p = 0.0f;
+  int count = 0, n = 0;
+  for (int c = c0 + warp; c < c1; c += 32) {
+    const long long seg = static_cast<long long>(c) + s;
+    if (e < a.E) {
+      p += a.seg_p[seg * a.E + e];
+      count += a.seg_count[seg * a.E + e];
+    }
+    n += a.seg_tokens[seg];
+  }
+  s_p[warp][lane] = p;
+  s_c[warp][lane] = count;
+  if (lane == 0) s_n[warp] = n;
+  __syncthreads();
+  if (warp == 0) {
+    p = 0.0f;
+    count = 0;
+    for (int w = 0; w < 32; ++w) {
+      p += s_p[w][lane];
+      count += s_c[w][lane];
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, s_n[lane]);
+    // N_s * f * P = E / k * count * (sum of p) / N_s
+    const float mean = n > 0 ? p / static_cast<float>(n) : 0.0f;
+    float term = static_cast<float>(count) * mean;
+    if (e < a.E) {
+      a.probs[static_cast<long long>(s) * a.E + e] = mean;
+      a.counts[static_cast<long long>(s) * a.E + e] = count;
+    }
+    double sum = e < a.E ? term : 0.0;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) {
+      a.term[static_cast<long long>(s) * gridDim.x + blockIdx.x] = sum;
+      if (blockIdx.x == 0) a.tokens[s] = n;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // the whole batch: terms and tokens of the sequences, squares of the segments
+  __shared__ double s_t[32], s_zz[32];
+  __shared__ long long s_m[32];
+  double t = 0.0, z = 0.0;
+  long long m = 0;
+  bool bad = false;
+  for (int i = threadIdx.x; i < a.S; i += 1024) {
+    for (int b = 0; b < static_cast<int>(gridDim.x); ++b)
+      t += __ldcg(a.term + static_cast<long long>(i) * gridDim.x + b);
+    m += __ldcg(a.tokens + i);
+    if (a.seq_offsets != nullptr) {
+      const int lo = a.seq_offsets[i], hi = a.seq_offsets[i + 1];
+      bad = bad || lo < 0 || hi < lo || hi > a.T;
+    }
+  }
+  if (bad) set_status(a.status, MOE_DEV_BAD_OFFSETS);
+  for (int c = threadIdx.x; c < a.chunks; c += 1024) {
+    const int t0 = c * a.chunk, t1 = min(t0 + a.chunk, a.T);
+    for (int q = sequence_of(a, t0); q < a.S; ++q) {
+      sequence_span(a, q, &begin, &end);
+      if (begin >= t1) break;
+      if (max(begin, t0) < min(end, t1)) z += a.seg_z[static_cast<long long>(c) + q];
+    }
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+    m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
+  }
+  if (lane == 0) {
+    s_t[warp] = t;
+    s_zz[warp] = z;
+    s_m[warp] = m;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    t = z = 0.0;
+    m = 0;
+    for (int w = 0; w < 32; ++w) {
+      t += s_t[w];
+      z += s_zz[w];
+      m += s_m[w];
+    }
+    const double total = m > 0 ? static_cast<double>(m) : 1.0;
+    const double balance = t * a.E / a.k / total;
+    z /= total;
+    a.loss[0] = static_cast<float>(a.balance * balance + a.z * z);
+    a.loss[1] = static_cast<float>(balance);
+    a.loss[2] = static_cast<float>(z);
+    a.tokens[a.S] = static_cast<int>(m);
+  }
+}
+
+// One group of lanes a token.  f is taken around its mean 1 over the experts,
+// which changes nothing in f - <f, p> but keeps the difference of near equals
+// exact.
+template <int LANES, int N, int VEC>
+__global__ void __launch_bounds__(kLossThreads) k_loss_bwd(const LossArgs a) {
+  constexpr int kGroups = kLossThreads / LANES;
+  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+  const uint32_t group_mask =
+      LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+  const int t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
+  const int total = __ldg(a.tokens + a.S);
+  const float scale = (a.dloss != nullptr ? __ldg(a.dloss) : 1.0f) /
+                      static_cast<float>(total > 0 ? total : 1);
+  int have = -1;               // the sequence whose f lies in the registers
+  float f[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = 0.0f;
+  for (int t = t0 + group; t < t1; t += kGroups) {
+    float x[N];
+    load_row<LANES, N, VEC>(a.logits + static_cast<long long>(t) * a.E, a.E, lane, -INFINITY, x);
+    const int s = sequence_of(a, t);
+    bool live = s < a.S && (a.mask == nullptr || a.mask[t] != 0);
+    if (live && a.seq_offsets != nullptr) live = t >= __ldg(a.seq_offsets + s);
+    if (live && s != have) {
+      const int n = __ldg(a.tokens + s);
+      const float per = static_cast<float>(a.E) / (static_cast<float>(a.k) * (n > 0 ? n : 1));
+#pragma unroll
+      for (int j = 0; j < N / VEC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const int e = expert_of<LANES, VEC>(lane, j) + i;
+          f[j * VEC + i] =
+              e < a.E ? __ldg(a.counts + static_cast<long long>(s) * a.E + e) * per - 1.0f : 0.0f;
+        }
+      have = s;
+    }
+    if (live) {
+      const float lse = row_softmax<LANES, N>(x, group_mask);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) dot += f[i] * x[i];
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(group_mask, dot, o);
+      const float zz = 2.0f * a.z * lse;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = scale * x[i] * (a.balance * (f[i] - dot) + zz);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = 0.0f;
+    }
+    if (a.dw != nullptr) {
+      const long long at = static_cast<long long>(t) * a.k;
+      float dot = 0.0f;
+      for (int i = lane; i < a.k; i += LANES) dot += __ldg(a.topk_w + at + i) * __ldg(a.dw + at + i);
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(group_mask, dot, o);
+      for (int i = 0; i < a.k; ++i) {
+        const int e = __ldg(a.topk_idx + at + i);
+        const float v = __ldg(a.topk_w + at + i) * (__ldg(a.dw + at + i) - dot);
+        if (lane == 0 && (e < 0 || e >= a.E)) set_status(a.status, MOE_DEV_BAD_EXPERT);
+#pragma unroll
+        for (int j = 0; j < N / VEC; ++j)
+#pragma unroll
+          for (int q = 0; q < VEC; ++q)
+            if (expert_of<LANES, VEC>(lane, j) + q == e) x[j * VEC + q] += v;
+      }
+    }
+    float* out = a.dlogits + static_cast<long long>(t) * a.E;
+#pragma unroll
+    for (int j = 0; j < N / VEC; ++j) {
+      const int e = expert_of<LANES, VEC>(lane, j);
+      if (e >= a.E) continue;
+      if constexpr (VEC == 4)
+        *reinterpret_cast<float4*>(out + e) =
+            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      else
+        out[e] = x[j];
+    }
+  }
+}
+
+// Calls f with the lanes a token, values a lane and vector width for E.
+template <typename F>
+cudaError_t with_shape(int E, bool vec, F f) {
+  if (vec) {
+    if (E <= 32) return f.template operator()<8, 4, 4>();
+    if (E <= 64) return f.template operator()<8, 8, 4>();
+    if (E <= 128) return f.template operator()<32, 4, 4>();
+    return f.template operator()<32, 8, 4>();
+  }
+  if (E <= 8) return f.template operator()<8, 1, 1>();
+  if (E <= 32) return f.template operator()<8, 4, 1>();
+  if (E <= 64) return f.template operator()<8, 8, 1>();
+  if (E <= 128) return f.template operator()<32, 4, 1>();
+  return f.template operator()<32, 8, 1>();
+}
+
+// Tokens a block takes: short enough that the blocks fill the GPU four times,
+// whole rounds of the block's groups.
+int chunk_tokens(int T, int sms) {
+  const int most = 256, least = 32;
+  const int want = T / (4 * sms);
+  return want <= least ? least : want >= most ? most : (want + 31) / 32 * 32;
+}
+
+// The workspace has to fit whatever GPU the call runs on: for the shortest chunks.
+size_t max_segments(const moe_router_loss_desc_t* d) {
+  return (static_cast<size_t>(d->T) + 31) / 32 + d->sequences;
+}
+
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+moe_status_t check_loss_desc(const moe_router_loss_desc_t* d) {
+  if (!d) return MOE_ERR_NULL;
+  if (d->T < 0 || d->T > (1 << 28) || d->E < 1 || d->E > kMaxExperts || d->k < 1 || d->k > d->E ||
+      d->k > kMaxTopK || d->sequences < 1 || d->sequences > 65535)
+    return MOE_ERR_SHAPE;
+  if (!isfinite(d->balance_coef) || !isfinite(d->z_coef)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+size_t loss_ws_bytes(const moe_router_loss_desc_t* d) {
+  const size_t segs = max_segments(d), blocks = (d->E + 31) / 32;
+  return up16(segs * d->E * 4) * 2 + up16(segs * 4) * 2 + up16(d->sequences * blocks * 8) + 16;
+}
+
+void fill(LossArgs& a, const moe_router_loss_desc_t* d) {
+  a.T = d->T;
+  a.E = d->E;
+  a.k = d->k;
+  a.S = d->sequences;
+  a.balance = d->balance_coef;
+  a.z = d->z_coef;
+}
+
+struct RunChunks {
+  const LossArgs& a;
+  cudaStream_t s;
+  template <int LANES, int N, int VEC>
+  cudaError_t operator()() const {
+    k_loss_chunks<LANES, N, VEC><<<a.chunks, kLossThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+struct RunBwd {
+  const LossArgs& a;
+  cudaStream_t s;
+  template <int LANES, int N, int VEC>
+  cudaError_t operator()() const {
+    k_loss_bwd<LANES, N, VEC><<<a.chunks, kLossThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_router_loss_workspace_size(const moe_router_loss_desc_t* desc, size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  const moe_status_t st = check_loss_desc(desc);
+  if (st != MOE_OK) return st;
+  *bytes = loss_ws_bytes(desc);
+  return MOE_OK;
+}
+
+moe_status_t moe_router_loss_fwd(const moe_router_loss_desc_t* desc, const float* logits,
+                                 const int32_t* topk_idx, const uint8_t* mask,
+                                 const int32_t* seq_offsets, int32_t* counts, int32_t* tokens,
+                                 float* probs, float* loss, void* ws, size_t ws_bytes,
+                                 cudaStream_t stream) {
+  moe_status_t st = check_loss_desc(desc);
+  if (st != MOE_OK) return st;
+  if (!counts || !tokens || !probs || !loss || !ws) return MOE_ERR_NULL;
+  if (desc->T > 0 && (!logits || !topk_idx)) return MOE_ERR_NULL;
+  if (desc->sequences > 1 && !seq_offsets) return MOE_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(seq_offsets, 4) ||
+      !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(probs, 4) || !aligned(loss, 4) ||
+      !aligned(ws, 16))
+    return MOE_ERR_SHAPE;
+  if (ws_bytes < loss_ws_bytes(desc)) return MOE_ERR_WORKSPACE;
+  LossArgs a = {};
+  int sms;
+  st = current_device(&sms, &a.status);
+  if (st != MOE_OK) return st;
+  fill(a, desc);
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.mask = mask;
+  a.seq_offsets = seq_offsets;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.probs = probs;
+  a.loss = loss;
+  a.chunk = chunk_tokens(a.T, sms);
+  a.chunks = (a.T + a.chunk - 1) / a.chunk;
+  const size_t segs = max_segments(desc);
+  const int e_blocks = (a.E + 31) / 32;
+  char* p = static_cast<char*>(ws);
+  auto take = [&p](size_t n) {
+    char* q = p;
+    p += up16(n);
+    return q;
+  };
+  a.seg_p = reinterpret_cast<float*>(take(segs * a.E * 4));
+  a.seg_count = reinterpret_cast<int32_t*>(take(segs * a.E * 4));
+  a.seg_z = reinterpret_cast<float*>(take(segs * 4));
+  a.seg_tokens = reinterpret_cast<int32_t*>(take(segs * 4));
+  a.term = reinterpret_cast<double*>(take(static_cast<size_t>(a.S) * e_blocks * 8));
+  a.done = reinterpret_cast<unsigned int*>(take(4));
+  cudaError_t err = cudaSuccess;
+  if (a.chunks > 0) {
+    err = with_shape(a.E, a.E % 4 == 0 && aligned(logits, 16), RunChunks{a, stream});
+  } else {
+    err = cudaMemsetAsync(a.done, 0, 4, stream);
+  }
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(e_blocks, a.S);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  err = cudaLaunchKernelEx(&cfg, k_loss_join, a);
+  return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float* logits,
+                                 const uint8_t* mask, const int32_t* seq_offsets,
+                                 const int32_t* counts, const int32_t* tokens, const float* dloss,
+                                 const float* dw, const float* topk_w, const int32_t* topk_idx,
+                                 float* dlogits, cudaStream_t stream) {
+  moe_status_t st = check_loss_desc(desc);
+  if (st != MOE_OK) return st;
+  if (!counts || !tokens) return MOE_ERR_NULL;
+  if (desc->T > 0 && (!logits || !dlogits)) return MOE_ERR_NULL;
+  if (dw && (!topk_w || !topk_idx)) return MOE_ERR_NULL;
+  if (desc->sequences > 1 && !seq_offsets) return MOE_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(seq_offsets, 4) ||
+      !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(dloss, 4) || !aligned(dw, 4) ||
+      !aligned(topk_w, 4) || !aligned(dlogits, 4))
+    return MOE_ERR_SHAPE;
+  LossArgs a = {};
+  int sms;
+  st = current_device(&sms, &a.status);
+  if (st != MOE_OK) return st;
+  if (desc->T == 0) return MOE_OK;
+  fill(a, desc);
+  a.logits = logits;
+  a.mask = mask;
+  a.seq_offsets = seq_offsets;
+  a.counts = const_cast<int32_t*>(counts);
+  a.tokens = const_cast<int32_t*>(tokens);
+  a.dloss = dloss;
+  a.dw = dw;
+  a.topk_w = topk_w;
+  a.topk_idx = topk_idx;
+  a.dlogits = dlogits;
+  a.chunk = chunk_tokens(a.T, sms);
+  a.chunks = (a.T + a.chunk - 1) / a.chunk;
+  const bool vec = a.E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
+  return with_shape(a.E, vec, RunBwd{a, stream}) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"
