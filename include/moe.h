@@ -1013,8 +1013,8 @@ moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float
  * for each of `batch` matrices of rows x cols.  The products run on the tensor
  * cores with fp16 operands and fp32 accumulation, the state X is kept in 32 bits
  * and out rounded once to bf16.  Up to eight of the default steps the 2-norm of
- * out's error is below 1e-2 of out's (5 steps on matrices with sides of 64 and
- * more: below 5e-3, rounding included).  (a, b, c) with which a singular value in
+ * out's error is below 1e-2 of out's (sides below 16: 2e-2; 5 steps on matrices
+ * with sides of 64 and more: 5e-3), rounding included.  (a, b, c) with which a singular value in
  * [0,1] could reach 2 within the steps, or |b| s^2 + |c| s^4 could pass 16, are
  * refused with MOE_ERR_UNSUPPORTED.  A zero matrix stays zero; an Inf or NaN
  * reaches its own matrix only. */

@@ -344,7 +344,8 @@ def binding():
         loader.exec_module(module)
         module.setup(torch, *[ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.moe_block_pre_norm_fwd, L.moe_block_pre_norm_bwd, L.moe_block_post_norm_fwd,
-            L.moe_block_post_norm_bwd, L.moe_grad_norm, L.moe_clip_grads)])
+            L.moe_block_post_norm_bwd, L.moe_grad_norm, L.moe_clip_grads, L.moe_router_loss_fwd,
+            L.moe_router_loss_bwd, L.moe_orthogonalize)])
         _binding = module
     return _binding
 
@@ -924,37 +925,6 @@ def moe_clip_grads(grads, norm, max_norm, eps=1e-6, stream=None):
 
 
 # ------------------------------------------------------- router's losses
-def _array(t, shape, dtype, name):
-    """Address of a contiguous tensor of the shape and type on the current
-    device; None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor of shape {shape}, got "
-                         f"{t.dtype} of shape {tuple(t.shape)} on {t.device}")
-    _on_device(t, name)
-    return t.data_ptr()
-
-
-def _on_device(t, name):
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"{torch.cuda.current_device()}")
-
-
-def _mask(mask, T):
-    if mask is not None and mask.dtype is torch.uint8:
-        return _array(mask, (T,), torch.uint8, "mask")
-    return _array(mask, (T,), torch.bool, "mask")
-
-
-def _workspace(ws):
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("the workspace must be a contiguous CUDA tensor")
-    _on_device(ws, "ws")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def moe_router_loss_workspace_size(desc):
     n = ctypes.c_size_t(0)
     _check(lib().moe_router_loss_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
@@ -965,32 +935,16 @@ def moe_router_loss_fwd(desc, logits, topk_idx, mask, seq_offsets, counts, token
                         stream=None):
     """counts, tokens, probs and loss (fp32 [3]: loss, balance, z) of a batch's
     routing; mask (bool or uint8 [T]) and seq_offsets (int32 [S+1]) or None."""
-    T, E, k, S = desc.T, desc.E, desc.k, desc.sequences
-    f32, i32 = torch.float32, torch.int32
-    _check(lib().moe_router_loss_fwd(
-        ctypes.byref(desc), _array(logits, (T, E), f32, "logits"),
-        _array(topk_idx, (T, k), i32, "topk_idx"), _mask(mask, T),
-        _array(seq_offsets, (S + 1,), i32, "seq_offsets"), _array(counts, (S, E), i32, "counts"),
-        _array(tokens, (S + 1,), i32, "tokens"), _array(probs, (S, E), f32, "probs"),
-        _array(loss, (3,), f32, "loss"), *_workspace(ws), _stream(stream)))
+    _check((_binding or binding()).router_loss_fwd(desc, logits, topk_idx, mask, seq_offsets,
+                                                   counts, tokens, probs, loss, ws, stream))
 
 
 def moe_router_loss_bwd(desc, logits, mask, seq_offsets, counts, tokens, dloss, routed, dlogits,
                         stream=None):
     """dlogits = the losses' gradient (dloss fp32 [1] or None: 1), joined to that
     of the selected weights where routed is a dict {dw, topk_w, topk_idx}."""
-    T, E, k, S = desc.T, desc.E, desc.k, desc.sequences
-    f32, i32 = torch.float32, torch.int32
-    dw = w = idx = None
-    if routed is not None:
-        dw = _array(routed["dw"], (T, k), f32, "dw")
-        w = _array(routed["topk_w"], (T, k), f32, "topk_w")
-        idx = _array(routed["topk_idx"], (T, k), i32, "topk_idx")
-    _check(lib().moe_router_loss_bwd(
-        ctypes.byref(desc), _array(logits, (T, E), f32, "logits"), _mask(mask, T),
-        _array(seq_offsets, (S + 1,), i32, "seq_offsets"), _array(counts, (S, E), i32, "counts"),
-        _array(tokens, (S + 1,), i32, "tokens"), _array(dloss, (1,), f32, "dloss"), dw, w, idx,
-        _array(dlogits, (T, E), f32, "dlogits"), _stream(stream)))
+    _check((_binding or binding()).router_loss_bwd(desc, logits, mask, seq_offsets, counts, tokens,
+                                                   dloss, routed, dlogits, stream))
 
 
 # ------------------------------------------------- orthogonalised updates
@@ -1000,32 +954,9 @@ def moe_orthogonalize_workspace_size(desc):
     return int(n.value)
 
 
-def _matrices(t, desc, dtype, name):
-    """[batch, rows, cols] (or one [rows, cols]) with unit stride along a row."""
-    if t is None:
-        return moe_matrices_t(None, 0, 0)
-    shape = (desc.batch, desc.rows, desc.cols)
-    if t.dtype is not dtype or not t.is_cuda or (
-            tuple(t.shape) != shape and (desc.batch != 1 or tuple(t.shape) != shape[1:])):
-        raise ValueError(f"{name}: expected a {dtype} CUDA tensor of shape {shape}, got {t.dtype} "
-                         f"of shape {tuple(t.shape)} on {t.device}")
-    _on_device(t, name)
-    if desc.cols > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: rows must have unit stride, got strides {t.stride()}")
-    # (strides along a dimension of one are whatever torch left there)
-    ld = t.stride(-2) if desc.rows > 1 else desc.cols
-    plane = t.stride(0) if desc.batch > 1 else ld * desc.rows
-    return moe_matrices_t(t.data_ptr(), ld, plane)
-
-
 def moe_orthogonalize(desc, grad, out, ws, mom=None, mom_out=None, stream=None):
     """out (bf16) = scale times the orthogonalised update of each matrix of grad;
     mom, mom_out (fp32): the momentum before and after (mom_out None: in place)."""
     if mom is not None and mom_out is None:
         mom_out = mom
-    g = torch.float32 if desc.grad_dtype == MOE_DTYPE_FP32 else torch.bfloat16
-    _check(lib().moe_orthogonalize(
-        ctypes.byref(desc), _matrices(grad, desc, g, "grad"),
-        _matrices(mom, desc, torch.float32, "mom"),
-        _matrices(mom_out, desc, torch.float32, "mom_out"),
-        _matrices(out, desc, torch.bfloat16, "out"), *_workspace(ws), _stream(stream)))
+    _check((_binding or binding()).orthogonalize(desc, grad, mom, mom_out, out, ws, stream))

@@ -78,8 +78,8 @@ def _build_binding(cmd, verbose):
     else:
         with contextlib.suppress(FileNotFoundError):
             os.remove(BINDING)
-        sys.stderr.write("the Python binding is not built: calls of the residual block's norms and "
-                         "of gradient lists will raise\n")
+        sys.stderr.write("the Python binding is not built: calls of the residual block's norms, of "
+                         "gradient lists, of the router's losses and of updates will raise\n")
 
 
 def build_library(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:

@@ -1,5 +1,5 @@
-/* Python binding of the residual block's norms and of gradient clipping, by
- * the CPython C API.
+/* Python binding of the residual block's norms, of gradient clipping, of the
+ * router's losses and of orthogonalised updates, by the CPython C API.
  *
  * These calls are small: with the tensors described in Python, their
  * arguments took longer than the kernels of a decode step (6 us for two
@@ -27,14 +27,19 @@ static struct {
   __typeof__(&moe_block_post_norm_bwd) post_bwd;
   __typeof__(&moe_grad_norm) grad_norm;
   __typeof__(&moe_clip_grads) clip;
+  __typeof__(&moe_router_loss_fwd) loss_fwd;
+  __typeof__(&moe_router_loss_bwd) loss_bwd;
+  __typeof__(&moe_orthogonalize) ortho;
 } lib;
 
 static struct {
-  PyObject *bf16, *f32, *i32;                 /* torch dtypes */
+  PyObject *bf16, *f32, *i32, *u8, *flag;     /* torch dtypes */
   PyObject *data_ptr, *stride, *numel, *element_size, *is_contiguous; /* torch.Tensor's methods */
+  PyObject *get_device;
   PyObject *raw_stream, *device;              /* torch._C functions */
   PyObject *s_dtype, *s_is_cuda, *s_shape, *s_cuda_stream;
-  PyObject *k_pre_w, *k_pre_b, *k_post_w, *k_post_b, *k_gate, *k_row_of, *k_topk_w, *k_y_out;
+  PyObject *k_pre_w, *k_pre_b, *k_post_w, *k_post_b, *k_gate, *k_row_of, *k_topk_w, *k_y_out,
+      *k_dw, *k_topk_idx;
 } py;
 
 /* ---------------------------------------------------------- one tensor */
@@ -464,6 +469,205 @@ static PyObject* clip_grads(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+/* --------------------------------------- router's losses, updates */
+/* Fails unless t is on the current device, whose number *device keeps (-1: not
+ * asked for yet, as there may be none before a tensor is known to be on one). */
+static int on_device(PyObject* t, long long* device) {
+  long long have;
+  if (*device < 0) {
+    PyObject* dev = PyObject_Vectorcall(py.device, NULL, 0, NULL);
+    if (!dev) return -1;
+    *device = PyLong_AsLongLong(dev);
+    Py_DECREF(dev);
+    if (*device < 0) return -1;
+  }
+  if (call_long(py.get_device, t, &have) < 0) return -1;
+  if (have == *device) return 0;
+  PyErr_Format(PyExc_ValueError, "a tensor is on cuda:%lld, the current device is cuda:%lld", have,
+               *device);
+  return -1;
+}
+
+/* A contiguous tensor of shape [rows, cols], or [rows] where cols < 0, on the
+ * device; None gives NULL. */
+static int get_array(PyObject* t, long long rows, long long cols, PyObject* dtype, long long* device,
+                     void** out) {
+  *out = NULL;
+  if (!t || t == Py_None) return 0;
+  if (check_type(t, dtype) < 0) return -1;
+  PyObject* shape = PyObject_GetAttr(t, py.s_shape);
+  if (!shape) return -1;
+  long long a = -1, b = cols;
+  int ok;
+  if (cols < 0)
+    ok = PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 1 &&
+         PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0)) == rows;
+  else
+    ok = two(shape, &a, &b) == 0 && a == rows && b == cols;
+  if (ok) {
+    PyObject* c = PyObject_Vectorcall(py.is_contiguous, &t, 1, NULL);
+    if (!c) {
+      Py_DECREF(shape);
+      return -1;
+    }
+    ok = c == Py_True;
+    Py_DECREF(c);
+  }
+  if (!ok && !PyErr_Occurred()) {
+    if (cols < 0)
+      PyErr_Format(PyExc_ValueError, "expected a contiguous tensor of shape (%lld,), got %S", rows,
+                   shape);
+    else
+      PyErr_Format(PyExc_ValueError, "expected a contiguous tensor of shape (%lld, %lld), got %S",
+                   rows, cols, shape);
+  }
+  Py_DECREF(shape);
+  if (!ok || on_device(t, device) < 0) return -1;
+  return address(t, out);
+}
+
+/* The mask: a byte a token, bool or uint8. */
+static int get_mask(PyObject* t, long long T, long long* device, void** out) {
+  PyObject* dtype = py.flag;
+  if (t != Py_None) {
+    PyObject* have = PyObject_GetAttr(t, py.s_dtype);
+    if (!have) return -1;
+    if (have == py.u8) dtype = py.u8;
+    Py_DECREF(have);
+  }
+  return get_array(t, T, -1, dtype, device, out);
+}
+
+static int get_workspace(PyObject* t, long long* device, void** out, size_t* bytes) {
+  return get_buffer(t, out, bytes) < 0 || on_device(t, device) < 0 ? -1 : 0;
+}
+
+/* A descriptor's bytes (a ctypes structure of the size), copied. */
+static int get_struct(PyObject* o, void* to, size_t size) {
+  Py_buffer b;
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) < 0) return -1;
+  const int ok = b.len == (Py_ssize_t)size;
+  if (ok) memcpy(to, b.buf, size);
+  PyBuffer_Release(&b);
+  if (!ok) PyErr_SetString(PyExc_ValueError, "expected the call's own descriptor");
+  return ok ? 0 : -1;
+}
+
+/* desc, logits, topk_idx, mask, seq_offsets, counts, tokens, probs, loss, ws, stream */
+static PyObject* router_loss_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  moe_router_loss_desc_t d;
+  void *logits, *idx, *mask, *offsets, *counts, *tokens, *probs, *loss, *ws;
+  size_t bytes;
+  cudaStream_t s;
+  int st;
+  (void)self;
+  if (want(n, 11) < 0 || get_struct(a[0], &d, sizeof(d)) < 0) return NULL;
+  const long long S = d.sequences;
+  long long dev = -1;
+  if (get_array(a[1], d.T, d.E, py.f32, &dev, &logits) < 0 ||
+      get_array(a[2], d.T, d.k, py.i32, &dev, &idx) < 0 || get_mask(a[3], d.T, &dev, &mask) < 0 ||
+      get_array(a[4], S + 1, -1, py.i32, &dev, &offsets) < 0 ||
+      get_array(a[5], S, d.E, py.i32, &dev, &counts) < 0 ||
+      get_array(a[6], S + 1, -1, py.i32, &dev, &tokens) < 0 ||
+      get_array(a[7], S, d.E, py.f32, &dev, &probs) < 0 ||
+      get_array(a[8], 3, -1, py.f32, &dev, &loss) < 0 || get_workspace(a[9], &dev, &ws, &bytes) < 0 ||
+      get_stream(a[10], &s) < 0)
+    return NULL;
+  CALL(st, lib.loss_fwd(&d, logits, idx, mask, offsets, counts, tokens, probs, loss, ws, bytes, s));
+  return PyLong_FromLong(st);
+}
+
+/* desc, logits, mask, seq_offsets, counts, tokens, dloss, routed or None, dlogits, stream */
+static PyObject* router_loss_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  moe_router_loss_desc_t d;
+  void *logits, *mask, *offsets, *counts, *tokens, *dloss, *dlogits;
+  void *dw = NULL, *w = NULL, *idx = NULL;
+  cudaStream_t s;
+  int st;
+  (void)self;
+  if (want(n, 10) < 0 || get_struct(a[0], &d, sizeof(d)) < 0) return NULL;
+  const long long S = d.sequences;
+  long long dev = -1;
+  if (a[7] != Py_None) {
+    PyObject *pdw, *pw, *pidx;
+    if (!PyDict_Check(a[7]) || !(pdw = PyDict_GetItem(a[7], py.k_dw)) ||
+        !(pw = PyDict_GetItem(a[7], py.k_topk_w)) || !(pidx = PyDict_GetItem(a[7], py.k_topk_idx)) ||
+        pdw == Py_None) {
+      PyErr_SetString(PyExc_ValueError, "routed must hold dw, topk_w and topk_idx");
+      return NULL;
+    }
+    if (get_array(pdw, d.T, d.k, py.f32, &dev, &dw) < 0 ||
+        get_array(pw, d.T, d.k, py.f32, &dev, &w) < 0 ||
+        get_array(pidx, d.T, d.k, py.i32, &dev, &idx) < 0)
+      return NULL;
+  }
+  if (get_array(a[1], d.T, d.E, py.f32, &dev, &logits) < 0 ||
+      get_mask(a[2], d.T, &dev, &mask) < 0 || get_array(a[3], S + 1, -1, py.i32, &dev, &offsets) < 0 ||
+      get_array(a[4], S, d.E, py.i32, &dev, &counts) < 0 ||
+      get_array(a[5], S + 1, -1, py.i32, &dev, &tokens) < 0 ||
+      get_array(a[6], 1, -1, py.f32, &dev, &dloss) < 0 ||
+      get_array(a[8], d.T, d.E, py.f32, &dev, &dlogits) < 0 || get_stream(a[9], &s) < 0)
+    return NULL;
+  CALL(st, lib.loss_bwd(&d, logits, mask, offsets, counts, tokens, dloss, dw, w, idx, dlogits, s));
+  return PyLong_FromLong(st);
+}
+
+/* [batch, rows, cols] (or one [rows, cols]) with unit stride along a row. */
+static int get_matrices(PyObject* t, const moe_orthogonalize_desc_t* d, PyObject* dtype,
+                        long long* device, moe_matrices_t* out) {
+  out->p = NULL;
+  out->ld = out->plane = 0;
+  if (!t || t == Py_None) return 0;
+  if (check_type(t, dtype) < 0 || on_device(t, device) < 0) return -1;
+  const long long want3[3] = {d->batch, d->rows, d->cols};
+  long long strides[3] = {0, 0, 0};
+  PyObject* shape = PyObject_GetAttr(t, py.s_shape);
+  if (!shape) return -1;
+  const Py_ssize_t dims = PyTuple_Check(shape) ? PyTuple_GET_SIZE(shape) : 0;
+  int ok = dims == 3 || (dims == 2 && d->batch == 1);
+  for (Py_ssize_t i = 0; ok && i < dims; ++i)
+    ok = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i)) == want3[3 - dims + i];
+  if (!ok && !PyErr_Occurred())
+    PyErr_Format(PyExc_ValueError, "expected a tensor of shape (%lld, %lld, %lld), got %S", want3[0],
+                 want3[1], want3[2], shape);
+  Py_DECREF(shape);
+  if (!ok) return -1;
+  PyObject* st = PyObject_Vectorcall(py.stride, &t, 1, NULL);
+  if (!st) return -1;
+  for (Py_ssize_t i = 0; i < dims; ++i)
+    strides[3 - dims + i] = PyLong_AsLongLong(PyTuple_GET_ITEM(st, i));
+  ok = d->cols <= 1 || strides[2] == 1;
+  if (!ok && !PyErr_Occurred())
+    PyErr_Format(PyExc_ValueError, "rows must have unit stride, got strides %S", st);
+  Py_DECREF(st);
+  if (!ok || PyErr_Occurred()) return -1;
+  /* strides along a dimension of one are whatever was left there */
+  out->ld = d->rows > 1 ? strides[1] : d->cols;
+  out->plane = d->batch > 1 ? strides[0] : out->ld * d->rows;
+  return address(t, &out->p);
+}
+
+/* desc, grad, mom, mom_out, out, ws, stream */
+static PyObject* orthogonalize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  moe_orthogonalize_desc_t d;
+  moe_matrices_t grad, mom, mom_out, out;
+  void* ws;
+  size_t bytes;
+  cudaStream_t s;
+  int st;
+  (void)self;
+  if (want(n, 7) < 0 || get_struct(a[0], &d, sizeof(d)) < 0) return NULL;
+  long long dev = -1;
+  if (get_matrices(a[1], &d, dtype_of(d.grad_dtype), &dev, &grad) < 0 ||
+      get_matrices(a[2], &d, py.f32, &dev, &mom) < 0 ||
+      get_matrices(a[3], &d, py.f32, &dev, &mom_out) < 0 ||
+      get_matrices(a[4], &d, py.bf16, &dev, &out) < 0 || get_workspace(a[5], &dev, &ws, &bytes) < 0 ||
+      get_stream(a[6], &s) < 0)
+    return NULL;
+  CALL(st, lib.ortho(&d, grad, mom, mom_out, out, ws, bytes, s));
+  return PyLong_FromLong(st);
+}
+
 /* ------------------------------------------------------------- the module */
 /* The object at `path` (names between dots) from `from`. */
 static PyObject* attr(PyObject* from, const char* path) {
@@ -481,16 +685,19 @@ static PyObject* attr(PyObject* from, const char* path) {
   return o;
 }
 
-/* torch, the six functions' addresses in the order of `lib` */
+/* torch, the functions' addresses in the order of `lib` */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (want(n, 7) < 0) return NULL;
+  if (want(n, 10) < 0) return NULL;
   struct {
     PyObject** to;
     const char* path;
   } found[] = {{&py.bf16, "bfloat16"},
                {&py.f32, "float32"},
                {&py.i32, "int32"},
+               {&py.u8, "uint8"},
+               {&py.flag, "bool"},
+               {&py.get_device, "Tensor.get_device"},
                {&py.data_ptr, "Tensor.data_ptr"},
                {&py.stride, "Tensor.stride"},
                {&py.numel, "Tensor.numel"},
@@ -503,8 +710,8 @@ static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (!o) return NULL;
     Py_XSETREF(*found[i].to, o);
   }
-  void* f[6];
-  for (int i = 0; i < 6; ++i) {
+  void* f[9];
+  for (int i = 0; i < 9; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a function's address is missing");
@@ -524,6 +731,9 @@ static PyMethodDef methods[] = {
     {"in_place", (PyCFunction)(void (*)(void))in_place, METH_FASTCALL, NULL},
     {"grad_norm", (PyCFunction)(void (*)(void))grad_norm, METH_FASTCALL, NULL},
     {"clip_grads", (PyCFunction)(void (*)(void))clip_grads, METH_FASTCALL, NULL},
+    {"router_loss_fwd", (PyCFunction)(void (*)(void))router_loss_fwd, METH_FASTCALL, NULL},
+    {"router_loss_bwd", (PyCFunction)(void (*)(void))router_loss_bwd, METH_FASTCALL, NULL},
+    {"orthogonalize", (PyCFunction)(void (*)(void))orthogonalize, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods,
@@ -538,7 +748,8 @@ PyMODINIT_FUNC PyInit__binding(void) {
                {&py.k_pre_w, "pre_w"},     {&py.k_pre_b, "pre_b"},
                {&py.k_post_w, "post_w"},   {&py.k_post_b, "post_b"},
                {&py.k_gate, "gate"},       {&py.k_row_of, "row_of"},
-               {&py.k_topk_w, "topk_w"},   {&py.k_y_out, "y_out"}};
+               {&py.k_topk_w, "topk_w"},   {&py.k_y_out, "y_out"},
+               {&py.k_dw, "dw"},           {&py.k_topk_idx, "topk_idx"}};
   for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i) {
     *names[i].to = PyUnicode_InternFromString(names[i].text);
     if (!*names[i].to) return NULL;

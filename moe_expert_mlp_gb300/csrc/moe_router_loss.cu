@@ -1,17 +1,18 @@
 // The router's losses and their gradient (see include/moe.h for the formulas).
 //
 // Both passes are one read of the logits: a token's row lies in the registers
-// of a group of 8 or 32 lanes, whose shuffles give its maximum, its sum of
-// exponentials and, in the backward, <f, p>.  What they cannot do without is
-// that read (and the backward's write); the arithmetic, one exponential an
-// element, is below it.
+// of a group of 8 or 32 lanes, whose exchanges give its maximum, its sum of
+// exponentials and, in the backward, <f, p>; the next token's row is on its way
+// meanwhile.  What they cannot do without is that read (and the backward's
+// write); the arithmetic, one exponential an element, is below it.
 //
 // Forward: the tokens are cut into chunks of equal length, one block each, and
 // a chunk at the ends of sequences into segments.  Chunks and sequences both
 // ascend, so the segment of chunk c and sequence s has the number c + s to
-// itself.  A block writes its segments' sums of p, counts and squares; a second
-// launch adds the segments of a sequence up in ascending order, so the result
-// does not depend on the order in which blocks ran.
+// itself.  A block writes its segments' sums of p, counts and squares, and the
+// segments of a sequence are added up in ascending order, so the result does
+// not depend on the order in which blocks ran: by a second launch, or, with no
+// more chunks than a cluster has blocks, by the cluster that made them.
 #include <math.h>
 
 #include "moe_internal.h"
@@ -21,7 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kLossThreads = 256;
-constexpr int kLossMaxLanes = 32;
+constexpr int kLossCluster = 8;       // chunks that one launch makes and joins
 
 struct LossArgs {
   const float* logits;
@@ -54,32 +55,62 @@ __device__ __forceinline__ int expert_of(int lane, int j) {
   return (j * LANES + lane) * VEC;
 }
 
-// Softmax of one row over the group's lanes, in place: x becomes p.  Returns
-// logsumexp.  A row without a logit above -inf has p = 0 and gives 0.
-template <int LANES, int N>
-__device__ __forceinline__ float row_softmax(float (&x)[N], uint32_t group_mask) {
+template <int LANES>
+__device__ __forceinline__ uint32_t group_lanes() {
+  if constexpr (LANES == 32)
+    return 0xFFFFFFFFu;
+  else
+    return ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+}
+
+// The largest of a group's values, NaN where there is one.
+template <int LANES>
+__device__ __forceinline__ float group_max(float v, uint32_t mask) {
+  if constexpr (LANES == 32) {
+    asm volatile("redux.sync.max.NaN.f32 %0, %0, %1;" : "+f"(v) : "r"(mask));
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      const float other = __shfl_xor_sync(mask, v, o);
+      v = other > v || other != other ? other : v;
+    }
+  }
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v, uint32_t mask) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+
+// Softmax of one row over the group's lanes, in place: x becomes p, and with DOT
+// dot <f, p>.  Returns logsumexp.  A row without a logit above -inf has p = 0 and
+// gives 0.
+template <int LANES, int N, bool DOT>
+__device__ __forceinline__ float row_softmax(float (&x)[N], const float* f, float& dot,
+                                             uint32_t mask) {
   float top = x[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) top = x[i] > top || x[i] != x[i] ? x[i] : top;
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    const float other = __shfl_xor_sync(group_mask, top, o);
-    top = other > top || other != other ? other : top;
-  }
+  top = group_max<LANES>(top, mask);
+  float sum = 0.0f;
+  dot = 0.0f;
   if (top == -INFINITY) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = 0.0f;
     return 0.0f;
   }
-  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    x[i] = expf(x[i] - top);
+    x[i] = __expf(x[i] - top);
     sum += x[i];
+    if constexpr (DOT) dot = fmaf(f[i], x[i], dot);
   }
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group_mask, sum, o);
+  sum = group_sum<LANES>(sum, mask);
   const float inv = 1.0f / sum;
+  if constexpr (DOT) dot = group_sum<LANES>(dot, mask) * inv;
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] *= inv;
   return top + logf(sum);
@@ -126,19 +157,20 @@ __device__ __forceinline__ void sequence_span(const LossArgs& a, int s, int* beg
   *end = min(__ldg(a.seq_offsets + s + 1), a.T);
 }
 
+template <typename V>
+__device__ __forceinline__ V lane_of(const V* v, int n) {
+  const int i = threadIdx.x & 31;
+  return i < n ? v[i] : V(0);
+}
+
+// A block's segments: sums of p, counts, squares and tokens of chunk c.
 template <int LANES, int N, int VEC>
-__global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) {
+__device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, float* s_p, int* s_count,
+                                               float* s_z, int* s_n) {
   constexpr int kGroups = kLossThreads / LANES;
-  __shared__ float s_p[kGroups * LANES * N];   // a row of each group
-  __shared__ int s_count[kMaxExperts];
-  __shared__ float s_z[kGroups];
-  __shared__ int s_n[kGroups];
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  const uint32_t group_mask =
-      LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
-  const int c = blockIdx.x;
+  const uint32_t mask = group_lanes<LANES>();
   const int t0 = c * a.chunk, t1 = min(t0 + a.chunk, a.T);
-  if (c == 0 && threadIdx.x == 0) *a.done = 0;
   for (int s = sequence_of(a, t0); s < a.S; ++s) {
     int begin, end;
     sequence_span(a, s, &begin, &end);
@@ -147,18 +179,31 @@ __global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) 
     end = min(end, t1);
     if (begin >= end) continue;
     for (int e = threadIdx.x; e < a.E; e += kLossThreads) s_count[e] = 0;
-    float acc[N], z = 0.0f;
+    float acc[N], next[N], z = 0.0f;
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < N; ++i) acc[i] = next[i] = 0.0f;
+    const float* row = a.logits + static_cast<long long>(begin + group) * a.E;
+    bool live = false;
+    if (begin + group < end) {
+      load_row<LANES, N, VEC>(row, a.E, lane, -INFINITY, next);
+      live = a.mask == nullptr || a.mask[begin + group] != 0;
+    }
     for (int t = begin + group; t < end; t += kGroups) {
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
-      float x[N];
-      load_row<LANES, N, VEC>(a.logits + static_cast<long long>(t) * a.E, a.E, lane, -INFINITY, x);
-      const float lse = row_softmax<LANES, N>(x, group_mask);
+      float x[N], unused;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = next[i];
+      const bool counted = live;
+      row += static_cast<long long>(kGroups) * a.E;
+      if (t + kGroups < end) {
+        load_row<LANES, N, VEC>(row, a.E, lane, -INFINITY, next);
+        live = a.mask == nullptr || a.mask[t + kGroups] != 0;
+      }
+      if (!counted) continue;
+      const float lse = row_softmax<LANES, N, false>(x, nullptr, unused, mask);
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += x[i];
-      z += lse * lse;
+      z = fmaf(lse, lse, z);
       ++n;
     }
 #pragma unroll
@@ -172,8 +217,7 @@ __global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) 
     }
     __syncthreads();
     for (int i = threadIdx.x; i < (end - begin) * a.k; i += kLossThreads) {
-      const int t = begin + i / a.k;
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
+      if (a.mask != nullptr && a.mask[begin + i / a.k] == 0) continue;
       const int e = __ldg(a.topk_idx + static_cast<long long>(begin) * a.k + i);
       if (e < 0 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
       else atomicAdd(&s_count[e], 1);
@@ -182,46 +226,47 @@ __global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) 
     const long long seg = static_cast<long long>(c) + s;
     for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
       float p = 0.0f;
+#pragma unroll 8
       for (int g = 0; g < kGroups; ++g) p += s_p[g * (LANES * N) + e];
       a.seg_p[seg * a.E + e] = p;
       a.seg_count[seg * a.E + e] = s_count[e];
     }
-    if (threadIdx.x == 0) {
-      float zz = 0.0f;
-      int nn = 0;
-      for (int g = 0; g < kGroups; ++g) {
-        zz += s_z[g];
-        nn += s_n[g];
+    if (threadIdx.x < 32) {
+      float zz = lane_of(s_z, kGroups);
+      int nn = lane_of(s_n, kGroups);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        zz += __shfl_xor_sync(0xFFFFFFFFu, zz, o);
+        nn += __shfl_xor_sync(0xFFFFFFFFu, nn, o);
       }
-      a.seg_z[seg] = zz;
-      a.seg_tokens[seg] = nn;
+      if (threadIdx.x == 0) {
+        a.seg_z[seg] = zz;
+        a.seg_tokens[seg] = nn;
+      }
     }
     __syncthreads();
   }
 }
 
-// One block: 32 experts of one sequence, its segments over 32 warps.  The last
-// block to end joins the sequences' terms.
-__global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
-  __shared__ float s_p[32][33];
-  __shared__ int s_c[32][33];
-  __shared__ int s_n[32];
-  __shared__ bool s_last;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + lane;
+// 32 experts (block eb of blocks) of sequence s: their segments' sums over the
+// block's warps.
+__device__ __forceinline__ void join_sequence(const LossArgs& a, int s, int eb, int blocks,
+                                              float (*s_p)[33], int (*s_c)[33], int* s_n) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int e = eb * 32 + lane;
   int begin, end;
   sequence_span(a, s, &begin, &end);
   const int c0 = begin / a.chunk, c1 = end > begin ? (end - 1) / a.chunk + 1 : c0;
   float p = 0.0f;
   int count = 0, n = 0;
-  for (int c = c0 + warp; c < c1; c += 32) {
+#pragma unroll 4
+  for (int c = c0 + warp; c < c1; c += warps) {
     const long long seg = static_cast<long long>(c) + s;
     if (e < a.E) {
-      p += a.seg_p[seg * a.E + e];
-      count += a.seg_count[seg * a.E + e];
+      p += __ldcg(a.seg_p + seg * a.E + e);
+      count += __ldcg(a.seg_count + seg * a.E + e);
     }
-    n += a.seg_tokens[seg];
+    n += __ldcg(a.seg_tokens + seg);
   }
   s_p[warp][lane] = p;
   s_c[warp][lane] = count;
@@ -229,58 +274,57 @@ __global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
   __syncthreads();
   if (warp == 0) {
     p = 0.0f;
-    count = 0;
-    for (int w = 0; w < 32; ++w) {
+    count = n = 0;
+    for (int w = 0; w < warps; ++w) {
       p += s_p[w][lane];
       count += s_c[w][lane];
+      n += s_n[w];
     }
-    n = __reduce_add_sync(0xFFFFFFFFu, s_n[lane]);
-    // N_s * f * P = E / k * count * (sum of p) / N_s
     const float mean = n > 0 ? p / static_cast<float>(n) : 0.0f;
-    float term = static_cast<float>(count) * mean;
     if (e < a.E) {
       a.probs[static_cast<long long>(s) * a.E + e] = mean;
       a.counts[static_cast<long long>(s) * a.E + e] = count;
     }
-    double sum = e < a.E ? term : 0.0;
+    // N_s f P = E / k * count * P
+    double sum = e < a.E ? static_cast<double>(count) * mean : 0.0;
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) {
-      a.term[static_cast<long long>(s) * gridDim.x + blockIdx.x] = sum;
-      if (blockIdx.x == 0) a.tokens[s] = n;
+      a.term[static_cast<long long>(s) * blocks + eb] = sum;
+      if (eb == 0) a.tokens[s] = n;
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!s_last) return;
-  // the whole batch: terms and tokens of the sequences, squares of the segments
-  __shared__ double s_t[32], s_zz[32];
+}
+
+// The whole batch, by one block: terms and tokens of the sequences, squares of
+// the segments.
+__device__ __forceinline__ void join_batch(const LossArgs& a, int blocks) {
+  __shared__ double s_t[32], s_z[32];
   __shared__ long long s_m[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double t = 0.0, z = 0.0;
   long long m = 0;
   bool bad = false;
-  for (int i = threadIdx.x; i < a.S; i += 1024) {
-    for (int b = 0; b < static_cast<int>(gridDim.x); ++b)
-      t += __ldcg(a.term + static_cast<long long>(i) * gridDim.x + b);
+  for (int i = threadIdx.x; i < a.S * blocks; i += blockDim.x) t += __ldcg(a.term + i);
+  for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
     m += __ldcg(a.tokens + i);
     if (a.seq_offsets != nullptr) {
-      const int lo = a.seq_offsets[i], hi = a.seq_offsets[i + 1];
+      const int lo = __ldg(a.seq_offsets + i), hi = __ldg(a.seq_offsets + i + 1);
       bad = bad || lo < 0 || hi < lo || hi > a.T;
     }
   }
   if (bad) set_status(a.status, MOE_DEV_BAD_OFFSETS);
-  for (int c = threadIdx.x; c < a.chunks; c += 1024) {
+  for (int c = threadIdx.x; c < a.chunks; c += blockDim.x) {
     const int t0 = c * a.chunk, t1 = min(t0 + a.chunk, a.T);
     for (int q = sequence_of(a, t0); q < a.S; ++q) {
+      int begin, end;
       sequence_span(a, q, &begin, &end);
       if (begin >= t1) break;
-      if (max(begin, t0) < min(end, t1)) z += a.seg_z[static_cast<long long>(c) + q];
+      if (max(begin, t0) < min(end, t1)) z += __ldcg(a.seg_z + static_cast<long long>(c) + q);
     }
   }
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
@@ -288,16 +332,16 @@ __global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
   }
   if (lane == 0) {
     s_t[warp] = t;
-    s_zz[warp] = z;
+    s_z[warp] = z;
     s_m[warp] = m;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     t = z = 0.0;
     m = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
       t += s_t[w];
-      z += s_zz[w];
+      z += s_z[w];
       m += s_m[w];
     }
     const double total = m > 0 ? static_cast<double>(m) : 1.0;
@@ -310,32 +354,99 @@ __global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
   }
 }
 
+// CLUSTER: the grid is one cluster, which joins its chunks itself.
+template <int LANES, int N, int VEC, bool CLUSTER>
+__global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) {
+  constexpr int kGroups = kLossThreads / LANES;
+  constexpr int kWarps = kLossThreads / 32;
+  __shared__ float s_p[kGroups * LANES * N];   // a row of each group
+  __shared__ int s_count[kMaxExperts];
+  __shared__ float s_z[kGroups];
+  __shared__ int s_n[kGroups];
+  if constexpr (!CLUSTER) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+  }
+  chunk_segments<LANES, N, VEC>(a, blockIdx.x, s_p, s_count, s_z, s_n);
+  if constexpr (CLUSTER) {
+    __shared__ float j_p[kWarps][33];
+    __shared__ int j_c[kWarps][33];
+    __shared__ int j_n[kWarps];
+    const int blocks = (a.E + 31) / 32;
+    cluster_sync();
+    for (int i = blockIdx.x; i < a.S * blocks; i += gridDim.x)
+      join_sequence(a, i / blocks, i % blocks, blocks, j_p, j_c, j_n);
+    cluster_sync();
+    if (blockIdx.x == 0) join_batch(a, blocks);
+  }
+}
+
+// One block: 32 experts of one sequence.  The last block to end joins the
+// sequences.
+__global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
+  __shared__ float j_p[32][33];
+  __shared__ int j_c[32][33];
+  __shared__ int j_n[32];
+  __shared__ bool s_last;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  join_sequence(a, blockIdx.y, blockIdx.x, gridDim.x, j_p, j_c, j_n);
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (s_last) join_batch(a, gridDim.x);
+}
+
 // One group of lanes a token.  f is taken around its mean 1 over the experts,
 // which changes nothing in f - <f, p> but keeps the difference of near equals
-// exact.
+// exact.  The selected experts' share goes through a row in shared memory, zero
+// between tokens: a slot a lane, where slots that name one expert twice are
+// added in their order.
 template <int LANES, int N, int VEC>
 __global__ void __launch_bounds__(kLossThreads) k_loss_bwd(const LossArgs a) {
   constexpr int kGroups = kLossThreads / LANES;
+  __shared__ __align__(16) float s_row[kGroups][LANES * N];
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  const uint32_t group_mask =
-      LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+  const uint32_t mask = group_lanes<LANES>();
   const int t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
   const int total = __ldg(a.tokens + a.S);
   const float scale = (a.dloss != nullptr ? __ldg(a.dloss) : 1.0f) /
                       static_cast<float>(total > 0 ? total : 1);
-  int have = -1;               // the sequence whose f lies in the registers
-  float f[N];
+  float* share = s_row[group];
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = 0.0f;
+  for (int i = 0; i < N; ++i) share[i * LANES + lane] = 0.0f;
+  __syncwarp(mask);
+  int have = -1;               // the sequence whose f lies in the registers
+  float f[N], next[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = next[i] = 0.0f;
+  if (t0 + group < t1)
+    load_row<LANES, N, VEC>(a.logits + static_cast<long long>(t0 + group) * a.E, a.E, lane,
+                            -INFINITY, next);
   for (int t = t0 + group; t < t1; t += kGroups) {
     float x[N];
-    load_row<LANES, N, VEC>(a.logits + static_cast<long long>(t) * a.E, a.E, lane, -INFINITY, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = next[i];
+    if (t + kGroups < t1)
+      load_row<LANES, N, VEC>(a.logits + static_cast<long long>(t + kGroups) * a.E, a.E, lane,
+                              -INFINITY, next);
+    const long long at = static_cast<long long>(t) * a.k;
+    float w = 0.0f, dw = 0.0f;
+    int idx = -1;
+    if (a.dw != nullptr && lane < a.k) {
+      w = __ldg(a.topk_w + at + lane);
+      dw = __ldg(a.dw + at + lane);
+      idx = __ldg(a.topk_idx + at + lane);
+    }
     const int s = sequence_of(a, t);
     bool live = s < a.S && (a.mask == nullptr || a.mask[t] != 0);
     if (live && a.seq_offsets != nullptr) live = t >= __ldg(a.seq_offsets + s);
     if (live && s != have) {
       const int n = __ldg(a.tokens + s);
-      const float per = static_cast<float>(a.E) / (static_cast<float>(a.k) * (n > 0 ? n : 1));
+      const float per =
+          static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n > 0 ? n : 1));
 #pragma unroll
       for (int j = 0; j < N / VEC; ++j)
 #pragma unroll
@@ -347,35 +458,55 @@ __global__ void __launch_bounds__(kLossThreads) k_loss_bwd(const LossArgs a) {
       have = s;
     }
     if (live) {
-      const float lse = row_softmax<LANES, N>(x, group_mask);
-      float dot = 0.0f;
+      float dot;
+      const float lse = row_softmax<LANES, N, true>(x, f, dot, mask);
+      const float b = scale * a.balance, zz = scale * (2.0f * a.z * lse - a.balance * dot);
 #pragma unroll
-      for (int i = 0; i < N; ++i) dot += f[i] * x[i];
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(group_mask, dot, o);
-      const float zz = 2.0f * a.z * lse;
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = scale * x[i] * (a.balance * (f[i] - dot) + zz);
+      for (int i = 0; i < N; ++i) x[i] *= fmaf(b, f[i], zz);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = 0.0f;
     }
     if (a.dw != nullptr) {
-      const long long at = static_cast<long long>(t) * a.k;
-      float dot = 0.0f;
-      for (int i = lane; i < a.k; i += LANES) dot += __ldg(a.topk_w + at + i) * __ldg(a.dw + at + i);
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(group_mask, dot, o);
-      for (int i = 0; i < a.k; ++i) {
-        const int e = __ldg(a.topk_idx + at + i);
-        const float v = __ldg(a.topk_w + at + i) * (__ldg(a.dw + at + i) - dot);
-        if (lane == 0 && (e < 0 || e >= a.E)) set_status(a.status, MOE_DEV_BAD_EXPERT);
-#pragma unroll
-        for (int j = 0; j < N / VEC; ++j)
-#pragma unroll
-          for (int q = 0; q < VEC; ++q)
-            if (expert_of<LANES, VEC>(lane, j) + q == e) x[j * VEC + q] += v;
+      float dot = w * dw;
+      for (int i = LANES + lane; i < a.k; i += LANES)
+        dot = fmaf(__ldg(a.topk_w + at + i), __ldg(a.dw + at + i), dot);
+      dot = group_sum<LANES>(dot, mask);
+      for (int i0 = 0; i0 < a.k; i0 += LANES) {
+        if (i0 > 0) {
+          const bool in = i0 + lane < a.k;
+          w = in ? __ldg(a.topk_w + at + i0 + lane) : 0.0f;
+          dw = in ? __ldg(a.dw + at + i0 + lane) : 0.0f;
+          idx = in ? __ldg(a.topk_idx + at + i0 + lane) : -1;
+        }
+        bool in = i0 + lane < a.k;
+        if (in && (idx < 0 || idx >= a.E)) {
+          set_status(a.status, MOE_DEV_BAD_EXPERT);
+          in = false;
+        }
+        const float v = w * (dw - dot);
+        const uint32_t same = __match_any_sync(mask, in ? idx : -1 - lane);
+        // the slots of one expert in their order, one at a time
+        for (uint32_t turn = __popc(same & ((1u << (threadIdx.x & 31)) - 1u));
+             __any_sync(mask, in); --turn) {
+          if (in && turn == 0) {
+            share[idx] += v;
+            in = false;
+          }
+          __syncwarp(mask);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < N / VEC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          x[j * VEC + i] += share[expert_of<LANES, VEC>(lane, j) + i];
+      __syncwarp(mask);
+#pragma unroll
+      for (int j = 0; j < N / VEC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) share[expert_of<LANES, VEC>(lane, j) + i] = 0.0f;
+      __syncwarp(mask);
     }
     float* out = a.dlogits + static_cast<long long>(t) * a.E;
 #pragma unroll
@@ -407,12 +538,11 @@ cudaError_t with_shape(int E, bool vec, F f) {
   return f.template operator()<32, 8, 1>();
 }
 
-// Tokens a block takes: short enough that the blocks fill the GPU four times,
-// whole rounds of the block's groups.
-int chunk_tokens(int T, int sms) {
-  const int most = 256, least = 32;
-  const int want = T / (4 * sms);
-  return want <= least ? least : want >= most ? most : (want + 31) / 32 * 32;
+// Tokens a block takes so that there are about `blocks` of them: 32 to 256, in
+// whole rounds of eight groups.
+int chunk_tokens(int T, int blocks) {
+  const int want = (T + blocks - 1) / blocks;
+  return want <= 32 ? 32 : want >= 256 ? 256 : (want + 7) / 8 * 8;
 }
 
 // The workspace has to fit whatever GPU the call runs on: for the shortest chunks.
@@ -452,8 +582,21 @@ struct RunChunks {
   cudaStream_t s;
   template <int LANES, int N, int VEC>
   cudaError_t operator()() const {
-    k_loss_chunks<LANES, N, VEC><<<a.chunks, kLossThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.chunks > kLossCluster) {
+      k_loss_chunks<LANES, N, VEC, false><<<a.chunks, kLossThreads, 0, s>>>(a);
+      return cudaGetLastError();
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = a.chunks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.chunks);
+    cfg.blockDim = dim3(kLossThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_loss_chunks<LANES, N, VEC, true>, a);
   }
 };
 
@@ -510,7 +653,7 @@ moe_status_t moe_router_loss_fwd(const moe_router_loss_desc_t* desc, const float
   a.tokens = tokens;
   a.probs = probs;
   a.loss = loss;
-  a.chunk = chunk_tokens(a.T, sms);
+  a.chunk = chunk_tokens(a.T, 4 * sms);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
   const size_t segs = max_segments(desc);
   const int e_blocks = (a.E + 31) / 32;
@@ -526,19 +669,21 @@ moe_status_t moe_router_loss_fwd(const moe_router_loss_desc_t* desc, const float
   a.seg_tokens = reinterpret_cast<int32_t*>(take(segs * 4));
   a.term = reinterpret_cast<double*>(take(static_cast<size_t>(a.S) * e_blocks * 8));
   a.done = reinterpret_cast<unsigned int*>(take(4));
-  cudaError_t err = cudaSuccess;
-  if (a.chunks > 0) {
-    err = with_shape(a.E, a.E % 4 == 0 && aligned(logits, 16), RunChunks{a, stream});
-  } else {
-    err = cudaMemsetAsync(a.done, 0, 4, stream);
-  }
-  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  // (without tokens one empty chunk, which writes the zeros)
+  if (a.chunks == 0) a.chunks = 1;
+  if (with_shape(a.E, a.E % 4 == 0 && aligned(logits, 16), RunChunks{a, stream}) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (a.chunks <= kLossCluster) return MOE_OK;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(e_blocks, a.S);
   cfg.blockDim = dim3(1024);
   cfg.stream = stream;
-  err = cudaLaunchKernelEx(&cfg, k_loss_join, a);
-  return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_loss_join, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float* logits,
@@ -572,7 +717,7 @@ moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float
   a.topk_w = topk_w;
   a.topk_idx = topk_idx;
   a.dlogits = dlogits;
-  a.chunk = chunk_tokens(a.T, sms);
+  a.chunk = chunk_tokens(a.T, 8 * sms);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
   const bool vec = a.E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
   return with_shape(a.E, vec, RunBwd{a, stream}) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
