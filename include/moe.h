@@ -963,8 +963,8 @@ moe_status_t moe_clip_grads(const moe_grad_t* grads, int32_t n, const float* nor
  * -inf has p = 0 and adds nothing to either loss.  An empty sequence has P = 0;
  * without counted tokens the losses are 0.  NaN and +Inf logits reach the
  * losses, P of their sequence and their token's gradient.  Sums over tokens are
- * fp32 within a block and added in one order, those over the batch fp64: equal
- * inputs give equal results on one GPU. */
+ * fp32, in chains of at most 32 (beyond 2^20 tokens T / 2^15) and then by halves,
+ * in one order: equal inputs give equal results on one GPU. */
 typedef struct {
   int32_t T;          /* tokens, 0..2^28 */
   int32_t E;          /* experts, 1..256 */

@@ -21,7 +21,9 @@
 namespace moe {
 namespace {
 
-constexpr int kLossThreads = 256;
+constexpr int kFwdThreads = 1024;
+constexpr int kBwdThreads = 256;
+constexpr int kFwdMostTokens = 1024;  // of a chunk: 32 of a warp are added in fp32 one by one
 constexpr int kLossCluster = 8;       // chunks that one launch makes and joins
 
 struct LossArgs {
@@ -42,7 +44,7 @@ struct LossArgs {
   int32_t* seg_count;          // [segments, E]
   float* seg_z;                // [segments]
   int32_t* seg_tokens;         // [segments]
-  double* term;                // [S, e_blocks]: N_s * sum f P over 32 experts
+  float* term;                 // [S, e_blocks]: sum of count * P over 32 experts
   unsigned int* done;
   int* status;
   int T, E, k, S, chunk, chunks;
@@ -63,17 +65,13 @@ __device__ __forceinline__ uint32_t group_lanes() {
     return ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
 }
 
-// The largest of a group's values, NaN where there is one.
 template <int LANES>
 __device__ __forceinline__ float group_max(float v, uint32_t mask) {
   if constexpr (LANES == 32) {
-    asm volatile("redux.sync.max.NaN.f32 %0, %0, %1;" : "+f"(v) : "r"(mask));
+    asm volatile("redux.sync.max.f32 %0, %0, %1;" : "+f"(v) : "r"(mask));
   } else {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) {
-      const float other = __shfl_xor_sync(mask, v, o);
-      v = other > v || other != other ? other : v;
-    }
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
   }
   return v;
 }
@@ -85,22 +83,29 @@ __device__ __forceinline__ float group_sum(float v, uint32_t mask) {
   return v;
 }
 
-// Softmax of one row over the group's lanes, in place: x becomes p, and with DOT
-// dot <f, p>.  Returns logsumexp.  A row without a logit above -inf has p = 0 and
-// gives 0.
+// Softmax of one row over the group's lanes: x becomes exp(x - top), inv the
+// reciprocal of their sum, and with DOT dot is <f, p>.  Returns logsumexp.  A row
+// without a logit above -inf has p = 0 and gives 0.  (The maxima pass over NaN,
+// which then reaches the sum.)
 template <int LANES, int N, bool DOT>
-__device__ __forceinline__ float row_softmax(float (&x)[N], const float* f, float& dot,
+__device__ __forceinline__ float row_softmax(float (&x)[N], float& inv, const float* f, float& dot,
                                              uint32_t mask) {
   float top = x[0];
 #pragma unroll
-  for (int i = 1; i < N; ++i) top = x[i] > top || x[i] != x[i] ? x[i] : top;
+  for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
   top = group_max<LANES>(top, mask);
   float sum = 0.0f;
   dot = 0.0f;
   if (top == -INFINITY) {
+    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.0f;
-    return 0.0f;
+    for (int i = 0; i < N; ++i) {
+      nan = nan || x[i] != x[i];
+      x[i] = 0.0f;
+    }
+    inv = __any_sync(mask, nan) ? __int_as_float(0x7FC00000) : 0.0f;
+    dot = inv;
+    return inv;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -109,10 +114,8 @@ __device__ __forceinline__ float row_softmax(float (&x)[N], const float* f, floa
     if constexpr (DOT) dot = fmaf(f[i], x[i], dot);
   }
   sum = group_sum<LANES>(sum, mask);
-  const float inv = 1.0f / sum;
+  inv = 1.0f / sum;
   if constexpr (DOT) dot = group_sum<LANES>(dot, mask) * inv;
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] *= inv;
   return top + logf(sum);
 }
 
@@ -158,17 +161,27 @@ __device__ __forceinline__ void sequence_span(const LossArgs& a, int s, int* beg
 }
 
 template <typename V>
-__device__ __forceinline__ V lane_of(const V* v, int n) {
-  const int i = threadIdx.x & 31;
-  return i < n ? v[i] : V(0);
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
 }
+
+// What a block sums up with, all but `part` a value a warp.
+struct LossShared {
+  float p[32][kMaxExperts];      // a row of each warp
+  float part[4][kMaxExperts];
+  int count[kMaxExperts];
+  float z[32];
+  int n[32];
+};
 
 // A block's segments: sums of p, counts, squares and tokens of chunk c.
 template <int LANES, int N, int VEC>
-__device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, float* s_p, int* s_count,
-                                               float* s_z, int* s_n) {
-  constexpr int kGroups = kLossThreads / LANES;
+__device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, LossShared& sh) {
+  constexpr int kGroups = kFwdThreads / LANES;
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+  const int warp = threadIdx.x >> 5;
   const uint32_t mask = group_lanes<LANES>();
   const int t0 = c * a.chunk, t1 = min(t0 + a.chunk, a.T);
   for (int s = sequence_of(a, t0); s < a.S; ++s) {
@@ -178,7 +191,7 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, float* 
     begin = max(begin, t0);
     end = min(end, t1);
     if (begin >= end) continue;
-    for (int e = threadIdx.x; e < a.E; e += kLossThreads) s_count[e] = 0;
+    if (threadIdx.x < kMaxExperts) sh.count[threadIdx.x] = 0;
     float acc[N], next[N], z = 0.0f;
     int n = 0;
 #pragma unroll
@@ -189,8 +202,16 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, float* 
       load_row<LANES, N, VEC>(row, a.E, lane, -INFINITY, next);
       live = a.mask == nullptr || a.mask[begin + group] != 0;
     }
+    __syncthreads();
+    // the experts' counts meanwhile
+    for (int i = threadIdx.x; i < (end - begin) * a.k; i += kFwdThreads) {
+      if (a.mask != nullptr && a.mask[begin + i / a.k] == 0) continue;
+      const int e = __ldg(a.topk_idx + static_cast<long long>(begin) * a.k + i);
+      if (e < 0 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
+      else atomicAdd(&sh.count[e], 1);
+    }
     for (int t = begin + group; t < end; t += kGroups) {
-      float x[N], unused;
+      float x[N], inv, unused;
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = next[i];
       const bool counted = live;
@@ -200,46 +221,50 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, float* 
         live = a.mask == nullptr || a.mask[t + kGroups] != 0;
       }
       if (!counted) continue;
-      const float lse = row_softmax<LANES, N, false>(x, nullptr, unused, mask);
+      const float lse = row_softmax<LANES, N, false>(x, inv, nullptr, unused, mask);
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] += x[i];
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
       z = fmaf(lse, lse, z);
       ++n;
     }
+    __syncwarp();
+    // the groups of a warp, then the warps
 #pragma unroll
-    for (int j = 0; j < N / VEC; ++j)
+    for (int o = LANES; o < 32; o <<= 1) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        s_p[group * (LANES * N) + expert_of<LANES, VEC>(lane, j) + i] = acc[j * VEC + i];
-    if (lane == 0) {
-      s_z[group] = z;
-      s_n[group] = n;
+      for (int i = 0; i < N; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], o);
+      z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+      n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < (end - begin) * a.k; i += kLossThreads) {
-      if (a.mask != nullptr && a.mask[begin + i / a.k] == 0) continue;
-      const int e = __ldg(a.topk_idx + static_cast<long long>(begin) * a.k + i);
-      if (e < 0 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
-      else atomicAdd(&s_count[e], 1);
+    if (threadIdx.x % 32 < LANES) {
+#pragma unroll
+      for (int j = 0; j < N / VEC; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          sh.p[warp][expert_of<LANES, VEC>(lane, j) + i] = acc[j * VEC + i];
+      if (lane == 0) {
+        sh.z[warp] = z;
+        sh.n[warp] = n;
+      }
     }
     __syncthreads();
     const long long seg = static_cast<long long>(c) + s;
-    for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
+    const int e = threadIdx.x % kMaxExperts, q = threadIdx.x / kMaxExperts;
+    if (e < a.E) {
       float p = 0.0f;
-#pragma unroll 8
-      for (int g = 0; g < kGroups; ++g) p += s_p[g * (LANES * N) + e];
-      a.seg_p[seg * a.E + e] = p;
-      a.seg_count[seg * a.E + e] = s_count[e];
-    }
-    if (threadIdx.x < 32) {
-      float zz = lane_of(s_z, kGroups);
-      int nn = lane_of(s_n, kGroups);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        zz += __shfl_xor_sync(0xFFFFFFFFu, zz, o);
-        nn += __shfl_xor_sync(0xFFFFFFFFu, nn, o);
-      }
-      if (threadIdx.x == 0) {
+      for (int w = 0; w < 8; ++w) p += sh.p[8 * q + w][e];
+      sh.part[q][e] = p;
+    }
+    __syncthreads();
+    if (q == 0 && e < a.E) {
+      a.seg_p[seg * a.E + e] = (sh.part[0][e] + sh.part[1][e]) + (sh.part[2][e] + sh.part[3][e]);
+      a.seg_count[seg * a.E + e] = sh.count[e];
+    }
+    if (warp == 31) {
+      const float zz = warp_sum(sh.z[threadIdx.x & 31]);
+      const int nn = warp_sum(sh.n[threadIdx.x & 31]);
+      if (threadIdx.x % 32 == 0) {
         a.seg_z[seg] = zz;
         a.seg_tokens[seg] = nn;
       }
@@ -249,10 +274,10 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, float* 
 }
 
 // 32 experts (block eb of blocks) of sequence s: their segments' sums over the
-// block's warps.
+// block's 32 warps.
 __device__ __forceinline__ void join_sequence(const LossArgs& a, int s, int eb, int blocks,
                                               float (*s_p)[33], int (*s_c)[33], int* s_n) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = eb * 32 + lane;
   int begin, end;
   sequence_span(a, s, &begin, &end);
@@ -260,7 +285,7 @@ __device__ __forceinline__ void join_sequence(const LossArgs& a, int s, int eb, 
   float p = 0.0f;
   int count = 0, n = 0;
 #pragma unroll 4
-  for (int c = c0 + warp; c < c1; c += warps) {
+  for (int c = c0 + warp; c < c1; c += 32) {
     const long long seg = static_cast<long long>(c) + s;
     if (e < a.E) {
       p += __ldcg(a.seg_p + seg * a.E + e);
@@ -272,23 +297,24 @@ __device__ __forceinline__ void join_sequence(const LossArgs& a, int s, int eb, 
   s_c[warp][lane] = count;
   if (lane == 0) s_n[warp] = n;
   __syncthreads();
-  if (warp == 0) {
-    p = 0.0f;
-    count = n = 0;
-    for (int w = 0; w < warps; ++w) {
-      p += s_p[w][lane];
-      count += s_c[w][lane];
-      n += s_n[w];
-    }
-    const float mean = n > 0 ? p / static_cast<float>(n) : 0.0f;
-    if (e < a.E) {
-      a.probs[static_cast<long long>(s) * a.E + e] = mean;
-      a.counts[static_cast<long long>(s) * a.E + e] = count;
+  // a warp an expert, its lanes the 32 sums
+  p = warp_sum(s_p[lane][warp]);
+  count = warp_sum(s_c[lane][warp]);
+  n = warp_sum(s_n[lane]);
+  __syncthreads();
+  const float mean = n > 0 ? p / static_cast<float>(n) : 0.0f;
+  if (lane == 0) {
+    const int mine = eb * 32 + warp;
+    if (mine < a.E) {
+      a.probs[static_cast<long long>(s) * a.E + mine] = mean;
+      a.counts[static_cast<long long>(s) * a.E + mine] = count;
     }
     // N_s f P = E / k * count * P
-    double sum = e < a.E ? static_cast<double>(count) * mean : 0.0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    s_p[0][warp] = mine < a.E ? static_cast<float>(count) * mean : 0.0f;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const float sum = warp_sum(s_p[0][lane]);
     if (lane == 0) {
       a.term[static_cast<long long>(s) * blocks + eb] = sum;
       if (eb == 0) a.tokens[s] = n;
@@ -300,11 +326,11 @@ __device__ __forceinline__ void join_sequence(const LossArgs& a, int s, int eb, 
 // The whole batch, by one block: terms and tokens of the sequences, squares of
 // the segments.
 __device__ __forceinline__ void join_batch(const LossArgs& a, int blocks) {
-  __shared__ double s_t[32], s_z[32];
-  __shared__ long long s_m[32];
+  __shared__ float s_t[32], s_z[32];
+  __shared__ int s_m[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double t = 0.0, z = 0.0;
-  long long m = 0;
+  float t = 0.0f, z = 0.0f;
+  int m = 0;
   bool bad = false;
   for (int i = threadIdx.x; i < a.S * blocks; i += blockDim.x) t += __ldcg(a.term + i);
   for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
@@ -324,58 +350,47 @@ __device__ __forceinline__ void join_batch(const LossArgs& a, int blocks) {
       if (max(begin, t0) < min(end, t1)) z += __ldcg(a.seg_z + static_cast<long long>(c) + q);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-    m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
-  }
+  t = warp_sum(t);
+  z = warp_sum(z);
+  m = warp_sum(m);
   if (lane == 0) {
     s_t[warp] = t;
     s_z[warp] = z;
     s_m[warp] = m;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    t = z = 0.0;
-    m = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-      t += s_t[w];
-      z += s_z[w];
-      m += s_m[w];
+  if (warp == 0) {
+    t = warp_sum(s_t[lane]);
+    z = warp_sum(s_z[lane]);
+    m = warp_sum(s_m[lane]);
+    if (lane == 0) {
+      const float total = static_cast<float>(m > 0 ? m : 1);
+      const float balance = t * (static_cast<float>(a.E) / static_cast<float>(a.k)) / total;
+      z /= total;
+      a.loss[0] = fmaf(a.balance, balance, a.z * z);
+      a.loss[1] = balance;
+      a.loss[2] = z;
+      a.tokens[a.S] = m;
     }
-    const double total = m > 0 ? static_cast<double>(m) : 1.0;
-    const double balance = t * a.E / a.k / total;
-    z /= total;
-    a.loss[0] = static_cast<float>(a.balance * balance + a.z * z);
-    a.loss[1] = static_cast<float>(balance);
-    a.loss[2] = static_cast<float>(z);
-    a.tokens[a.S] = static_cast<int>(m);
   }
 }
 
 // CLUSTER: the grid is one cluster, which joins its chunks itself.
 template <int LANES, int N, int VEC, bool CLUSTER>
-__global__ void __launch_bounds__(kLossThreads) k_loss_chunks(const LossArgs a) {
-  constexpr int kGroups = kLossThreads / LANES;
-  constexpr int kWarps = kLossThreads / 32;
-  __shared__ float s_p[kGroups * LANES * N];   // a row of each group
-  __shared__ int s_count[kMaxExperts];
-  __shared__ float s_z[kGroups];
-  __shared__ int s_n[kGroups];
+__global__ void __launch_bounds__(kFwdThreads) k_loss_chunks(const LossArgs a) {
+  __shared__ LossShared sh;
   if constexpr (!CLUSTER) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
   }
-  chunk_segments<LANES, N, VEC>(a, blockIdx.x, s_p, s_count, s_z, s_n);
+  chunk_segments<LANES, N, VEC>(a, blockIdx.x, sh);
   if constexpr (CLUSTER) {
-    __shared__ float j_p[kWarps][33];
-    __shared__ int j_c[kWarps][33];
-    __shared__ int j_n[kWarps];
+    __shared__ float j_p[32][33];
+    __shared__ int j_c[32][33];
     const int blocks = (a.E + 31) / 32;
     cluster_sync();
     for (int i = blockIdx.x; i < a.S * blocks; i += gridDim.x)
-      join_sequence(a, i / blocks, i % blocks, blocks, j_p, j_c, j_n);
+      join_sequence(a, i / blocks, i % blocks, blocks, j_p, j_c, sh.n);
     cluster_sync();
     if (blockIdx.x == 0) join_batch(a, blocks);
   }
@@ -390,13 +405,16 @@ __global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
   __shared__ bool s_last;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   join_sequence(a, blockIdx.y, blockIdx.x, gridDim.x, j_p, j_c, j_n);
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
-    __threadfence();
+  if (gridDim.x * gridDim.y > 1) {
+    if (threadIdx.x == 0) {
+      __threadfence();
+      s_last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) return;
   }
-  __syncthreads();
-  if (s_last) join_batch(a, gridDim.x);
+  join_batch(a, gridDim.x);
 }
 
 // One group of lanes a token.  f is taken around its mean 1 over the experts,
@@ -405,8 +423,8 @@ __global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
 // between tokens: a slot a lane, where slots that name one expert twice are
 // added in their order.
 template <int LANES, int N, int VEC>
-__global__ void __launch_bounds__(kLossThreads) k_loss_bwd(const LossArgs a) {
-  constexpr int kGroups = kLossThreads / LANES;
+__global__ void __launch_bounds__(kBwdThreads) k_loss_bwd(const LossArgs a) {
+  constexpr int kGroups = kBwdThreads / LANES;
   __shared__ __align__(16) float s_row[kGroups][LANES * N];
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
   const uint32_t mask = group_lanes<LANES>();
@@ -458,9 +476,10 @@ __global__ void __launch_bounds__(kLossThreads) k_loss_bwd(const LossArgs a) {
       have = s;
     }
     if (live) {
-      float dot;
-      const float lse = row_softmax<LANES, N, true>(x, f, dot, mask);
-      const float b = scale * a.balance, zz = scale * (2.0f * a.z * lse - a.balance * dot);
+      float inv, dot;
+      const float lse = row_softmax<LANES, N, true>(x, inv, f, dot, mask);
+      const float b = scale * inv * a.balance;
+      const float zz = scale * inv * (2.0f * a.z * lse - a.balance * dot);
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] *= fmaf(b, f[i], zz);
     } else {
@@ -538,11 +557,11 @@ cudaError_t with_shape(int E, bool vec, F f) {
   return f.template operator()<32, 8, 1>();
 }
 
-// Tokens a block takes so that there are about `blocks` of them: 32 to 256, in
-// whole rounds of eight groups.
-int chunk_tokens(int T, int blocks) {
+// Tokens a block takes so that there are about `blocks` of them: 32 to `most`,
+// in whole rounds of eight groups.
+int chunk_tokens(int T, int blocks, int most) {
   const int want = (T + blocks - 1) / blocks;
-  return want <= 32 ? 32 : want >= 256 ? 256 : (want + 7) / 8 * 8;
+  return want <= 32 ? 32 : want >= most ? most : (want + 7) / 8 * 8;
 }
 
 // The workspace has to fit whatever GPU the call runs on: for the shortest chunks.
@@ -565,7 +584,7 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 
 size_t loss_ws_bytes(const moe_router_loss_desc_t* d) {
   const size_t segs = max_segments(d), blocks = (d->E + 31) / 32;
-  return up16(segs * d->E * 4) * 2 + up16(segs * 4) * 2 + up16(d->sequences * blocks * 8) + 16;
+  return up16(segs * d->E * 4) * 2 + up16(segs * 4) * 2 + up16(d->sequences * blocks * 4) + 16;
 }
 
 void fill(LossArgs& a, const moe_router_loss_desc_t* d) {
@@ -583,7 +602,7 @@ struct RunChunks {
   template <int LANES, int N, int VEC>
   cudaError_t operator()() const {
     if (a.chunks > kLossCluster) {
-      k_loss_chunks<LANES, N, VEC, false><<<a.chunks, kLossThreads, 0, s>>>(a);
+      k_loss_chunks<LANES, N, VEC, false><<<a.chunks, kFwdThreads, 0, s>>>(a);
       return cudaGetLastError();
     }
     cudaLaunchAttribute attr;
@@ -592,7 +611,7 @@ struct RunChunks {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.chunks);
-    cfg.blockDim = dim3(kLossThreads);
+    cfg.blockDim = dim3(kFwdThreads);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -605,7 +624,7 @@ struct RunBwd {
   cudaStream_t s;
   template <int LANES, int N, int VEC>
   cudaError_t operator()() const {
-    k_loss_bwd<LANES, N, VEC><<<a.chunks, kLossThreads, 0, s>>>(a);
+    k_loss_bwd<LANES, N, VEC><<<a.chunks, kBwdThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
 };
@@ -653,7 +672,7 @@ moe_status_t moe_router_loss_fwd(const moe_router_loss_desc_t* desc, const float
   a.tokens = tokens;
   a.probs = probs;
   a.loss = loss;
-  a.chunk = chunk_tokens(a.T, 4 * sms);
+  a.chunk = chunk_tokens(a.T, sms, kFwdMostTokens);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
   const size_t segs = max_segments(desc);
   const int e_blocks = (a.E + 31) / 32;
@@ -667,7 +686,7 @@ moe_status_t moe_router_loss_fwd(const moe_router_loss_desc_t* desc, const float
   a.seg_count = reinterpret_cast<int32_t*>(take(segs * a.E * 4));
   a.seg_z = reinterpret_cast<float*>(take(segs * 4));
   a.seg_tokens = reinterpret_cast<int32_t*>(take(segs * 4));
-  a.term = reinterpret_cast<double*>(take(static_cast<size_t>(a.S) * e_blocks * 8));
+  a.term = reinterpret_cast<float*>(take(static_cast<size_t>(a.S) * e_blocks * 4));
   a.done = reinterpret_cast<unsigned int*>(take(4));
   // (without tokens one empty chunk, which writes the zeros)
   if (a.chunks == 0) a.chunks = 1;
@@ -717,7 +736,7 @@ moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float
   a.topk_w = topk_w;
   a.topk_idx = topk_idx;
   a.dlogits = dlogits;
-  a.chunk = chunk_tokens(a.T, 8 * sms);
+  a.chunk = chunk_tokens(a.T, 8 * sms, 256);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
   const bool vec = a.E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
   return with_shape(a.E, vec, RunBwd{a, stream}) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
