@@ -10,24 +10,32 @@
 // Numbers.  The operands of the products are fp16: X is bounded (its singular
 // values stay below 2, see the descriptor's checks), so fp16's 11 bits serve,
 // where bf16's 8 would leave an error of one to several percent.  The powers of
-// two kScaleA, kScaleB and 2^x_exp keep them clear of fp16's subnormals.  The
+// two kScaleA and 2^x_exp keep A and X clear of fp16's subnormals.  The
 // state X is held in 32 bits, as the fp16 operand and the fp16 of what it
 // leaves: a X is exact, and the operand's rounding E enters only through B E,
-// which lies in X's own row space -- a direction that X does not have stays
+// which lies in X's own column space -- a direction that X does not have stays
 // empty, where a rounded state would fill it and grow by a each step (3.44 by
 // default: 485 over five).  In the last two steps B is held as B - s I with
 // s = tr(B)/m and X' = (a + s) X + (B - s I) X: near the end B's eigenvalues
 // crowd around s, so the rounded part is small.  Not earlier, where E would get
 // into the empty directions through s.
 //
-// The products run on CTA pairs (2-SM MMA), 256 x 256 tiles, as the weight
-// gradients of moe_gemm.cu: warp 0 of each CTA feeds a ring of five 32 KB stages
-// by TMA, warp 1 of the lead issues the MMAs, eight warps read the accumulators
-// of the tile before.
+// All products of all steps are one launch.  Its work is a list of 256 x 256
+// tiles: group of matrices by group, step by step, in a step A's tiles of every
+// matrix, then B's, then X's, dealt out to the CTA pairs in turn.  A tile waits only for its own matrix's
+// tiles of the product before, by a counter: those stand earlier in the list, so
+// with every pair resident (a cooperative launch) each wait ends, and with a few
+// matrices they are done long before, so that no product ends in a wave that is
+// half empty (32 matrices of 7168 x 2048: 15 launches took 15.7 ms).
+//
+// A pair works as the weight gradients of moe_gemm.cu do (2-SM MMA): warp 0 of
+// each CTA feeds a ring of 32 KB stages by TMA, warp 1 of the lead issues the
+// MMAs, eight warps read the accumulators of the tile before.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include "moe_f2.cuh"
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -43,13 +51,14 @@ constexpr int kBoxBytes = 64 * kBK * 2;
 constexpr int kTmemCols = 2 * kTile;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kEpiBarrier = 1;
-constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes;
+constexpr int kMirrorPitch = 40;               // halves from one mirrored row to the next
+constexpr int kMirrorBytes = 16 * kMirrorPitch * 2;   // 16 x 32 of a tile, a warp
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
+                         kEpiWarps * kMirrorBytes;
 constexpr int kMaxSide = 16384;
 constexpr int kMaxSteps = 16;
 constexpr int kNormParts = 64;                 // most blocks that share a matrix in the norm
 constexpr float kScaleA = 4096.0f;             // A's entries are at most 4
-constexpr float kScaleB = 2048.0f;             // B's at most 16
 
 // kind::f16 with fp16 A and B, fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -59,55 +68,146 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
 
 enum Product : int {
   kGram = 0,     // A = X X^T (or X^T X), upper tiles, mirrored
-  kPoly = 1,     // B = b A + c A A, upper tiles, mirrored
-  kUpdate = 2,   // X' = a X + B X (or a X + X B)
+  kPoly = 1,     // B = b A + c A A - s I, upper tiles, mirrored
+  kUpdate = 2,   // X' = (a + s) X + B X (or X B)
   kLast = 3      // the same into the caller's tensor
 };
 
 struct OrthoArgs {
-  CUtensorMap ta;              // first operand, [batch][.][.]
-  CUtensorMap tb;
-  int batch, M, N, K;          // output rows and columns, contraction
-  __half* out_h;               // A, B or X' (operand), rows ld_h apart
-  long long ld_h, plane_h;
+  CUtensorMap x_k[2], x_mn[2]; // both X buffers, 64 x 128 boxes and 64 x 64 boxes
+  CUtensorMap map_a, map_b;
+  __half* x[2];                // [batch][rows][ld_x]
   __half* x_lo;                // the state's lower half, in place
-  const __half* in_h;          // kPoly: A; kUpdate: X
-  float* part;                 // kGram: (sum of A_ii, of A_ij^2) by tile, CTA and warp
-  float* shift;                // [batch] the s of B - s I
-  int use_shift;
-  int m;                       // the small side
-  float acc_scale;             // accumulator -> what is stored
-  float b, c;                  // kPoly
-  float a, to_out;             // kUpdate, kLast: X's coefficient, and what all is scaled by
-  // kLast: the caller's tensor
+  __half* mat_a;               // [batch][m][ld_a]
+  __half* mat_b;
+  long long ld_x, plane_x, ld_a, plane_a;
+  int batch, rows, cols, m, steps;
+  int groups;                  // of matrices that go through the steps together
+  int tall;                    // more rows than columns: A = X^T X, X' = X B
+  float* part;                 // [batch][tiles of A][2 CTAs][8 warps]: sums of A_ii, A_ij^2
+  float* shift;                // [batch] s
+  unsigned int* done;          // [batch][3] finished warps' shares of A's, B's, X's tiles
+  float a, b, c;
+  float x_scale, scale;
   __nv_bfloat16* out;
   long long ld_out, plane_out;
-  int out_vec;                 // rows may be written 8 elements at a time
+  int out_vec;                 // out's rows may be written 16 elements at a time
   int* status;
 };
 
-struct TileAt {
-  int z, mb, nb;
+// One tile of the list.
+struct Work {
+  int op, step, z, mb, nb;
 };
 
-// Tile t: matrix after matrix; symmetric products by columns nb of 1, 2, ...
-// tiles mb <= nb.
-template <bool SYM>
-__device__ __forceinline__ TileAt tile_at(int t, int per, int m_tiles) {
-  TileAt w;
-  w.z = t / per;
-  const int r = t - w.z * per;
-  if constexpr (SYM) {
+// The list's shape.
+struct Plan {
+  int m_tiles, r_tiles, c_tiles;   // of the small side, X's rows and columns
+  int sym, full;                   // tiles of A (and B) and of X
+  int per_matrix, total;           // of one matrix in a step, of all
+};
+
+__device__ __forceinline__ Plan plan_of(const OrthoArgs& g) {
+  Plan p;
+  p.m_tiles = (g.m + kTile - 1) / kTile;
+  p.r_tiles = (g.rows + kTile - 1) / kTile;
+  p.c_tiles = (g.cols + kTile - 1) / kTile;
+  p.sym = p.m_tiles * (p.m_tiles + 1) / 2;
+  p.full = p.r_tiles * p.c_tiles;
+  p.per_matrix = 2 * p.sym + p.full;
+  p.total = g.steps * g.batch * p.per_matrix;
+  return p;
+}
+
+// Symmetric products go by columns nb of 1, 2, ... tiles mb <= nb; X with the
+// small side inside, so that the long side's panel is shared by its neighbours.
+__device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t) {
+  Work w;
+  // group i holds the matrices floor(i batch / groups) and on
+  const int share = g.steps * p.per_matrix;
+  const int q = t / share;
+  const int i = static_cast<int>((static_cast<long long>(q + 1) * g.groups - 1) / g.batch);
+  const int z0 = static_cast<int>(static_cast<long long>(i) * g.batch / g.groups);
+  const int z1 = static_cast<int>(static_cast<long long>(i + 1) * g.batch / g.groups);
+  int r = t - z0 * share;
+  const int per_step = (z1 - z0) * p.per_matrix;
+  w.step = r / per_step;
+  r -= w.step * per_step;
+  const int sym = (z1 - z0) * p.sym;
+  if (r < 2 * sym) {
+    w.op = r < sym ? kGram : kPoly;
+    r -= w.op == kGram ? 0 : sym;
+    const int z = r / p.sym;
+    w.z = z0 + z;
+    r -= z * p.sym;
     int nb = static_cast<int>((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
     while (nb * (nb + 1) / 2 > r) --nb;
     while ((nb + 1) * (nb + 2) / 2 <= r) ++nb;
     w.nb = nb;
     w.mb = r - nb * (nb + 1) / 2;
   } else {
-    w.nb = r / m_tiles;
-    w.mb = r - w.nb * m_tiles;
+    w.op = w.step + 1 == g.steps ? kLast : kUpdate;
+    r -= 2 * sym;
+    const int z = r / p.full;
+    w.z = z0 + z;
+    r -= z * p.full;
+    const int inside = g.tall ? p.c_tiles : p.r_tiles;
+    const int outside = r / inside;
+    r -= outside * inside;
+    w.mb = g.tall ? outside : r;
+    w.nb = g.tall ? r : outside;
   }
   return w;
+}
+
+// Contraction length, columns that the tile's MMAs compute (a multiple of 32, or
+// of 128 where the second operand lies along its rows), and the operands' ways to
+// lie.
+struct Shape {
+  int num_kb, n_eff;
+  bool a_mn, b_mn;
+};
+
+__device__ __forceinline__ Shape shape_of(const OrthoArgs& g, const Work& w) {
+  Shape s;
+  const bool gram = w.op == kGram, update = w.op >= kUpdate;
+  s.a_mn = gram && g.tall;
+  s.b_mn = (gram && g.tall) || (update && !g.tall);
+  const int K = gram ? (g.tall ? g.rows : g.cols) : g.m;
+  s.num_kb = (K + kBK - 1) / kBK;
+  const int left = (update ? g.cols : g.m) - w.nb * kTile;
+  const int unit = s.b_mn ? 128 : 32;
+  s.n_eff = min(kTile, (left + unit - 1) / unit * unit);
+  return s;
+}
+
+// Waits until the tiles that w reads are finished; false when that takes too long
+// or the CTA has given up.
+__device__ __forceinline__ bool wait_inputs(const OrthoArgs& g, const Plan& p, const Work& w,
+                                            volatile int* abort_flag) {
+  if (w.op == kGram && w.step == 0) return true;
+  const unsigned int share = 2 * kEpiWarps;
+  const unsigned int* ctr = g.done + 3 * w.z + (w.op == kGram ? 2 : w.op == kPoly ? 0 : 1);
+  const unsigned int target =
+      share * (w.op == kGram ? w.step * p.full : (w.step + 1) * p.sym);
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+  if (v < target) {
+    const unsigned long long t0 = global_ns();
+    while (true) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+      if (v >= target) break;
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        set_status(g.status, MOE_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  // what other SMs stored is now read by TMA
+  asm volatile("fence.proxy.async;" ::: "memory");
+  return true;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -115,28 +215,18 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void store_half16(__half* dst, const float (&v)[16]) {
-  uint4* p = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    p[q] = make_uint4(pack_half2(v[8 * q], v[8 * q + 1]), pack_half2(v[8 * q + 2], v[8 * q + 3]),
-                      pack_half2(v[8 * q + 4], v[8 * q + 5]),
-                      pack_half2(v[8 * q + 6], v[8 * q + 7]));
+// 32 bytes, past L1 (other SMs write them in the same launch).
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
 }
 
-__device__ __forceinline__ void load_half16(const __half* src, float (&v)[16]) {
-  const uint4* p = reinterpret_cast<const uint4*>(src);
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint4 w = p[q];
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      v[8 * q + 2 * i] = f.x;
-      v[8 * q + 2 * i + 1] = f.y;
-    }
-  }
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // s of matrix z from kGram's sums, by one warp: tr(B) / m = (b tr(A) + c |A|^2) / m.
@@ -156,11 +246,182 @@ __device__ __forceinline__ float shift_of(const OrthoArgs& g, int z, int parts, 
   return (g.b * tr + g.c * sq) / static_cast<float>(g.m);
 }
 
-template <int OP, bool AMN, bool BMN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    k_ortho_gemm(const __grid_constant__ OrthoArgs g) {
+// A pair of fp16 as two fp32 in one operand of the packed arithmetic.
+__device__ __forceinline__ F2 half_pair(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2(f.x, f.y);
+}
+
+__device__ __forceinline__ uint32_t pack_half(F2 v) {
+  const float2 f = parts(v);
+  return pack_half2(f.x, f.y);
+}
+
+// One warp's share of a tile: 32 rows, 16 of every 32 columns.  The loads of the
+// state (or of A) run kAhead chunks ahead; `read` is called once the accumulator
+// has been read.
+constexpr int kAhead = 4;
+
+template <int OP, typename READ>
+__device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, const Work& w,
+                                         uint32_t tbase, int row0, int col0, int lane, int ewarp,
+                                         uint32_t rank, __half* mirror_buf, READ read) {
   constexpr bool kSym = OP == kGram || OP == kPoly;
-  constexpr uint32_t kIdesc = idesc_f16(kTile, kTile, AMN, BMN);
+  constexpr bool kState = OP == kUpdate || OP == kLast;
+  const int M = kSym ? g.m : g.rows, N = kSym ? g.m : g.cols;
+  const int row = row0 + lane;
+  const bool live = row < M;
+  const bool mirror = kSym && w.mb != w.nb;
+  const bool shifted = w.step + 2 >= g.steps;
+  const int nch = min(kTile / 32, (N - col0 + 31) / 32);   // may be <= 0
+  const long long ld = kSym ? g.ld_a : g.ld_x;
+  const long long at0 = static_cast<long long>(w.z) * (kSym ? g.plane_a : g.plane_x) + row * ld +
+                        col0;
+  // v = keep * (what was loaded) + accumulator, where not kGram; then * scale
+  float s = 0.0f, keep = 0.0f, scale = 1.0f;
+  if constexpr (OP == kGram) {
+    scale = kScaleA / (g.x_scale * g.x_scale);
+  } else if constexpr (OP == kPoly) {
+    scale = g.c / (kScaleA * kScaleA);
+    keep = g.b / kScaleA;
+    if (shifted && w.mb == w.nb) {
+      s = shift_of(g, w.z, p.sym * 2 * kEpiWarps, lane);
+      if (w.mb == 0 && rank == 0 && ewarp == 0 && lane == 0) g.shift[w.z] = s;
+    }
+  } else {
+    keep = g.a + (shifted ? __ldcg(g.shift + w.z) : 0.0f);
+    if constexpr (OP == kLast) scale = g.scale / g.x_scale;
+  }
+  const F2 keep2 = f2(keep), scale2 = f2(scale);
+  const __half* src = OP == kPoly ? g.mat_a : g.x[w.step & 1];
+  __half* dst = OP == kGram ? g.mat_a : OP == kPoly ? g.mat_b : g.x[(w.step + 1) & 1];
+  constexpr int kBuf = OP == kGram ? 1 : kAhead;
+  uint32_t hi[kBuf][8] = {}, lo[kState ? kBuf : 1][8] = {};
+  float tr = 0.0f, sq = 0.0f;
+
+  auto fetch = [&](int j, int b) {
+    if constexpr (OP != kGram) {
+      if (live && j < nch) {
+        load32(src + at0 + 32 * j, hi[b]);
+        if constexpr (kState) load32(g.x_lo + at0 + 32 * j, lo[b]);
+      }
+    }
+  };
+  auto chunk = [&](int j, int b) {
+    const int col = col0 + 32 * j;
+    uint32_t acc[16];
+    tmem_ld16(tbase + 32 * j, acc);
+    tmem_ld_wait16(acc);
+    if (j + 1 == nch) read();
+    F2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = f2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
+      if constexpr (OP == kPoly) v[i] = v[i] * scale2;
+      if constexpr (OP != kGram) v[i] = fma2(keep2, half_pair(hi[b][i]), v[i]);
+      if constexpr (kState) v[i] = fma2(keep2, half_pair(lo[b][i]), v[i]);
+      if constexpr (OP == kGram || OP == kLast) v[i] = v[i] * scale2;
+    }
+    if constexpr (OP == kPoly) {
+      if (s != 0.0f && w.mb == w.nb) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = parts(v[i]);
+          v[i] = f2(col + 2 * i == row ? f.x - s : f.x, col + 2 * i + 1 == row ? f.y - s : f.y);
+        }
+      }
+    }
+    fetch(j + kAhead, b);
+    uint32_t h[8];
+    if constexpr (OP != kLast) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = pack_half(v[i]);
+      if (live) store32(dst + at0 + 32 * j, h);
+    }
+    if constexpr (OP == kGram) {
+      if (shifted) {             // of what is stored, within the matrix
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 q = parts(half_pair(h[i]));
+          const float x = live && col + 2 * i < N ? q.x * (1.0f / kScaleA) : 0.0f;
+          const float y = live && col + 2 * i + 1 < N ? q.y * (1.0f / kScaleA) : 0.0f;
+          sq = fmaf(x, x, fmaf(y, y, sq));
+          if (col + 2 * i == row) tr += x;
+          if (col + 2 * i + 1 == row) tr += y;
+        }
+      }
+    }
+    if constexpr (OP == kUpdate) {
+      uint32_t l[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l[i] = pack_half(fma2(f2(-1.0f), half_pair(h[i]), v[i]));
+      if (live) store32(g.x_lo + at0 + 32 * j, l);
+    }
+    if constexpr (kSym) {
+      if (mirror) {              // 16 columns of 32 rows become 16 rows of 32
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2 two = *reinterpret_cast<const __half2*>(&h[i]);
+          mirror_buf[(2 * i) * kMirrorPitch + lane] = __low2half(two);
+          mirror_buf[(2 * i + 1) * kMirrorPitch + lane] = __high2half(two);
+        }
+        __syncwarp();
+        const int r = lane >> 1, c = 16 * (lane & 1);
+        const uint4* q = reinterpret_cast<const uint4*>(mirror_buf + r * kMirrorPitch + c);
+        const uint4 q0 = q[0], q1 = q[1];
+        const uint32_t t[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        if (col + r < N && row0 + c < M)
+          store32(dst + static_cast<long long>(w.z) * g.plane_a + (col + r) * ld + row0 + c, t);
+        __syncwarp();
+      }
+    }
+    if constexpr (OP == kLast) {
+      if (live) {
+        __nv_bfloat16* o = g.out + static_cast<long long>(w.z) * g.plane_out + row * g.ld_out + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = parts(v[i]);
+          h[i] = pack_bf16x2(f.x, f.y);
+        }
+        if (g.out_vec && col + 16 <= N) {
+          store32(o, h);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (col + i < N)
+              reinterpret_cast<uint16_t*>(o)[i] = static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  };
+
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) fetch(b, kBuf > 1 ? b : 0);
+  if (nch <= 0) read();
+#pragma unroll 1
+  for (int j = 0; j < nch; j += kAhead) {
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b)
+      if (j + b < nch) chunk(j + b, kBuf > 1 ? b : 0);
+  }
+  if constexpr (OP == kGram) {
+    if (shifted) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        tr += __shfl_xor_sync(0xFFFFFFFFu, tr, o);
+        sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+      }
+      const int tile = w.nb * (w.nb + 1) / 2 + w.mb;
+      if (lane == 0)
+        reinterpret_cast<float2*>(g.part)[((static_cast<long long>(w.z) * p.sym + tile) * 2 + rank) *
+                                              kEpiWarps + ewarp] =
+            make_float2(tr, mirror ? 2.0f * sq : sq);
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_ortho_steps(const __grid_constant__ OrthoArgs g) {
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
   __shared__ __align__(8) uint64_t empty_bar[kStages];
@@ -194,26 +455,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();                            // peer barriers initialised before any remote use
   tc_fence_after();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort_flag = &s_abort;
-  const int m_tiles = (g.M + kTile - 1) / kTile, n_tiles = (g.N + kTile - 1) / kTile;
-  const int per = kSym ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
-  const int total = per * g.batch;
-  const int num_kb = (g.K + kBK - 1) / kBK;
+  const Plan p = plan_of(g);
 
   if (warp == 0) {
     // ====================== TMA producer (both CTAs) ======================
     if (lane == 0) {
-      tma_prefetch_desc(&g.ta);
-      tma_prefetch_desc(&g.tb);
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
-        const TileAt w = tile_at<kSym>(t, per, m_tiles);
+      for (int t = pair; t < p.total && ok; t += npairs) {
+        const Work w = work_at(g, p, t);
+        const Shape sh = shape_of(g, w);
+        const int now = w.step & 1;
+        const CUtensorMap* ta = &g.map_a;
+        const CUtensorMap* tb = &g.map_a;
+        if (w.op == kGram) {
+          ta = tb = g.tall ? &g.x_mn[now] : &g.x_k[now];
+        } else if (w.op != kPoly) {
+          ta = g.tall ? &g.x_k[now] : &g.map_b;
+          tb = g.tall ? &g.map_b : &g.x_mn[now];
+        }
         const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
-        const int n0 = w.nb * kTile + 128 * static_cast<int>(rank);
-        for (int kb = 0; kb < num_kb; ++kb) {
+        const int n0 = w.nb * kTile + (sh.n_eff / 2) * static_cast<int>(rank);
+        ok = wait_inputs(g, p, w, abort_flag);
+        for (int kb = 0; kb < sh.num_kb && ok; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, g.status, abort_flag)) {
             ok = false;
             break;
@@ -224,17 +490,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // boxes past a tensor's end are filled with zeros and count whole
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStageBytes);
           const int k0 = kb * kBK;
-          if constexpr (AMN) {
-            tma_load_3d_pair(sa, &g.ta, fb, m0, k0, w.z);
-            tma_load_3d_pair(sa + kBoxBytes, &g.ta, fb, m0 + 64, k0, w.z);
+          if (sh.a_mn) {
+            tma_load_3d_pair(sa, ta, fb, m0, k0, w.z);
+            tma_load_3d_pair(sa + kBoxBytes, ta, fb, m0 + 64, k0, w.z);
           } else {
-            tma_load_3d_pair(sa, &g.ta, fb, k0, m0, w.z);
+            tma_load_3d_pair(sa, ta, fb, k0, m0, w.z);
           }
-          if constexpr (BMN) {
-            tma_load_3d_pair(sb, &g.tb, fb, n0, k0, w.z);
-            tma_load_3d_pair(sb + kBoxBytes, &g.tb, fb, n0 + 64, k0, w.z);
+          if (sh.b_mn) {
+            tma_load_3d_pair(sb, tb, fb, n0, k0, w.z);
+            tma_load_3d_pair(sb + kBoxBytes, tb, fb, n0 + 64, k0, w.z);
           } else {
-            tma_load_3d_pair(sb, &g.tb, fb, k0, n0, w.z);
+            tma_load_3d_pair(sb, tb, fb, k0, n0, w.z);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -249,13 +515,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t stage = 0, phase = 0;
       int it = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs, ++it) {
+      for (int t = pair; t < p.total && ok; t += npairs, ++it) {
+        const Work w = work_at(g, p, t);
+        const Shape sh = shape_of(g, w);
+        const uint32_t idesc = idesc_f16(kTile, sh.n_eff, sh.a_mn, sh.b_mn);
         const int acc = it & 1;
         const uint32_t acc_par = (it >> 1) & 1;
         if (!mbar_wait(&tempty_bar[acc], acc_par ^ 1u, g.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kTile;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = 0; kb < sh.num_kb; ++kb) {
           if (!mbar_wait(&full_bar[stage], phase, g.status, abort_flag)) {
             ok = false;
             break;
@@ -265,11 +534,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t b_base = a_base + kHalfBytes;
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t ad = AMN ? sdesc_sw128(a_base + k * 2048, kBoxBytes, 1024)
-                                    : sdesc_sw128(a_base + k * 32, 16, 1024);
-            const uint64_t bd = BMN ? sdesc_sw128(b_base + k * 2048, kBoxBytes, 1024)
-                                    : sdesc_sw128(b_base + k * 32, 16, 1024);
-            umma_bf16_pair(d_tmem, ad, bd, kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
+            const uint64_t ad = sh.a_mn ? sdesc_sw128(a_base + k * 2048, kBoxBytes, 1024)
+                                        : sdesc_sw128(a_base + k * 32, 16, 1024);
+            const uint64_t bd = sh.b_mn ? sdesc_sw128(b_base + k * 2048, kBoxBytes, 1024)
+                                        : sdesc_sw128(b_base + k * 32, 16, 1024);
+            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
           }
           umma_commit_pair(&empty_bar[stage]);
           if (++stage == kStages) {
@@ -284,119 +553,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ====================== epilogue (both CTAs) ==========================
     // eight warps, two per TMEM lane quarter, 16 of every 32 columns each
-    const int quarter = warp & 3;
-    const int hc = 16 * ((warp - 2) >> 2);
+    const int quarter = warp & 3, ewarp = warp - 2;
+    const int hc = 16 * (ewarp >> 2);
+    __half* mirror_buf = reinterpret_cast<__half*>(smem + kStages * kStageBytes) +
+                         ewarp * (kMirrorBytes / 2);
     int it = 0;
-    for (int t = pair; t < total; t += npairs, ++it) {
-      const TileAt w = tile_at<kSym>(t, per, m_tiles);
-      const int row = w.mb * kTile + 128 * static_cast<int>(rank) + quarter * 32 + lane;
-      const int n0 = w.nb * kTile + hc;
+    for (int t = pair; t < p.total; t += npairs, ++it) {
+      const Work w = work_at(g, p, t);
+      const int row0 = w.mb * kTile + 128 * static_cast<int>(rank) + quarter * 32;
+      const int col0 = w.nb * kTile + hc;
       const int acc = it & 1;
       const uint32_t acc_par = (it >> 1) & 1;
-      const bool mirror = kSym && w.mb != w.nb;
-      const bool live = row < g.M;
-      float keep = OP == kUpdate || OP == kLast ? g.a : 0.0f;
-      float s = 0.0f;
-      if constexpr (OP == kUpdate || OP == kLast) {
-        if (g.use_shift) keep += __ldcg(g.shift + w.z);
-        keep *= g.to_out;
-      }
-      if constexpr (OP == kPoly) {
-        if (g.use_shift && w.mb == w.nb) {
-          s = shift_of(g, w.z, per * 2 * kEpiWarps, lane);
-          if (w.mb == 0 && rank == 0 && warp == 2 && lane == 0) g.shift[w.z] = s;
-        }
-      }
       int ok = 1;
       if (lane == 0) ok = mbar_wait(&tfull_bar[acc], acc_par, g.status, abort_flag);
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTile + hc;
-      const int nch = min(kTile / 32, (g.N - n0 + 31) / 32);   // of this warp's columns; may be <= 0
-      float tr = 0.0f, sq = 0.0f;
-      uint32_t r[16];
-#pragma unroll 1
-      for (int j = 0; j < nch; ++j) {
-        tmem_ld16(tbase + 32 * j, r);
-        const int col = n0 + 32 * j;
-        float in[16], lo[16], v[16];
-        const long long at = static_cast<long long>(w.z) * g.plane_h + row * g.ld_h + col;
-        if constexpr (OP != kGram) {
-          if (live) load_half16(g.in_h + at, in);
-          if constexpr (OP != kPoly) {
-            if (live) load_half16(g.x_lo + at, lo);
-          }
-        }
-        tmem_ld_wait16(r);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float x = __uint_as_float(r[i]) * g.acc_scale;
-          if constexpr (OP == kGram) {
-            v[i] = x;
-          } else if constexpr (OP == kPoly) {
-            v[i] = fmaf(in[i], g.b * (kScaleB / kScaleA), x);
-            if (col + i == row) v[i] -= s * kScaleB;
-          } else {
-            v[i] = fmaf(keep, in[i] + lo[i], x);
-          }
-        }
-        if constexpr (OP == kGram) {
-          // of what is stored, within the matrix
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i] = __half2float(__float2half_rn(v[i]));
-            const float x = live && col + i < g.N ? v[i] * (1.0f / kScaleA) : 0.0f;
-            sq = fmaf(x, x, sq);
-            if (col + i == row) tr += x;
-          }
-        }
-        if (live) {
-          if constexpr (kSym) {
-            store_half16(g.out_h + at, v);
-            if (mirror) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (col + i < g.N)
-                  g.out_h[static_cast<long long>(w.z) * g.plane_h + (col + i) * g.ld_h + row] =
-                      __float2half_rn(v[i]);
-            }
-          } else if constexpr (OP == kUpdate) {
-            store_half16(g.out_h + at, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) lo[i] = v[i] - __half2float(__float2half_rn(v[i]));
-            store_half16(g.x_lo + at, lo);
-          } else {
-            __nv_bfloat16* dst = g.out + static_cast<long long>(w.z) * g.plane_out +
-                                 row * g.ld_out + col;
-            if (g.out_vec && col + 16 <= g.N) {
-              uint4* p = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                p[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                                  pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                  pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                                  pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (col + i < g.N) dst[i] = __float2bfloat16_rn(v[i]);
-            }
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-      if constexpr (OP == kGram) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          tr += __shfl_xor_sync(0xFFFFFFFFu, tr, o);
-          sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-        }
+      const uint32_t tbase =
+          tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTile + hc;
+      auto read = [&]() {                    // the accumulator is free again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+      };
+      if (w.op == kGram)
+        epilogue<kGram>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+      else if (w.op == kPoly)
+        epilogue<kPoly>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+      else if (w.op == kUpdate)
+        epilogue<kUpdate>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+      else
+        epilogue<kLast>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+      if (w.op != kLast) {
+        // the tile's stores, before the count that tells of them (TMA reads them)
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
         if (lane == 0)
-          reinterpret_cast<float2*>(g.part)[(static_cast<long long>(t) * 2 + rank) * kEpiWarps +
-                                            warp - 2] = make_float2(tr, mirror ? 2.0f * sq : sq);
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.done + 3 * w.z + w.op)
+                       : "memory");
       }
     }
   }
@@ -429,6 +623,7 @@ struct PrepArgs {
   __half* x_hi;
   __half* x_lo;
   long long ld_x, plane_x;
+  unsigned int* done;          // [batch][3], set to zero
 };
 
 // U's elements c .. c+n-1 of a row (n <= 8), and where asked the new momentum.
@@ -501,8 +696,8 @@ __device__ __forceinline__ void update_of(const PrepArgs& p, int z, int r, int c
 template <bool F32>
 __global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
   __shared__ double s_sum[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int z = blockIdx.y;
+  if (blockIdx.x == 0 && threadIdx.x < 3) p.done[3 * z + threadIdx.x] = 0;
   const int units = (p.cols + 7) / 8;
   const long long count = static_cast<long long>(p.rows) * units;
   double sum = 0.0;
@@ -535,7 +730,6 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
 // X = U / (|U| + eps) as fp16 and the fp16 of the rest.
 template <bool F32>
 __global__ void __launch_bounds__(256) k_ortho_start(const PrepArgs p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int z = blockIdx.y;
   double sum = 0.0;
   for (int i = threadIdx.x & 31; i < p.parts; i += 32)
@@ -620,7 +814,7 @@ struct Layout {
   int m;                                   // the small side
   long long ld_x, plane_x, ld_a, plane_a;  // elements
   int parts;                               // kGram's sums of a matrix
-  size_t x0, x1, lo, a, b, part, norm, shift, bytes;
+  size_t x0, x1, lo, a, b, part, norm, shift, done, bytes;
 };
 
 Layout layout_of(const moe_orthogonalize_desc_t* d) {
@@ -647,23 +841,37 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   w.part = take(n * w.parts * 8);
   w.norm = take(n * kNormParts * 8);
   w.shift = take(n * 4);
+  w.done = take(n * 12);
   w.bytes = at > 0 ? at : 256;
   return w;
 }
 
-template <int OP, bool AMN, bool BMN>
-cudaError_t launch_product(const OrthoArgs& g, int sms, cudaStream_t s) {
-  cudaError_t err = cudaFuncSetAttribute(k_ortho_gemm<OP, AMN, BMN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+bool operand_map(CUtensorMap* map, const void* p, long long cols, long long rows, long long batch,
+                 long long ld, long long plane, bool mn) {
+  return encode_map_3d(map, p, cols, rows, batch, ld * 2, plane * 2, 64, mn ? 64 : 128,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+}
+
+// Every pair stays until the list's end and waits for others' tiles: a
+// cooperative launch, so that all are resident.
+cudaError_t launch_steps(OrthoArgs& g, int sms, cudaStream_t s) {
+  cudaError_t err = cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
-  const long long mt = (g.M + kTile - 1) / kTile, nt = (g.N + kTile - 1) / kTile;
-  const long long tiles =
-      g.batch * (OP == kGram || OP == kPoly ? mt * (mt + 1) / 2 : mt * nt);
-  const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
+  const long long mt = (g.m + kTile - 1) / kTile;
+  const long long full = static_cast<long long>((g.rows + kTile - 1) / kTile) *
+                         ((g.cols + kTile - 1) / kTile);
+  const long long most = g.batch * (full > mt * (mt + 1) / 2 ? full : mt * (mt + 1) / 2);
+  const long long pairs = most < sms / 2 ? most : sms / 2;
+  // together as many matrices as give A's product two tiles a pair: then a
+  // product's inputs are done by the time the list comes to it, and no more
+  // matrices than that take turns in L2
+  const long long sym = mt * (mt + 1) / 2;
+  const long long together = (2 * pairs + sym - 1) / sym;
+  g.groups = static_cast<int>(g.batch > together ? g.batch / together : 1);
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(kThreads);
@@ -671,13 +879,7 @@ cudaError_t launch_product(const OrthoArgs& g, int sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_ortho_gemm<OP, AMN, BMN>, g);
-}
-
-bool operand_map(CUtensorMap* map, const void* p, long long cols, long long rows, long long batch,
-                 long long ld, long long plane, bool mn) {
-  return encode_map_3d(map, p, cols, rows, batch, ld * 2, plane * 2, 64, mn ? 64 : 128,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+  return cudaLaunchKernelEx(&cfg, k_ortho_steps, g);
 }
 
 struct Tensor {
@@ -728,6 +930,9 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
     if ((st = Tensor{mom_out, 4}.check(desc, &vec)) != MOE_OK) return st;
   }
   if ((st = Tensor{out, 2}.check(desc, &out_vec)) != MOE_OK) return st;
+  if (reinterpret_cast<uintptr_t>(out.p) % 32 || (desc->rows > 1 && out.ld % 16) ||
+      (desc->batch > 1 && out.plane % 16))
+    out_vec = false;
   // a written matrix keeps clear of the next one
   const long long span = static_cast<long long>(desc->rows - 1);
   if (desc->batch > 1 &&
@@ -744,10 +949,7 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
 
   char* base = static_cast<char*>(ws);
   auto half_at = [base](size_t at) { return reinterpret_cast<__half*>(base + at); };
-  __half *x_now = half_at(w.x0), *x_next = half_at(w.x1), *A = half_at(w.a), *B = half_at(w.b);
-  float* part = reinterpret_cast<float*>(base + w.part);
-  float* shift = reinterpret_cast<float*>(base + w.shift);
-  const bool tall = desc->rows > desc->cols;
+  __half* x0 = half_at(w.x0);
   // X times a power of two near sqrt(rows cols), so that its entries are about 1
   // where the norm is 1
   const int x_exp = static_cast<int>(
@@ -777,10 +979,11 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   p.part = reinterpret_cast<double*>(base + w.norm);
   p.eps = desc->eps;
   p.x_scale = x_scale;
-  p.x_hi = x_now;
+  p.x_hi = x0;
   p.x_lo = half_at(w.lo);
   p.ld_x = w.ld_x;
   p.plane_x = w.plane_x;
+  p.done = reinterpret_cast<unsigned int*>(base + w.done);
   const long long units = static_cast<long long>(desc->rows) * ((desc->cols + 7) / 8);
   const long long most = (units + 255) / 256;
   p.parts = static_cast<int>(most < kNormParts ? most : kNormParts);
@@ -797,72 +1000,43 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
 
   OrthoArgs g = {};
-  g.batch = desc->batch;
+  __half* x1 = half_at(w.x1);
+  if (!operand_map(&g.x_k[0], x0, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, false) ||
+      !operand_map(&g.x_k[1], x1, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, false) ||
+      !operand_map(&g.x_mn[0], x0, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true) ||
+      !operand_map(&g.x_mn[1], x1, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true) ||
+      !operand_map(&g.map_a, half_at(w.a), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
+      !operand_map(&g.map_b, half_at(w.b), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false))
+    return MOE_ERR_CUDA;
+  g.x[0] = x0;
+  g.x[1] = x1;
   g.x_lo = p.x_lo;
-  g.part = part;
-  g.shift = shift;
+  g.mat_a = half_at(w.a);
+  g.mat_b = half_at(w.b);
+  g.ld_x = w.ld_x;
+  g.plane_x = w.plane_x;
+  g.ld_a = w.ld_a;
+  g.plane_a = w.plane_a;
+  g.batch = desc->batch;
+  g.rows = desc->rows;
+  g.cols = desc->cols;
   g.m = w.m;
+  g.steps = desc->steps;
+  g.tall = desc->rows > desc->cols;
+  g.part = reinterpret_cast<float*>(base + w.part);
+  g.shift = reinterpret_cast<float*>(base + w.shift);
+  g.done = p.done;
+  g.a = desc->a;
   g.b = desc->b;
   g.c = desc->c;
-  g.status = status;
+  g.x_scale = x_scale;
+  g.scale = desc->scale;
   g.out = static_cast<__nv_bfloat16*>(out.p);
   g.ld_out = out.ld;
   g.plane_out = out.plane;
   g.out_vec = out_vec;
-  for (int step = 0; step < desc->steps; ++step) {
-    const bool last = step + 1 == desc->steps;
-    g.use_shift = step + 2 >= desc->steps;
-    // A
-    g.M = g.N = w.m;
-    g.K = tall ? desc->rows : desc->cols;
-    g.out_h = A;
-    g.ld_h = w.ld_a;
-    g.plane_h = w.plane_a;
-    g.acc_scale = kScaleA / (x_scale * x_scale);
-    if (!operand_map(&g.ta, x_now, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, tall))
-      return MOE_ERR_CUDA;
-    g.tb = g.ta;
-    cudaError_t err = tall ? launch_product<kGram, true, true>(g, sms, stream)
-                           : launch_product<kGram, false, false>(g, sms, stream);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    // B
-    g.K = w.m;
-    g.in_h = A;
-    g.out_h = B;
-    g.acc_scale = desc->c * (kScaleB / (kScaleA * kScaleA));
-    if (!operand_map(&g.ta, A, w.m, w.m, desc->batch, w.ld_a, w.plane_a, false))
-      return MOE_ERR_CUDA;
-    g.tb = g.ta;
-    if (launch_product<kPoly, false, false>(g, sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-    // X
-    g.M = desc->rows;
-    g.N = desc->cols;
-    g.K = w.m;
-    g.in_h = x_now;
-    g.out_h = x_next;
-    g.ld_h = w.ld_x;
-    g.plane_h = w.plane_x;
-    g.a = desc->a;
-    g.to_out = last ? desc->scale / x_scale : 1.0f;
-    g.acc_scale = g.to_out / kScaleB;
-    CUtensorMap bm, xm;
-    if (!operand_map(&bm, B, w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
-        !operand_map(&xm, x_now, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, !tall))
-      return MOE_ERR_CUDA;
-    g.ta = tall ? xm : bm;
-    g.tb = tall ? bm : xm;
-    if (last)
-      err = tall ? launch_product<kLast, false, false>(g, sms, stream)
-                 : launch_product<kLast, false, true>(g, sms, stream);
-    else
-      err = tall ? launch_product<kUpdate, false, false>(g, sms, stream)
-                 : launch_product<kUpdate, false, true>(g, sms, stream);
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    __half* t = x_now;
-    x_now = x_next;
-    x_next = t;
-  }
-  return MOE_OK;
+  g.status = status;
+  return launch_steps(g, sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -130,5 +130,5 @@ def orthogonalize_rounded(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0)
         if step >= steps - 2:
             s = (b * np.trace(A) + c * (A * A).sum()) / len(A)
             B = B - s * np.eye(len(A))
-        x = (a + s) * x + half(B, 2048.0) @ hi
+        x = (a + s) * x + half(B, 1.0) @ hi
     return scale * (x.T if tall else x)
