@@ -11,8 +11,8 @@
 // values stay below 2, see the descriptor's checks), so fp16's 11 bits serve,
 // where bf16's 8 would leave an error of one to several percent.  The powers of
 // two kScaleA and 2^x_exp keep A and X clear of fp16's subnormals.  The
-// state X is held in 32 bits, as the fp16 operand and the fp16 of what it
-// leaves: a X is exact, and the operand's rounding E enters only through B E,
+// state X is held in fp32 beside its operand: a X is exact, and the operand's
+// rounding E enters only through B E,
 // which lies in X's own column space -- a direction that X does not have stays
 // empty, where a rounded state would fill it and grow by a each step (3.44 by
 // default: 485 over five).  In the last two steps B is held as B - s I with
@@ -30,7 +30,11 @@
 //
 // A pair works as the weight gradients of moe_gemm.cu do (2-SM MMA): warp 0 of
 // each CTA feeds a ring of 32 KB stages by TMA, warp 1 of the lead issues the
-// MMAs, eight warps read the accumulators of the tile before.
+// MMAs, eight warps read the accumulators of the tile before.  What bounds it is
+// the tensor pipe with its operands' way through shared memory, which the
+// epilogue's accesses share: the state therefore lies in blocks of 32 rows by 16
+// columns in the order in which a warp's lanes take it, whole lines at a time,
+// where rows 4 KB apart took four times the passes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -44,9 +48,10 @@ namespace {
 
 constexpr int kTile = 256;                     // both sides of a pair's tile
 constexpr int kBK = 64;                        // 64 fp16 = one 128-byte swizzle row
-constexpr int kStages = 6;
-constexpr int kHalfBytes = 128 * kBK * 2;      // one CTA's half of an operand
-constexpr int kStageBytes = 2 * kHalfBytes;
+constexpr int kSub = 2;                        // such blocks of the contraction a stage
+constexpr int kStages = 3;
+constexpr int kHalfBytes = 128 * kBK * 2;      // one CTA's half of an operand's block
+constexpr int kStageBytes = 2 * kSub * kHalfBytes;
 constexpr int kBoxBytes = 64 * kBK * 2;
 constexpr int kTmemCols = 2 * kTile;
 constexpr int kThreads = 320;
@@ -77,10 +82,10 @@ struct OrthoArgs {
   CUtensorMap x_k[2], x_mn[2]; // both X buffers, 64 x 128 boxes and 64 x 64 boxes
   CUtensorMap map_a, map_b;
   __half* x[2];                // [batch][rows][ld_x]
-  __half* x_lo;                // the state's lower half, in place
+  float* state;                // [batch][blocks of 32 x 16], in place
   __half* mat_a;               // [batch][m][ld_a]
   __half* mat_b;
-  long long ld_x, plane_x, ld_a, plane_a;
+  long long ld_x, plane_x, ld_a, plane_a, plane_s;
   int batch, rows, cols, m, steps;
   int groups;                  // of matrices that go through the steps together
   int tall;                    // more rows than columns: A = X^T X, X' = X B
@@ -160,11 +165,11 @@ __device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t
   return w;
 }
 
-// Contraction length, columns that the tile's MMAs compute (a multiple of 32, or
+// Stages of the contraction, columns that the tile's MMAs compute (a multiple of 32, or
 // of 128 where the second operand lies along its rows), and the operands' ways to
 // lie.
 struct Shape {
-  int num_kb, n_eff;
+  int num_st, n_eff;
   bool a_mn, b_mn;
 };
 
@@ -174,7 +179,7 @@ __device__ __forceinline__ Shape shape_of(const OrthoArgs& g, const Work& w) {
   s.a_mn = gram && g.tall;
   s.b_mn = (gram && g.tall) || (update && !g.tall);
   const int K = gram ? (g.tall ? g.rows : g.cols) : g.m;
-  s.num_kb = (K + kBK - 1) / kBK;
+  s.num_st = (K + kSub * kBK - 1) / (kSub * kBK);
   const int left = (update ? g.cols : g.m) - w.nb * kTile;
   const int unit = s.b_mn ? 128 : 32;
   s.n_eff = min(kTile, (left + unit - 1) / unit * unit);
@@ -210,20 +215,26 @@ __device__ __forceinline__ bool wait_inputs(const OrthoArgs& g, const Plan& p, c
   return true;
 }
 
+// Where the state has the first 8 of row r's 16 elements from column c (a
+// multiple of 16) on; the other 8 are 256 further.
+__host__ __device__ inline long long state_at(int col_blocks, int r, int c) {
+  return (static_cast<long long>(r / 32) * col_blocks + c / 16) * 512 + (r % 32) * 8;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // 32 bytes, past L1 (other SMs write them in the same launch).
-__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+__device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
   asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
                  "=r"(w[6]), "=r"(w[7])
                : "l"(p));
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
@@ -293,17 +304,24 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
     if constexpr (OP == kLast) scale = g.scale / g.x_scale;
   }
   const F2 keep2 = f2(keep), scale2 = f2(scale);
-  const __half* src = OP == kPoly ? g.mat_a : g.x[w.step & 1];
+  const __half* src = g.mat_a;
   __half* dst = OP == kGram ? g.mat_a : OP == kPoly ? g.mat_b : g.x[(w.step + 1) & 1];
   constexpr int kBuf = OP == kGram ? 1 : kAhead;
-  uint32_t hi[kBuf][8] = {}, lo[kState ? kBuf : 1][8] = {};
+  uint32_t in[kBuf][kState ? 16 : 8] = {};   // kPoly: A as fp16; the state as fp32
+  float* state = nullptr;
+  if constexpr (kState)
+    state = g.state + w.z * g.plane_s + state_at((N + 15) / 16, row, col0);
   float tr = 0.0f, sq = 0.0f;
 
   auto fetch = [&](int j, int b) {
     if constexpr (OP != kGram) {
       if (live && j < nch) {
-        load32(src + at0 + 32 * j, hi[b]);
-        if constexpr (kState) load32(g.x_lo + at0 + 32 * j, lo[b]);
+        if constexpr (kState) {
+          load_words(state + 1024 * j, &in[b][0]);
+          load_words(state + 1024 * j + 256, &in[b][8]);
+        } else {
+          load_words(src + at0 + 32 * j, &in[b][0]);
+        }
       }
     }
   };
@@ -317,9 +335,10 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = f2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
-      if constexpr (OP == kPoly) v[i] = v[i] * scale2;
-      if constexpr (OP != kGram) v[i] = fma2(keep2, half_pair(hi[b][i]), v[i]);
-      if constexpr (kState) v[i] = fma2(keep2, half_pair(lo[b][i]), v[i]);
+      if constexpr (OP == kPoly) v[i] = fma2(keep2, half_pair(in[b][i]), v[i] * scale2);
+      if constexpr (kState)
+        v[i] = fma2(keep2, f2(__uint_as_float(in[b][2 * i]), __uint_as_float(in[b][2 * i + 1])),
+                    v[i]);
       if constexpr (OP == kGram || OP == kLast) v[i] = v[i] * scale2;
     }
     if constexpr (OP == kPoly) {
@@ -336,7 +355,7 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
     if constexpr (OP != kLast) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[i] = pack_half(v[i]);
-      if (live) store32(dst + at0 + 32 * j, h);
+      if (live) store_words(dst + at0 + 32 * j, h);
     }
     if constexpr (OP == kGram) {
       if (shifted) {             // of what is stored, within the matrix
@@ -352,10 +371,17 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
       }
     }
     if constexpr (OP == kUpdate) {
-      uint32_t l[8];
+      if (live) {
+        float x[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l[i] = pack_half(fma2(f2(-1.0f), half_pair(h[i]), v[i]));
-      if (live) store32(g.x_lo + at0 + 32 * j, l);
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = parts(v[i]);
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        }
+        store32(state + 1024 * j, reinterpret_cast<const float(&)[8]>(x[0]));
+        store32(state + 1024 * j + 256, reinterpret_cast<const float(&)[8]>(x[8]));
+      }
     }
     if constexpr (kSym) {
       if (mirror) {              // 16 columns of 32 rows become 16 rows of 32
@@ -371,7 +397,7 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
         const uint4 q0 = q[0], q1 = q[1];
         const uint32_t t[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
         if (col + r < N && row0 + c < M)
-          store32(dst + static_cast<long long>(w.z) * g.plane_a + (col + r) * ld + row0 + c, t);
+          store_words(dst + static_cast<long long>(w.z) * g.plane_a + (col + r) * ld + row0 + c, t);
         __syncwarp();
       }
     }
@@ -384,7 +410,7 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
           h[i] = pack_bf16x2(f.x, f.y);
         }
         if (g.out_vec && col + 16 <= N) {
-          store32(o, h);
+          store_words(o, h);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -479,28 +505,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
         const int n0 = w.nb * kTile + (sh.n_eff / 2) * static_cast<int>(rank);
         ok = wait_inputs(g, p, w, abort_flag);
-        for (int kb = 0; kb < sh.num_kb && ok; ++kb) {
+        for (int st = 0; st < sh.num_st && ok; ++st) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, g.status, abort_flag)) {
             ok = false;
             break;
           }
           uint8_t* sa = smem + stage * kStageBytes;
-          uint8_t* sb = sa + kHalfBytes;
+          uint8_t* sb = sa + kSub * kHalfBytes;
           const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
           // boxes past a tensor's end are filled with zeros and count whole
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStageBytes);
-          const int k0 = kb * kBK;
-          if (sh.a_mn) {
-            tma_load_3d_pair(sa, ta, fb, m0, k0, w.z);
-            tma_load_3d_pair(sa + kBoxBytes, ta, fb, m0 + 64, k0, w.z);
-          } else {
-            tma_load_3d_pair(sa, ta, fb, k0, m0, w.z);
-          }
-          if (sh.b_mn) {
-            tma_load_3d_pair(sb, tb, fb, n0, k0, w.z);
-            tma_load_3d_pair(sb + kBoxBytes, tb, fb, n0 + 64, k0, w.z);
-          } else {
-            tma_load_3d_pair(sb, tb, fb, k0, n0, w.z);
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            const int k0 = (st * kSub + u) * kBK;
+            if (sh.a_mn) {
+              tma_load_3d_pair(sa + u * kHalfBytes, ta, fb, m0, k0, w.z);
+              tma_load_3d_pair(sa + u * kHalfBytes + kBoxBytes, ta, fb, m0 + 64, k0, w.z);
+            } else {
+              tma_load_3d_pair(sa + u * kHalfBytes, ta, fb, k0, m0, w.z);
+            }
+            if (sh.b_mn) {
+              tma_load_3d_pair(sb + u * kHalfBytes, tb, fb, n0, k0, w.z);
+              tma_load_3d_pair(sb + u * kHalfBytes + kBoxBytes, tb, fb, n0 + 64, k0, w.z);
+            } else {
+              tma_load_3d_pair(sb + u * kHalfBytes, tb, fb, k0, n0, w.z);
+            }
           }
           if (++stage == kStages) {
             stage = 0;
@@ -524,21 +553,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&tempty_bar[acc], acc_par ^ 1u, g.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kTile;
-        for (int kb = 0; kb < sh.num_kb; ++kb) {
+        for (int st = 0; st < sh.num_st; ++st) {
           if (!mbar_wait(&full_bar[stage], phase, g.status, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t a_base = smem_u32(smem + stage * kStageBytes);
-          const uint32_t b_base = a_base + kHalfBytes;
+          const uint32_t b_base = a_base + kSub * kHalfBytes;
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t ad = sh.a_mn ? sdesc_sw128(a_base + k * 2048, kBoxBytes, 1024)
-                                        : sdesc_sw128(a_base + k * 32, 16, 1024);
-            const uint64_t bd = sh.b_mn ? sdesc_sw128(b_base + k * 2048, kBoxBytes, 1024)
-                                        : sdesc_sw128(b_base + k * 32, 16, 1024);
-            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < kSub * kBK / 16; ++k) {
+            const uint32_t ab = a_base + (k / 4) * kHalfBytes, bb = b_base + (k / 4) * kHalfBytes;
+            const uint64_t ad = sh.a_mn ? sdesc_sw128(ab + k % 4 * 2048, kBoxBytes, 1024)
+                                        : sdesc_sw128(ab + k % 4 * 32, 16, 1024);
+            const uint64_t bd = sh.b_mn ? sdesc_sw128(bb + k % 4 * 2048, kBoxBytes, 1024)
+                                        : sdesc_sw128(bb + k % 4 * 32, 16, 1024);
+            umma_bf16_pair(d_tmem, ad, bd, idesc, (st > 0 || k > 0) ? 1u : 0u);
           }
           umma_commit_pair(&empty_bar[stage]);
           if (++stage == kStages) {
@@ -621,8 +651,8 @@ struct PrepArgs {
   int parts;
   float eps, x_scale;          // X is held times x_scale
   __half* x_hi;
-  __half* x_lo;
-  long long ld_x, plane_x;
+  float* state;
+  long long ld_x, plane_x, plane_s;
   unsigned int* done;          // [batch][3], set to zero
 };
 
@@ -727,7 +757,7 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
   }
 }
 
-// X = U / (|U| + eps) as fp16 and the fp16 of the rest.
+// X = U / (|U| + eps), as fp32 and fp16.
 template <bool F32>
 __global__ void __launch_bounds__(256) k_ortho_start(const PrepArgs p) {
   const int z = blockIdx.y;
@@ -745,19 +775,15 @@ __global__ void __launch_bounds__(256) k_ortho_start(const PrepArgs p) {
     const int c = static_cast<int>(i - static_cast<long long>(r) * units) * 8;
     float u[8];
     update_of<F32, false>(p, z, r, c, min(8, p.cols - c), u);
-    float lo[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      u[k] *= mul;
-      lo[k] = u[k] - __half2float(__float2half_rn(u[k]));
-    }
-    const long long at = z * p.plane_x + r * p.ld_x + c;
-    *reinterpret_cast<uint4*>(p.x_hi + at) =
+    for (int k = 0; k < 8; ++k) u[k] *= mul;
+    *reinterpret_cast<uint4*>(p.x_hi + z * p.plane_x + r * p.ld_x + c) =
         make_uint4(pack_half2(u[0], u[1]), pack_half2(u[2], u[3]), pack_half2(u[4], u[5]),
                    pack_half2(u[6], u[7]));
-    *reinterpret_cast<uint4*>(p.x_lo + at) =
-        make_uint4(pack_half2(lo[0], lo[1]), pack_half2(lo[2], lo[3]), pack_half2(lo[4], lo[5]),
-                   pack_half2(lo[6], lo[7]));
+    // (with an odd number of units the last block's second half stays as it is:
+    // what comes of it is not stored)
+    store32(p.state + z * p.plane_s + state_at((p.cols + 15) / 16, r, c & ~15) + 256 * (c / 8 % 2),
+            u);
   }
 }
 
@@ -812,9 +838,9 @@ moe_status_t check_ortho_desc(const moe_orthogonalize_desc_t* d) {
 
 struct Layout {
   int m;                                   // the small side
-  long long ld_x, plane_x, ld_a, plane_a;  // elements
+  long long ld_x, plane_x, ld_a, plane_a, plane_s;  // elements
   int parts;                               // kGram's sums of a matrix
-  size_t x0, x1, lo, a, b, part, norm, shift, done, bytes;
+  size_t x0, x1, state, a, b, part, norm, shift, done, bytes;
 };
 
 Layout layout_of(const moe_orthogonalize_desc_t* d) {
@@ -823,6 +849,7 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   w.m = d->rows < d->cols ? d->rows : d->cols;
   w.ld_x = up(d->cols, 16);
   w.plane_x = w.ld_x * d->rows;
+  w.plane_s = static_cast<long long>((d->rows + 31) / 32) * ((d->cols + 15) / 16) * 512;
   w.ld_a = up(w.m, 16);
   w.plane_a = w.ld_a * w.m;
   const int mt = (w.m + kTile - 1) / kTile;
@@ -835,7 +862,7 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   };
   w.x0 = take(n * w.plane_x * 2);
   w.x1 = take(n * w.plane_x * 2);
-  w.lo = take(n * w.plane_x * 2);
+  w.state = take(n * w.plane_s * 4);
   w.a = take(n * w.plane_a * 2);
   w.b = take(n * w.plane_a * 2);
   w.part = take(n * w.parts * 8);
@@ -980,7 +1007,8 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   p.eps = desc->eps;
   p.x_scale = x_scale;
   p.x_hi = x0;
-  p.x_lo = half_at(w.lo);
+  p.state = reinterpret_cast<float*>(base + w.state);
+  p.plane_s = w.plane_s;
   p.ld_x = w.ld_x;
   p.plane_x = w.plane_x;
   p.done = reinterpret_cast<unsigned int*>(base + w.done);
@@ -1010,7 +1038,8 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
     return MOE_ERR_CUDA;
   g.x[0] = x0;
   g.x[1] = x1;
-  g.x_lo = p.x_lo;
+  g.state = p.state;
+  g.plane_s = w.plane_s;
   g.mat_a = half_at(w.a);
   g.mat_b = half_at(w.b);
   g.ld_x = w.ld_x;

@@ -110,8 +110,8 @@ def orthogonalize(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0):
 
 
 def orthogonalize_rounded(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0):
-    """The same with the roundings that the kernels make: operands as fp16 of
-    values times powers of two, X as an fp16 and the fp16 of the rest."""
+    """The same with the roundings that the kernels make: the products' operands as
+    fp16 of values times powers of two."""
     a, b, c = coefficients
 
     def half(v, by):
@@ -123,7 +123,6 @@ def orthogonalize_rounded(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0)
     x = x.T if tall else x
     for step in range(steps):
         hi = half(x, xs)
-        x = hi + half(x - hi, xs)
         A = half(hi @ hi.T, 4096.0)
         B = b * A + c * (A @ A)
         s = 0.0
