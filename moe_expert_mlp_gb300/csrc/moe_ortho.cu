@@ -10,7 +10,7 @@
 // Numbers.  The operands of the products are fp16: X is bounded (its singular
 // values stay below 2, see the descriptor's checks), so fp16's 11 bits serve,
 // where bf16's 8 would leave an error of one to several percent.  The powers of
-// two kScaleA and 2^x_exp keep A and X clear of fp16's subnormals.  The
+// two kOrthoScaleA and 2^x_exp keep A and X clear of fp16's subnormals.  The
 // state X is held in fp32 beside its operand: a X is exact, and the operand's
 // rounding E enters only through B E,
 // which lies in X's own column space -- a direction that X does not have stays
@@ -35,13 +35,9 @@
 // epilogue's accesses share: the state therefore lies in blocks of 32 rows by 16
 // columns in the order in which a warp's lanes take it, whole lines at a time,
 // where rows 4 KB apart took four times the passes.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <math.h>
 
-#include "moe_f2.cuh"
-#include "moe_internal.h"
-#include "moe_ptx.cuh"
+#include "moe_ortho.cuh"
 
 namespace moe {
 namespace {
@@ -63,7 +59,6 @@ constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
 constexpr int kMaxSide = 16384;
 constexpr int kMaxSteps = 16;
 constexpr int kNormParts = 64;                 // most blocks that share a matrix in the norm
-constexpr float kScaleA = 4096.0f;             // A's entries are at most 4
 
 // kind::f16 with fp16 A and B, fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -221,11 +216,6 @@ __host__ __device__ inline long long state_at(int col_blocks, int r, int c) {
   return (static_cast<long long>(r / 32) * col_blocks + c / 16) * 512 + (r % 32) * 8;
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // 32 bytes, past L1 (other SMs write them in the same launch).
 __device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
   asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -291,10 +281,10 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
   // v = keep * (what was loaded) + accumulator, where not kGram; then * scale
   float s = 0.0f, keep = 0.0f, scale = 1.0f;
   if constexpr (OP == kGram) {
-    scale = kScaleA / (g.x_scale * g.x_scale);
+    scale = kOrthoScaleA / (g.x_scale * g.x_scale);
   } else if constexpr (OP == kPoly) {
-    scale = g.c / (kScaleA * kScaleA);
-    keep = g.b / kScaleA;
+    scale = g.c / (kOrthoScaleA * kOrthoScaleA);
+    keep = g.b / kOrthoScaleA;
     if (shifted && w.mb == w.nb) {
       s = shift_of(g, w.z, p.sym * 2 * kEpiWarps, lane);
       if (w.mb == 0 && rank == 0 && ewarp == 0 && lane == 0) g.shift[w.z] = s;
@@ -362,8 +352,8 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 q = parts(half_pair(h[i]));
-          const float x = live && col + 2 * i < N ? q.x * (1.0f / kScaleA) : 0.0f;
-          const float y = live && col + 2 * i + 1 < N ? q.y * (1.0f / kScaleA) : 0.0f;
+          const float x = live && col + 2 * i < N ? q.x * (1.0f / kOrthoScaleA) : 0.0f;
+          const float y = live && col + 2 * i + 1 < N ? q.y * (1.0f / kOrthoScaleA) : 0.0f;
           sq = fmaf(x, x, fmaf(y, y, sq));
           if (col + 2 * i == row) tr += x;
           if (col + 2 * i + 1 == row) tr += y;
@@ -635,94 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------- preparation
-struct PrepArgs {
-  const void* grad;
-  long long ld_g, plane_g;
-  const float* mom;            // null: no momentum
-  long long ld_m, plane_m;
-  float* mom_out;
-  long long ld_mo, plane_mo;
-  int f32;                     // grad's type
-  int vec;                     // rows may be moved 8 elements at a time
-  int rows, cols, batch;
-  float mu, nu;                // m' = mu m + nu g
-  int nesterov;
-  double* part;                // [batch][parts]
-  int parts;
-  float eps, x_scale;          // X is held times x_scale
-  __half* x_hi;
-  float* state;
-  long long ld_x, plane_x, plane_s;
-  unsigned int* done;          // [batch][3], set to zero
-};
-
-// U's elements c .. c+n-1 of a row (n <= 8), and where asked the new momentum.
-template <bool F32, bool WRITE>
-__device__ __forceinline__ void update_of(const PrepArgs& p, int z, int r, int c, int n,
-                                          float (&u)[8]) {
-  float g[8], m[8];
-  const long long at = z * p.plane_g + r * p.ld_g + c;
-  if (p.vec) {
-    if constexpr (F32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.grad) + at);
-      const float4 x = __ldg(q), y = __ldg(q + 1);
-      g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w;
-      g[4] = y.x, g[5] = y.y, g[6] = y.z, g[7] = y.w;
-    } else {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(p.grad) + at));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        g[2 * i] = bf16_lo(w[i]);
-        g[2 * i + 1] = bf16_hi(w[i]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (F32)
-        g[i] = i < n ? __ldg(static_cast<const float*>(p.grad) + at + i) : 0.0f;
-      else
-        g[i] = i < n ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[at + i]) : 0.0f;
-    }
-  }
-  if (p.mom == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = g[i];
-    return;
-  }
-  // WRITE: m' from m; otherwise m' as it was written
-  const float* src = WRITE ? p.mom : p.mom_out;
-  const long long am = WRITE ? z * p.plane_m + r * p.ld_m + c : z * p.plane_mo + r * p.ld_mo + c;
-  if (p.vec) {
-    const float4* q = reinterpret_cast<const float4*>(src + am);
-    const float4 x = q[0], y = q[1];
-    m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w;
-    m[4] = y.x, m[5] = y.y, m[6] = y.z, m[7] = y.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = i < n ? src[am + i] : 0.0f;
-  }
-  if constexpr (WRITE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fmaf(p.mu, m[i], p.nu * g[i]);
-    float* dst = p.mom_out + z * p.plane_mo + r * p.ld_mo + c;
-    if (p.vec) {
-      reinterpret_cast<float4*>(dst)[0] = make_float4(m[0], m[1], m[2], m[3]);
-      reinterpret_cast<float4*>(dst)[1] = make_float4(m[4], m[5], m[6], m[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) dst[i] = m[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.mu, m[i], p.nu * g[i]) : m[i];
-}
-
-// The new momentum, and the squares of U: eight in fp32, the rest in fp64, and
-// those eight in fp64 too where their sum leaves fp32's middle range.
+// The new momentum, and the squares of U: eight in fp32, the rest in fp64.
 template <bool F32>
 __global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
   __shared__ double s_sum[8];
@@ -737,15 +640,7 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
     const int c = static_cast<int>(i - static_cast<long long>(r) * units) * 8;
     float u[8];
     update_of<F32, true>(p, z, r, c, min(8, p.cols - c), u);
-    float sq = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sq = fmaf(u[k], u[k], sq);
-    if (sq > 1e-30f && sq < 1e30f) {
-      sum += sq;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum += static_cast<double>(u[k]) * u[k];
-    }
+    sum += squares_of(u);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -844,7 +739,7 @@ struct Layout {
 };
 
 Layout layout_of(const moe_orthogonalize_desc_t* d) {
-  Layout w;
+  Layout w = {};
   const size_t n = d->batch;
   w.m = d->rows < d->cols ? d->rows : d->cols;
   w.ld_x = up(d->cols, 16);
@@ -854,6 +749,10 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   w.plane_a = w.ld_a * w.m;
   const int mt = (w.m + kTile - 1) / kTile;
   w.parts = mt * (mt + 1) / 2 * 2 * kEpiWarps;
+  if (small_ortho(d->rows, d->cols)) {     // all in registers and shared memory
+    w.bytes = 256;
+    return w;
+  }
   size_t at = 0;
   auto take = [&at](size_t b) {
     const size_t p = at;
@@ -957,9 +856,6 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
     if ((st = Tensor{mom_out, 4}.check(desc, &vec)) != MOE_OK) return st;
   }
   if ((st = Tensor{out, 2}.check(desc, &out_vec)) != MOE_OK) return st;
-  if (reinterpret_cast<uintptr_t>(out.p) % 32 || (desc->rows > 1 && out.ld % 16) ||
-      (desc->batch > 1 && out.plane % 16))
-    out_vec = false;
   // a written matrix keeps clear of the next one
   const long long span = static_cast<long long>(desc->rows - 1);
   if (desc->batch > 1 &&
@@ -1003,9 +899,14 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   p.mu = desc->momentum;
   p.nu = 1.0f - desc->dampening;
   p.nesterov = desc->nesterov;
-  p.part = reinterpret_cast<double*>(base + w.norm);
   p.eps = desc->eps;
   p.x_scale = x_scale;
+  if (small_ortho(desc->rows, desc->cols)) {
+    SmallOrthoArgs small = {p, static_cast<__nv_bfloat16*>(out.p), out.ld, out.plane, out_vec,
+                            desc->steps, desc->a, desc->b, desc->c, desc->scale};
+    return launch_small_ortho(small, sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  p.part = reinterpret_cast<double*>(base + w.norm);
   p.x_hi = x0;
   p.state = reinterpret_cast<float*>(base + w.state);
   p.plane_s = w.plane_s;
@@ -1063,7 +964,8 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   g.out = static_cast<__nv_bfloat16*>(out.p);
   g.ld_out = out.ld;
   g.plane_out = out.plane;
-  g.out_vec = out_vec;
+  g.out_vec = out_vec && reinterpret_cast<uintptr_t>(out.p) % 32 == 0 &&
+              (desc->rows == 1 || out.ld % 16 == 0) && (desc->batch == 1 || out.plane % 16 == 0);
   g.status = status;
   return launch_steps(g, sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
