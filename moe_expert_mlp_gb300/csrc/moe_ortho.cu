@@ -43,6 +43,7 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 256;                     // both sides of a pair's tile
+constexpr int kNarrow = 64;                     // a tile's least width
 constexpr int kBK = 64;                        // 64 fp16 = one 128-byte swizzle row
 constexpr int kSub = 2;                        // such blocks of the contraction a stage
 constexpr int kStages = 3;
@@ -83,6 +84,7 @@ struct OrthoArgs {
   long long ld_x, plane_x, ld_a, plane_a, plane_s;
   int batch, rows, cols, m, steps;
   int groups;                  // of matrices that go through the steps together
+  int sym_w, full_w;           // tiles' widths: of A and B, of X
   int tall;                    // more rows than columns: A = X^T X, X' = X B
   float* part;                 // [batch][tiles of A][2 CTAs][8 warps]: sums of A_ii, A_ij^2
   float* shift;                // [batch] s
@@ -95,32 +97,43 @@ struct OrthoArgs {
   int* status;
 };
 
-// One tile of the list.
+// One tile of the list: rows mb*256 and on, columns nb*width and on; nr: its number
+// among its product's of the matrix.
 struct Work {
-  int op, step, z, mb, nb;
+  int op, step, z, mb, nb, nr;
 };
 
 // The list's shape.
 struct Plan {
-  int m_tiles, r_tiles, c_tiles;   // of the small side, X's rows and columns
+  int r_tiles, c_tiles;            // of X's rows and columns
+  int s_tiles, ratio;              // of A's columns, and how many of them are 256 wide
   int sym, full;                   // tiles of A (and B) and of X
   int per_matrix, total;           // of one matrix in a step, of all
 };
 
+__host__ __device__ inline int tiles_of(int n, int width) { return (n + width - 1) / width; }
+
+// Tiles on or right of the diagonal's 256 x 256 blocks.
+__host__ __device__ inline int sym_tiles(int m, int width) {
+  const int rows = tiles_of(m, kTile), ratio = kTile / width;
+  return rows * tiles_of(m, width) - ratio * (rows * (rows - 1) / 2);
+}
+
 __device__ __forceinline__ Plan plan_of(const OrthoArgs& g) {
   Plan p;
-  p.m_tiles = (g.m + kTile - 1) / kTile;
-  p.r_tiles = (g.rows + kTile - 1) / kTile;
-  p.c_tiles = (g.cols + kTile - 1) / kTile;
-  p.sym = p.m_tiles * (p.m_tiles + 1) / 2;
+  p.r_tiles = tiles_of(g.rows, kTile);
+  p.c_tiles = tiles_of(g.cols, g.full_w);
+  p.s_tiles = tiles_of(g.m, g.sym_w);
+  p.ratio = kTile / g.sym_w;
+  p.sym = sym_tiles(g.m, g.sym_w);
   p.full = p.r_tiles * p.c_tiles;
   p.per_matrix = 2 * p.sym + p.full;
   p.total = g.steps * g.batch * p.per_matrix;
   return p;
 }
 
-// Symmetric products go by columns nb of 1, 2, ... tiles mb <= nb; X with the
-// small side inside, so that the long side's panel is shared by its neighbours.
+// Symmetric products go row by row of 256; X with the small side inside, so that
+// the long side's panel is shared by its neighbours.
 __device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t) {
   Work w;
   // group i holds the matrices floor(i batch / groups) and on
@@ -140,17 +153,20 @@ __device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t
     const int z = r / p.sym;
     w.z = z0 + z;
     r -= z * p.sym;
-    int nb = static_cast<int>((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
-    while (nb * (nb + 1) / 2 > r) --nb;
-    while ((nb + 1) * (nb + 2) / 2 <= r) ++nb;
-    w.nb = nb;
-    w.mb = r - nb * (nb + 1) / 2;
+    w.nr = r;
+    w.mb = 0;
+    for (int n = p.s_tiles; r >= n; n -= p.ratio) {
+      r -= n;
+      ++w.mb;
+    }
+    w.nb = w.mb * p.ratio + r;
   } else {
     w.op = w.step + 1 == g.steps ? kLast : kUpdate;
     r -= 2 * sym;
     const int z = r / p.full;
     w.z = z0 + z;
     r -= z * p.full;
+    w.nr = r;
     const int inside = g.tall ? p.c_tiles : p.r_tiles;
     const int outside = r / inside;
     r -= outside * inside;
@@ -160,11 +176,11 @@ __device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t
   return w;
 }
 
-// Stages of the contraction, columns that the tile's MMAs compute (a multiple of 32, or
-// of 128 where the second operand lies along its rows), and the operands' ways to
-// lie.
+// Stages of the contraction, the tile's first column, the columns that its MMAs
+// compute (a multiple of 32, or of 128 where the second operand lies along its
+// rows), and the operands' ways to lie.
 struct Shape {
-  int num_st, n_eff;
+  int num_st, col0, n_eff;
   bool a_mn, b_mn;
 };
 
@@ -175,9 +191,11 @@ __device__ __forceinline__ Shape shape_of(const OrthoArgs& g, const Work& w) {
   s.b_mn = (gram && g.tall) || (update && !g.tall);
   const int K = gram ? (g.tall ? g.rows : g.cols) : g.m;
   s.num_st = (K + kSub * kBK - 1) / (kSub * kBK);
-  const int left = (update ? g.cols : g.m) - w.nb * kTile;
+  const int width = update ? g.full_w : g.sym_w;
+  s.col0 = w.nb * width;
+  const int left = (update ? g.cols : g.m) - s.col0;
   const int unit = s.b_mn ? 128 : 32;
-  s.n_eff = min(kTile, (left + unit - 1) / unit * unit);
+  s.n_eff = min(width, (left + unit - 1) / unit * unit);
   return s;
 }
 
@@ -192,22 +210,18 @@ __device__ __forceinline__ bool wait_inputs(const OrthoArgs& g, const Plan& p, c
       share * (w.op == kGram ? w.step * p.full : (w.step + 1) * p.sym);
   unsigned int v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
-  if (v < target) {
-    const unsigned long long t0 = global_ns();
-    while (true) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
-      if (v >= target) break;
-      if (*abort_flag) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        set_status(g.status, MOE_DEV_TIMEOUT);
-        return false;
-      }
+  if (v >= target) return true;
+  const unsigned long long t0 = global_ns();
+  while (true) {
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+    if (v >= target) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      set_status(g.status, MOE_DEV_TIMEOUT);
+      return false;
     }
   }
-  // what other SMs stored is now read by TMA
-  asm volatile("fence.proxy.async;" ::: "memory");
-  return true;
 }
 
 // Where the state has the first 8 of row r's 16 elements from column c (a
@@ -259,22 +273,24 @@ __device__ __forceinline__ uint32_t pack_half(F2 v) {
 }
 
 // One warp's share of a tile: 32 rows, 16 of every 32 columns.  The loads of the
-// state (or of A) run kAhead chunks ahead; `read` is called once the accumulator
-// has been read.
+// state (or of A) run kAhead chunks ahead, the first ones before `ready` waits for
+// the accumulator; `read` is called once the accumulator has been read.
 constexpr int kAhead = 4;
 
-template <int OP, typename READ>
-__device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, const Work& w,
-                                         uint32_t tbase, int row0, int col0, int lane, int ewarp,
-                                         uint32_t rank, __half* mirror_buf, READ read) {
+template <int OP, typename READY, typename READ>
+__device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, const Work& w,
+                                         int width, uint32_t tbase, int row0, int col0, int lane,
+                                         int ewarp, uint32_t rank, __half* mirror_buf, READY ready,
+                                         READ read) {
   constexpr bool kSym = OP == kGram || OP == kPoly;
   constexpr bool kState = OP == kUpdate || OP == kLast;
   const int M = kSym ? g.m : g.rows, N = kSym ? g.m : g.cols;
   const int row = row0 + lane;
   const bool live = row < M;
-  const bool mirror = kSym && w.mb != w.nb;
+  const bool diagonal = kSym && w.nb / p.ratio == w.mb;
+  const bool mirror = kSym && !diagonal;
   const bool shifted = w.step + 2 >= g.steps;
-  const int nch = min(kTile / 32, (N - col0 + 31) / 32);   // may be <= 0
+  const int nch = min(width / 32, (N - col0 + 31) / 32);   // may be <= 0
   const long long ld = kSym ? g.ld_a : g.ld_x;
   const long long at0 = static_cast<long long>(w.z) * (kSym ? g.plane_a : g.plane_x) + row * ld +
                         col0;
@@ -285,9 +301,9 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
   } else if constexpr (OP == kPoly) {
     scale = g.c / (kOrthoScaleA * kOrthoScaleA);
     keep = g.b / kOrthoScaleA;
-    if (shifted && w.mb == w.nb) {
+    if (shifted && diagonal) {
       s = shift_of(g, w.z, p.sym * 2 * kEpiWarps, lane);
-      if (w.mb == 0 && rank == 0 && ewarp == 0 && lane == 0) g.shift[w.z] = s;
+      if (w.nr == 0 && rank == 0 && ewarp == 0 && lane == 0) g.shift[w.z] = s;
     }
   } else {
     keep = g.a + (shifted ? __ldcg(g.shift + w.z) : 0.0f);
@@ -332,7 +348,7 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
       if constexpr (OP == kGram || OP == kLast) v[i] = v[i] * scale2;
     }
     if constexpr (OP == kPoly) {
-      if (s != 0.0f && w.mb == w.nb) {
+      if (s != 0.0f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 f = parts(v[i]);
@@ -413,6 +429,7 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
 
 #pragma unroll
   for (int b = 0; b < kAhead; ++b) fetch(b, kBuf > 1 ? b : 0);
+  if (!ready()) return false;
   if (nch <= 0) read();
 #pragma unroll 1
   for (int j = 0; j < nch; j += kAhead) {
@@ -427,13 +444,13 @@ __device__ __forceinline__ void epilogue(const OrthoArgs& g, const Plan& p, cons
         tr += __shfl_xor_sync(0xFFFFFFFFu, tr, o);
         sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
       }
-      const int tile = w.nb * (w.nb + 1) / 2 + w.mb;
       if (lane == 0)
-        reinterpret_cast<float2*>(g.part)[((static_cast<long long>(w.z) * p.sym + tile) * 2 + rank) *
+        reinterpret_cast<float2*>(g.part)[((static_cast<long long>(w.z) * p.sym + w.nr) * 2 + rank) *
                                               kEpiWarps + ewarp] =
             make_float2(tr, mirror ? 2.0f * sq : sq);
     }
   }
+  return true;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -493,8 +510,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tb = g.tall ? &g.map_b : &g.x_mn[now];
         }
         const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
-        const int n0 = w.nb * kTile + (sh.n_eff / 2) * static_cast<int>(rank);
+        const int n0 = sh.col0 + (sh.n_eff / 2) * static_cast<int>(rank);
+        // a second box of the second operand's half, where it lies along its rows
+        const bool two = sh.n_eff > 128;
+        const uint32_t tx = 2 * kSub * (kHalfBytes + (sh.b_mn && !two ? kBoxBytes : kHalfBytes));
         ok = wait_inputs(g, p, w, abort_flag);
+        // what other SMs stored is now read by TMA
+        asm volatile("fence.proxy.async;" ::: "memory");
         for (int st = 0; st < sh.num_st && ok; ++st) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, g.status, abort_flag)) {
             ok = false;
@@ -504,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint8_t* sb = sa + kSub * kHalfBytes;
           const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
           // boxes past a tensor's end are filled with zeros and count whole
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
             const int k0 = (st * kSub + u) * kBK;
@@ -516,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (sh.b_mn) {
               tma_load_3d_pair(sb + u * kHalfBytes, tb, fb, n0, k0, w.z);
-              tma_load_3d_pair(sb + u * kHalfBytes + kBoxBytes, tb, fb, n0 + 64, k0, w.z);
+              if (two) tma_load_3d_pair(sb + u * kHalfBytes + kBoxBytes, tb, fb, n0 + 64, k0, w.z);
             } else {
               tma_load_3d_pair(sb + u * kHalfBytes, tb, fb, k0, n0, w.z);
             }
@@ -580,30 +602,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0;
     for (int t = pair; t < p.total; t += npairs, ++it) {
       const Work w = work_at(g, p, t);
+      const int width = w.op >= kUpdate ? g.full_w : g.sym_w;
       const int row0 = w.mb * kTile + 128 * static_cast<int>(rank) + quarter * 32;
-      const int col0 = w.nb * kTile + hc;
+      const int col0 = w.nb * width + hc;
       const int acc = it & 1;
       const uint32_t acc_par = (it >> 1) & 1;
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait(&tfull_bar[acc], acc_par, g.status, abort_flag);
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTile + hc;
+      // what the epilogue reads beside the accumulator is there
+      int ok = 1;
+      if (lane == 0 && w.op != kGram) ok = wait_inputs(g, p, w, abort_flag);
+      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      auto ready = [&]() {
+        int full = 1;
+        if (lane == 0) full = mbar_wait(&tfull_bar[acc], acc_par, g.status, abort_flag);
+        full = __shfl_sync(0xFFFFFFFFu, full, 0);
+        tc_fence_after();
+        return full != 0;
+      };
       auto read = [&]() {                    // the accumulator is free again
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
       };
+      bool done;
       if (w.op == kGram)
-        epilogue<kGram>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+        done = epilogue<kGram>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
+                               read);
       else if (w.op == kPoly)
-        epilogue<kPoly>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+        done = epilogue<kPoly>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
+                               read);
       else if (w.op == kUpdate)
-        epilogue<kUpdate>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+        done = epilogue<kUpdate>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
+                               read);
       else
-        epilogue<kLast>(g, p, w, tbase, row0, col0, lane, ewarp, rank, mirror_buf, read);
+        done = epilogue<kLast>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
+                               read);
+      if (!done) break;
       if (w.op != kLast) {
         // the tile's stores, before the count that tells of them (TMA reads them)
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -747,8 +782,7 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   w.plane_s = static_cast<long long>((d->rows + 31) / 32) * ((d->cols + 15) / 16) * 512;
   w.ld_a = up(w.m, 16);
   w.plane_a = w.ld_a * w.m;
-  const int mt = (w.m + kTile - 1) / kTile;
-  w.parts = mt * (mt + 1) / 2 * 2 * kEpiWarps;
+  w.parts = sym_tiles(w.m, kNarrow) * 2 * kEpiWarps;   // for the narrowest tiles
   if (small_ortho(d->rows, d->cols)) {     // all in registers and shared memory
     w.bytes = 256;
     return w;
@@ -784,16 +818,23 @@ cudaError_t launch_steps(OrthoArgs& g, int sms, cudaStream_t s) {
   cudaError_t err = cudaFuncSetAttribute(k_ortho_steps, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
-  const long long mt = (g.m + kTile - 1) / kTile;
-  const long long full = static_cast<long long>((g.rows + kTile - 1) / kTile) *
-                         ((g.cols + kTile - 1) / kTile);
-  const long long most = g.batch * (full > mt * (mt + 1) / 2 ? full : mt * (mt + 1) / 2);
-  const long long pairs = most < sms / 2 ? most : sms / 2;
+  // narrower tiles as long as they are one for each pair: a product of few tiles
+  // takes as long as one of them (8 matrices of 256 x 512: 150 -> WWW us)
+  const int most = sms / 2;
+  auto sym = [&](int width) { return static_cast<long long>(g.batch) * sym_tiles(g.m, width); };
+  auto full = [&](int width) {
+    return static_cast<long long>(g.batch) * tiles_of(g.rows, kTile) * tiles_of(g.cols, width);
+  };
+  g.sym_w = g.full_w = kTile;
+  while (g.sym_w > (g.tall ? 128 : kNarrow) && sym(g.sym_w / 2) <= most) g.sym_w /= 2;
+  while (g.full_w > (g.tall ? kNarrow : 128) && full(g.full_w / 2) <= most) g.full_w /= 2;
+  const long long tiles = sym(g.sym_w) > full(g.full_w) ? sym(g.sym_w) : full(g.full_w);
+  const long long pairs = tiles < most ? tiles : most;
   // together as many matrices as give A's product two tiles a pair: then a
   // product's inputs are done by the time the list comes to it, and no more
   // matrices than that take turns in L2
-  const long long sym = mt * (mt + 1) / 2;
-  const long long together = (2 * pairs + sym - 1) / sym;
+  const int each = sym_tiles(g.m, g.sym_w);
+  const long long together = (2 * pairs + each - 1) / each;
   g.groups = static_cast<int>(g.batch > together ? g.batch / together : 1);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeCooperative;
