@@ -59,7 +59,7 @@ constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
                          kEpiWarps * kMirrorBytes;
 constexpr int kMaxSide = 16384;
 constexpr int kMaxSteps = 16;
-constexpr int kNormParts = 64;                 // most blocks that share a matrix in the norm
+constexpr int kNormParts = 608;                // most blocks that share a matrix in the norm
 
 // kind::f16 with fp16 A and B, fp32 accumulation.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
@@ -660,22 +660,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------- preparation
-// The new momentum, and the squares of U: eight in fp32, the rest in fp64.
+// Bound by memory (4 matrices of 7168 x 2048 with a momentum: 96 us for the 587 MB
+// of the first, 138 us for the 587 MB of the second).
+constexpr int kPrepUnits = 2;
+
+// The new momentum, and the squares of U.
 template <bool F32>
-__global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
+__global__ void __launch_bounds__(256, 3) k_ortho_norm(const PrepArgs p) {
   __shared__ double s_sum[8];
   const int z = blockIdx.y;
   if (blockIdx.x == 0 && threadIdx.x < 3) p.done[3 * z + threadIdx.x] = 0;
-  const int units = (p.cols + 7) / 8;
-  const long long count = static_cast<long long>(p.rows) * units;
+  const unsigned units = (p.cols + 7) / 8;
+  const unsigned count = p.rows * units;
+  const unsigned stride = gridDim.x * 256;
   double sum = 0.0;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < count;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const int r = static_cast<int>(i / units);
-    const int c = static_cast<int>(i - static_cast<long long>(r) * units) * 8;
-    float u[8];
-    update_of<F32, true>(p, z, r, c, min(8, p.cols - c), u);
-    sum += squares_of(u);
+  for (unsigned i0 = blockIdx.x * 256 + threadIdx.x; i0 < count; i0 += kPrepUnits * stride) {
+    float g[kPrepUnits][8], m[kPrepUnits][8];
+    int r[kPrepUnits], c[kPrepUnits];
+#pragma unroll
+    for (int q = 0; q < kPrepUnits; ++q) {
+      const unsigned i = i0 + q * stride;
+      r[q] = i / units;
+      c[q] = (i - r[q] * units) * 8;
+      if (i >= count) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[q][k] = 0.0f;
+        continue;
+      }
+      load_grad<F32>(p, z, r[q], c[q], min(8, p.cols - c[q]), g[q]);
+      if (p.mom != nullptr)
+        load_floats(p.mom + z * p.plane_m + r[q] * p.ld_m + c[q], min(8, p.cols - c[q]), p.vec,
+                    m[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kPrepUnits; ++q) {
+      if (i0 + q * stride >= count) continue;
+      if (p.mom != nullptr) {
+        step_momentum(p, z, r[q], c[q], min(8, p.cols - c[q]), g[q], m[q]);
+        direction(p, g[q], m[q]);
+      }
+    }
+    sum += squares_of(g);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -683,37 +708,61 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const PrepArgs p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) sum += s_sum[w];
-    p.part[static_cast<long long>(z) * p.parts + blockIdx.x] = sum;
+    p.part[static_cast<long long>(z) * kNormParts + blockIdx.x] = sum;
   }
 }
 
-// X = U / (|U| + eps), as fp32 and fp16.
+// X = U / (|U| + eps), as fp32 and fp16.  A warp takes a block of the state, 32 rows
+// by 16 columns, a row a lane: whole sectors of the rows, whole lines of the state.
 template <bool F32>
-__global__ void __launch_bounds__(256) k_ortho_start(const PrepArgs p) {
+__global__ void __launch_bounds__(256, 4) k_ortho_start(const PrepArgs p) {
+  __shared__ float s_mul;
   const int z = blockIdx.y;
-  double sum = 0.0;
-  for (int i = threadIdx.x & 31; i < p.parts; i += 32)
-    sum += p.part[static_cast<long long>(z) * p.parts + i];
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {          // fp64 for one warp only
+    double sum = 0.0;
+    for (int i = lane; i < p.parts; i += 32)
+      sum += p.part[static_cast<long long>(z) * kNormParts + i];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  const float mul = static_cast<float>(p.x_scale / (sqrt(sum) + p.eps));
-  const int units = (p.cols + 7) / 8;
-  const long long count = static_cast<long long>(p.rows) * units;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < count;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const int r = static_cast<int>(i / units);
-    const int c = static_cast<int>(i - static_cast<long long>(r) * units) * 8;
-    float u[8];
-    update_of<F32, false>(p, z, r, c, min(8, p.cols - c), u);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) s_mul = static_cast<float>(p.x_scale / (sqrt(sum) + p.eps));
+  }
+  __syncthreads();
+  const float mul = s_mul;
+  const int col_blocks = (p.cols + 15) / 16;
+  const int blocks = (p.rows + 31) / 32 * col_blocks;
+  const bool reads_grad = p.mom == nullptr || p.nesterov;
+  for (int i = blockIdx.x * 8 + threadIdx.x / 32; i < blocks; i += gridDim.x * 8) {
+    const int rb = i / col_blocks;
+    const int r = rb * 32 + lane, c0 = (i - rb * col_blocks) * 16;
+    if (r >= p.rows) continue;
+    float g[2][8], m[2][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) u[k] *= mul;
-    *reinterpret_cast<uint4*>(p.x_hi + z * p.plane_x + r * p.ld_x + c) =
-        make_uint4(pack_half2(u[0], u[1]), pack_half2(u[2], u[3]), pack_half2(u[4], u[5]),
-                   pack_half2(u[6], u[7]));
-    // (with an odd number of units the last block's second half stays as it is:
-    // what comes of it is not stored)
-    store32(p.state + z * p.plane_s + state_at((p.cols + 15) / 16, r, c & ~15) + 256 * (c / 8 % 2),
-            u);
+    for (int q = 0; q < 2; ++q) {
+      const int c = c0 + 8 * q, n = min(8, p.cols - c);
+      if (n <= 0) continue;
+      if (reads_grad) load_grad<F32>(p, z, r, c, n, g[q]);
+      if (p.mom != nullptr)
+        load_floats(p.mom_out + z * p.plane_mo + r * p.ld_mo + c, n, p.vec, m[q]);
+    }
+    float* state = p.state + z * p.plane_s + state_at(col_blocks, r, c0);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int c = c0 + 8 * q;
+      // (with an odd number of units the last block's second half stays as it is:
+      // what comes of it is not stored)
+      if (c >= p.cols) continue;
+      float u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = reads_grad ? g[q][k] : 0.0f;
+      if (p.mom != nullptr) direction(p, u, m[q]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] *= mul;
+      *reinterpret_cast<uint4*>(p.x_hi + z * p.plane_x + r * p.ld_x + c) =
+          make_uint4(pack_half2(u[0], u[1]), pack_half2(u[2], u[3]), pack_half2(u[4], u[5]),
+                     pack_half2(u[6], u[7]));
+      store32(state + 256 * q, u);
+    }
   }
 }
 
@@ -955,11 +1004,15 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   p.plane_x = w.plane_x;
   p.done = reinterpret_cast<unsigned int*>(base + w.done);
   const long long units = static_cast<long long>(desc->rows) * ((desc->cols + 7) / 8);
-  const long long most = (units + 255) / 256;
-  p.parts = static_cast<int>(most < kNormParts ? most : kNormParts);
-  const dim3 norm_grid(p.parts, desc->batch);
-  const long long start_blocks = (units + 1023) / 1024;
-  const dim3 start_grid(static_cast<unsigned>(start_blocks), desc->batch);
+  const long long blocks = (units + 256 * kPrepUnits - 1) / (256 * kPrepUnits);
+  p.parts = static_cast<int>(blocks < kNormParts ? blocks : kNormParts);
+  // blocks a matrix in the second: enough to fill the GPU, few enough that taking
+  // the norm's root does not count
+  const long long state_blocks = w.plane_s / 512;
+  const long long fill = (8ll * sms + desc->batch - 1) / desc->batch;
+  const unsigned start_blocks = static_cast<unsigned>(
+      (state_blocks + 7) / 8 < fill ? (state_blocks + 7) / 8 : fill);
+  const dim3 norm_grid(p.parts, desc->batch), start_grid(start_blocks, desc->batch);
   if (f32) {
     k_ortho_norm<true><<<norm_grid, 256, 0, stream>>>(p);
     k_ortho_start<true><<<start_grid, 256, 0, stream>>>(p);

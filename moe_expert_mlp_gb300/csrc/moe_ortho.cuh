@@ -35,81 +35,89 @@ struct PrepArgs {
   unsigned int* done;          // [batch][3], set to zero
 };
 
-// U's elements c .. c+n-1 of a row (n <= 8), and where asked the new momentum.
-template <bool F32, bool WRITE>
-__device__ __forceinline__ void update_of(const PrepArgs& p, int z, int r, int c, int n,
-                                          float (&u)[8]) {
-  float g[8], m[8];
+// 8 floats of a row from c on, n of them where they are not aligned.
+__device__ __forceinline__ void load_floats(const float* src, int n, bool vec, float (&v)[8]) {
+  if (vec) {
+    const float4* q = reinterpret_cast<const float4*>(src);
+    const float4 x = q[0], y = q[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? src[i] : 0.0f;
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_grad(const PrepArgs& p, int z, int r, int c, int n,
+                                          float (&g)[8]) {
   const long long at = z * p.plane_g + r * p.ld_g + c;
-  if (p.vec) {
-    if constexpr (F32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.grad) + at);
-      const float4 x = __ldg(q), y = __ldg(q + 1);
-      g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w;
-      g[4] = y.x, g[5] = y.y, g[6] = y.z, g[7] = y.w;
-    } else {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(p.grad) + at));
+  if constexpr (F32) {
+    load_floats(static_cast<const float*>(p.grad) + at, n, p.vec, g);
+  } else {
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.grad) + at;
+    if (p.vec) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         g[2 * i] = bf16_lo(w[i]);
         g[2 * i + 1] = bf16_hi(w[i]);
       }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (F32)
-        g[i] = i < n ? __ldg(static_cast<const float*>(p.grad) + at + i) : 0.0f;
-      else
-        g[i] = i < n ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.grad)[at + i]) : 0.0f;
-    }
-  }
-  if (p.mom == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = g[i];
-    return;
-  }
-  // WRITE: m' from m; otherwise m' as it was written
-  const float* src = WRITE ? p.mom : p.mom_out;
-  const long long am = WRITE ? z * p.plane_m + r * p.ld_m + c : z * p.plane_mo + r * p.ld_mo + c;
-  if (p.vec) {
-    const float4* q = reinterpret_cast<const float4*>(src + am);
-    const float4 x = q[0], y = q[1];
-    m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w;
-    m[4] = y.x, m[5] = y.y, m[6] = y.z, m[7] = y.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = i < n ? src[am + i] : 0.0f;
-  }
-  if constexpr (WRITE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fmaf(p.mu, m[i], p.nu * g[i]);
-    float* dst = p.mom_out + z * p.plane_mo + r * p.ld_mo + c;
-    if (p.vec) {
-      reinterpret_cast<float4*>(dst)[0] = make_float4(m[0], m[1], m[2], m[3]);
-      reinterpret_cast<float4*>(dst)[1] = make_float4(m[4], m[5], m[6], m[7]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) dst[i] = m[i];
+      for (int i = 0; i < 8; ++i) g[i] = i < n ? __bfloat162float(src[i]) : 0.0f;
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? fmaf(p.mu, m[i], p.nu * g[i]) : m[i];
 }
 
-// Squares of 8 values: in fp32, and in fp64 where their sum leaves fp32's middle
-// range.
-__device__ __forceinline__ double squares_of(const float (&u)[8]) {
-  float sq = 0.0f;
+// The new momentum of 8 elements from the old one, in place and stored.
+__device__ __forceinline__ void step_momentum(const PrepArgs& p, int z, int r, int c, int n,
+                                              const float (&g)[8], float (&m)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sq = fmaf(u[k], u[k], sq);
-  if (sq > 1e-30f && sq < 1e30f) return sq;
+  for (int i = 0; i < 8; ++i) m[i] = fmaf(p.mu, m[i], p.nu * g[i]);
+  float* dst = p.mom_out + z * p.plane_mo + r * p.ld_mo + c;
+  if (p.vec) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(m[0], m[1], m[2], m[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(m[4], m[5], m[6], m[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) dst[i] = m[i];
+  }
+}
+
+// U of the gradient g and the new momentum, into g.
+__device__ __forceinline__ void direction(const PrepArgs& p, float (&g)[8], const float (&m)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = p.nesterov ? fmaf(p.mu, m[i], p.nu * g[i]) : m[i];
+}
+
+// Squares of 8 N values: in fp32, and in fp64 where their sum leaves fp32's middle
+// range.  (One fp64 addition for them all: this GPU's rate of those is 1/64.)
+template <int N>
+__device__ __forceinline__ double squares_of(const float (&u)[N][8]) {
+  float sq[N], all = 0.0f;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    sq[q] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sq[q] = fmaf(u[q][k], u[q][k], sq[q]);
+    all += sq[q];
+  }
+  if ((all > 1e-30f && all < 1e30f) || all == 0.0f) {
+    bool zeros = true;             // a sum of 0 is one of zeros, or of squares below fp32's range
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) zeros = zeros && u[q][k] == 0.0f;
+    if (all != 0.0f || zeros) return all;
+  }
   double sum = 0.0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sum += static_cast<double>(u[k]) * u[k];
+  for (int q = 0; q < N; ++q)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += static_cast<double>(u[q][k]) * u[q][k];
   return sum;
 }
 

@@ -160,12 +160,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
     const int count = max(0, row1 - row0) * units;
     for (int i = threadIdx.x; i < count; i += kSmallThreads) {
       const int r = row0 + i / units, c = col0 + i % units * 8;
-      float u[8];
+      const int k8 = min(8, col1 - c);
+      float u1[1][8];
+      float (&u)[8] = u1[0];
       if (p.f32)
-        update_of<true, true>(p, z, r, c, min(8, col1 - c), u);
+        load_grad<true>(p, z, r, c, k8, u);
       else
-        update_of<false, true>(p, z, r, c, min(8, col1 - c), u);
-      sum += squares_of(u);
+        load_grad<false>(p, z, r, c, k8, u);
+      if (p.mom != nullptr) {
+        float mom[8];
+        load_floats(p.mom + z * p.plane_m + r * p.ld_m + c, k8, p.vec, mom);
+        step_momentum(p, z, r, c, k8, u, mom);
+        direction(p, u, mom);
+      }
+      sum += squares_of(u1);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (c + k < col1) {
