@@ -483,18 +483,32 @@ __global__ void __launch_bounds__(1024) k_loss_join(const LossArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0 && !ascends(a, s))
     set_status(a.status, MOE_DEV_BAD_OFFSETS);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // eight segments a warp on their way at once; tokens and squares: a segment a lane
+  constexpr int kAhead = 8;
   float p = 0.0f, z = 0.0f;
   int count = 0, n = 0;
-#pragma unroll 4
-  for (int c = c0 + warp; c < c1; c += 32) {
-    const long long seg = static_cast<long long>(c) + s;
-    if (e < a.E) {
-      p += __ldcg(a.seg_p + seg * a.E + e);
-      count += __ldcg(a.seg_count + seg * a.E + e);
+  for (int c = c0 + warp; c < c1; c += 32 * kAhead) {
+    float ps[kAhead];
+    int cs[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const long long at = (static_cast<long long>(c) + 32 * i + s) * a.E + e;
+      const bool in = c + 32 * i < c1 && e < a.E;
+      ps[i] = in ? __ldcg(a.seg_p + at) : 0.0f;
+      cs[i] = in ? __ldcg(a.seg_count + at) : 0;
     }
-    n += __ldcg(a.seg_tokens + seg);
-    z += __ldcg(a.seg_z + seg);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      p += ps[i];
+      count += cs[i];
+    }
   }
+  for (int c = c0 + threadIdx.x; c < c1; c += 1024) {
+    n += __ldcg(a.seg_tokens + static_cast<long long>(c) + s);
+    z += __ldcg(a.seg_z + static_cast<long long>(c) + s);
+  }
+  n = warp_sum(n);
+  z = warp_sum(z);
   s_p[warp][lane] = p;
   s_c[warp][lane] = count;
   if (lane == 0) {
