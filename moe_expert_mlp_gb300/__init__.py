@@ -40,3 +40,4 @@ from ._lib import (  # noqa: F401
 )
 from .block import MoEResidualBlock  # noqa: F401
 from .layer import MoEExpertMLP  # noqa: F401
+from .updates import OrthogonalUpdates  # noqa: F401

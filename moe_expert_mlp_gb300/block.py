@@ -1,6 +1,6 @@
 """One residual block around a routed-expert MLP layer on one GPU: pre norm,
-the layer, post norm with gate and scaled residual, their backward, and the
-clipping of the block's gradients.
+the layer, post norm with gate and scaled residual, their backward, the clipping
+of the block's gradients and the updates they give the experts.
 
     x     = N1(res)
     out   = MoE(x)                         (MoEExpertMLP, combined tokens)
@@ -15,6 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .updates import OrthogonalUpdates
 
 
 class MoEResidualBlock:
@@ -73,6 +74,15 @@ class MoEResidualBlock:
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.norms = torch.zeros(n, dtype=torch.float32, device=dev)
         self.norm_ws = torch.empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=dev)
+        self.updates = None            # the experts', see orthogonal_updates
+
+    def orthogonal_updates(self, **kw):
+        """From now on step() ends with the orthogonalised updates of the experts'
+        weights, self.updates.outs for layer.w1p and layer.w2 (their clipped
+        gradients' matrices, one an expert; the packed FC1's padding rows stay
+        zero); kw: as OrthogonalUpdates."""
+        self.updates = OrthogonalUpdates([self.layer.dw1p, self.layer.dw2], **kw)
+        return self.updates
 
     def forward_norm(self, res, stream=None):
         """x = N1(res), the layer's input (and the router's)."""
@@ -81,9 +91,10 @@ class MoEResidualBlock:
                                  self.x, stream)
         return self.x
 
-    def forward(self, res, logits, bias=None, gate=None, stream=None, timer=None):
-        """res [T,d] (kept for the backward) -> res_out; logits, bias: the
-        router's, as MoEExpertMLP.forward; gate fp32 [T] with a token gate.  A
+    def forward(self, res, logits, bias=None, gate=None, stream=None, timer=None, mask=None,
+                seq_offsets=None):
+        """res [T,d] (kept for the backward) -> res_out; logits, bias, mask and
+        seq_offsets: the router's, as MoEExpertMLP.forward; gate fp32 [T] with a token gate.  A
         router that reads x calls forward_norm first; the norm runs again here,
         with the same result."""
         if self.token_gate and gate is None:
@@ -92,7 +103,7 @@ class MoEResidualBlock:
         self.gate = gate if self.token_gate else self.params.get("gate")
         with t(timer, "pre_norm"):
             self.forward_norm(res, stream)
-        layer.route(self.x, logits, bias, stream, timer)
+        layer.route(self.x, logits, bias, stream, timer, mask, seq_offsets)
         layer.mlp_forward(stream, timer)
         with t(timer, "combine_post_norm"):
             L.moe_block_post_norm_fwd(
@@ -100,24 +111,25 @@ class MoEResidualBlock:
                 dict(row_of=layer.row_of, topk_w=layer.topk_w, y_out=layer.out), stream)
         return self.res_out
 
-    def backward_branch(self, dres_out, stream=None, timer=None):
+    def backward_branch(self, dres_out, stream=None, timer=None, dloss=None):
         """Gradient of res_out back to the layer's input: layer.dx, layer.dlogits
-        and the gradients of the post norm, gate and experts."""
+        and the gradients of the post norm, gate and experts; dloss: as
+        MoEExpertMLP.backward."""
         layer = self.layer
         with layer._t(timer, "post_norm_bwd"):
             L.moe_block_post_norm_bwd(self.desc, dres_out, None, None, layer.out,
                                       dict(self.params, gate=self.gate), None, self.dout,
                                       self.grads, self.ws, 1.0, stream)
-        layer.backward(self.dout, stream, timer)
+        layer.backward(self.dout, stream, timer, dloss)
         return layer.dx
 
-    def backward(self, dres_out, stream=None, timer=None):
+    def backward(self, dres_out, stream=None, timer=None, dloss=None):
         """dres_out [T,d] -> dres, the gradient of res through the residual, the
         norms and the experts.  The router's logits are an input, so their
         gradient (layer.dlogits) is not carried into x: a caller that made them
         from x calls backward_branch, adds its part to layer.dx and calls
         backward_norm."""
-        self.backward_branch(dres_out, stream, timer)
+        self.backward_branch(dres_out, stream, timer, dloss)
         return self.backward_norm(dres_out, stream, timer)
 
     def backward_norm(self, dres_out, stream=None, timer=None):
@@ -135,10 +147,15 @@ class MoEResidualBlock:
         L.moe_clip_grads(self.gradients, self.norm, max_norm, eps, stream)
         return self.norm
 
-    def step(self, res, logits, bias, dres_out, max_norm=None, gate=None, stream=None, timer=None):
-        """One forward and backward of the block, gradients clipped."""
-        self.forward(res, logits, bias, gate, stream, timer)
-        self.backward(dres_out, stream, timer)
+    def step(self, res, logits, bias, dres_out, max_norm=None, gate=None, stream=None, timer=None,
+             mask=None, seq_offsets=None, dloss=None):
+        """One forward and backward of the block, gradients clipped, and where
+        orthogonal_updates() asked for them the experts' updates."""
+        self.forward(res, logits, bias, gate, stream, timer, mask, seq_offsets)
+        self.backward(dres_out, stream, timer, dloss)
         if max_norm is not None:
             self.clip_gradients(max_norm, stream=stream)
+        if self.updates is not None:
+            with self.layer._t(timer, "updates"):
+                self.updates.step(stream)
         return self.dres

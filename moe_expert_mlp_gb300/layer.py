@@ -20,7 +20,7 @@ class MoEExpertMLP:
     def __init__(self, E, d, F, T=0, k=1, act="swiglu", alpha=1.0, limit=math.inf,
                  linear_offset=0.0, out_scale=1.0, has_b1=False, has_b2=False, sm_margin=0,
                  capacity=None, device="cuda", recompute_h=False, dtype="bf16",
-                 keep_bf16_copies=None):
+                 keep_bf16_copies=None, balance_coef=0.0, z_coef=0.0, sequences=1):
         self.desc = L.make_desc(T, E, k, d, F, act=act, alpha=alpha, limit=limit,
                                 linear_offset=linear_offset, out_scale=out_scale,
                                 has_b1=has_b1, has_b2=has_b2, sm_margin=sm_margin,
@@ -105,6 +105,20 @@ class MoEExpertMLP:
         self.dx = z(max(T, 1), d)
         self.dlogits = z(max(T, 1), E, dtype=f32)
         self.ws = torch.zeros(max(L.moe_workspace_size(self.desc), 256), dtype=torch.uint8, device=dev)
+        # the router's losses, with a coefficient that is not 0: computed beside
+        # the routing (router_loss: their weighted sum, balance and z; and each
+        # sequence's experts' counts, its tokens and mean probabilities), their
+        # gradient joined to the router's own in dlogits
+        self.loss_desc = None
+        if T > 0 and (balance_coef or z_coef):
+            self.loss_desc = L.make_router_loss_desc(T, E, k, sequences, balance_coef, z_coef)
+            self.router_loss = z(3, dtype=f32)
+            self.loss_counts = z(sequences, E, dtype=i32)
+            self.loss_tokens = z(sequences + 1, dtype=i32)
+            self.loss_probs = z(sequences, E, dtype=f32)
+            self.loss_ws = torch.empty(L.moe_router_loss_workspace_size(self.loss_desc),
+                                       dtype=torch.uint8, device=dev)
+        self._loss_inputs = None       # logits, mask, seq_offsets of the last routing
         if self.f32:
             self.w1t = z(E, d, self.W1)
             self.w2t = z(E, F, d)
@@ -211,7 +225,10 @@ class MoEExpertMLP:
     def _t(timer, name):
         return timer(name) if timer is not None else contextlib.nullcontext()
 
-    def route(self, x, logits, bias=None, stream=None, timer=None):
+    def route(self, x, logits, bias=None, stream=None, timer=None, mask=None, seq_offsets=None):
+        """Routing and permutation; mask (bool or uint8 [T]) and seq_offsets (int32
+        [sequences+1]) are the router's losses' (which keep them, and the logits,
+        for the backward)."""
         with self._t(timer, "route_permute"):
             if self.mx:          # x_perm's rowwise MXFP8 copy written by the gather
                 L.moe_route_permute_mx(self.desc, logits, bias, x, self.topk_idx, self.topk_w,
@@ -224,6 +241,19 @@ class MoEExpertMLP:
                                     self.counts, self.offsets, self.padded_offsets,
                                     self.tile_prefix, self.row_src, self.row_of, self.x_perm,
                                     self.ws, stream)
+        self._router_losses(logits, mask, seq_offsets, stream, timer)
+
+    def _router_losses(self, logits, mask, seq_offsets, stream, timer):
+        if self.loss_desc is None:
+            if mask is not None or seq_offsets is not None:
+                raise ValueError("a mask and sequences belong to the router's losses, whose "
+                                 "coefficients are 0")
+            return
+        self._loss_inputs = (logits, mask, seq_offsets)
+        with self._t(timer, "router_loss"):
+            L.moe_router_loss_fwd(self.loss_desc, logits, self.topk_idx, mask, seq_offsets,
+                                  self.loss_counts, self.loss_tokens, self.loss_probs,
+                                  self.router_loss, self.loss_ws, stream)
 
     @staticmethod
     def _rowwise(mx):
@@ -233,16 +263,21 @@ class MoEExpertMLP:
     def _colwise(mx):
         return dict(qt=mx["qt"], scale_t=mx["scale_t"], layout="mma")
 
-    def route_fused(self, x, w_router, bias=None, logits_out=None, stream=None, timer=None):
+    def route_fused(self, x, w_router, bias=None, logits_out=None, stream=None, timer=None,
+                    mask=None, seq_offsets=None):
         """Routing from the tokens themselves, in one launch: router GEMM
         (x W_r^T) with the top-k in its epilogue, then the same permutation
-        as route(); w_router bf16 [E,d]; logits_out fp32 [T,E] or None."""
+        as route(); w_router bf16 [E,d]; logits_out fp32 [T,E] or None (the
+        router's losses need them); mask, seq_offsets as route()."""
+        if self.loss_desc is not None and logits_out is None:
+            raise ValueError("the router's losses read the logits: give logits_out")
         self._x_row_fused = False
         with self._t(timer, "route_fused"):
             L.moe_route_permute_fused(self.desc, x, w_router, bias, logits_out, self.topk_idx,
                                       self.topk_w, self.counts, self.offsets,
                                       self.padded_offsets, self.tile_prefix, self.row_src,
                                       self.row_of, self.x_perm, self.ws, stream)
+        self._router_losses(logits_out, mask, seq_offsets, stream, timer)
 
     def set_groups(self, counts, stream=None):
         """Groups given directly (no router): counts int32 [E] on device."""
@@ -468,14 +503,16 @@ class MoEExpertMLP:
             with self._t(timer, "bias_grads"):
                 L.moe_bias_grads(self.desc, self.dy, self.dh, c, po, self.db1p, self.db2, stream)
 
-    def forward(self, x, logits, bias=None, stream=None, timer=None):
-        self.route(x, logits, bias, stream, timer)
+    def forward(self, x, logits, bias=None, stream=None, timer=None, mask=None, seq_offsets=None):
+        self.route(x, logits, bias, stream, timer, mask, seq_offsets)
         self.mlp_forward(stream, timer)
         with self._t(timer, "combine"):
             L.moe_unpermute_combine(self.desc, self.y, self.row_of, self.topk_w, self.out, stream)
         return self.out
 
-    def backward(self, dout, stream=None, timer=None):
+    def backward(self, dout, stream=None, timer=None, dloss=None):
+        """dout [T,d] -> dx, dlogits and the weights' gradients; dloss fp32 [1]: the
+        gradient of the router's weighted loss (None: 1)."""
         with self._t(timer, "combine_bwd"):
             if self.mx:          # dY's rowwise MXFP8 copy written by the combine backward
                 L.moe_unpermute_combine_bwd_mx(self.desc, dout, self.y, self.row_of, self.topk_w,
@@ -490,13 +527,22 @@ class MoEExpertMLP:
         with self._t(timer, "permute_bwd"):
             L.moe_permute_bwd(self.desc, self.dx_perm, self.row_of, self.dx, stream)
         with self._t(timer, "route_bwd"):
-            L.moe_route_bwd(self.desc, self.dw, self.topk_w, self.topk_idx, self.dlogits, stream)
+            if self.loss_desc is not None:
+                logits, mask, seq_offsets = self._loss_inputs
+                L.moe_router_loss_bwd(self.loss_desc, logits, mask, seq_offsets, self.loss_counts,
+                                      self.loss_tokens, dloss,
+                                      dict(dw=self.dw, topk_w=self.topk_w, topk_idx=self.topk_idx),
+                                      self.dlogits, stream)
+            else:
+                L.moe_route_bwd(self.desc, self.dw, self.topk_w, self.topk_idx, self.dlogits,
+                                stream)
         return self.dx
 
-    def step(self, x, logits, bias, dout, stream=None, timer=None):
+    def step(self, x, logits, bias, dout, stream=None, timer=None, mask=None, seq_offsets=None,
+             dloss=None):
         """One whole forward + backward pass of the layer."""
-        self.forward(x, logits, bias, stream, timer)
-        self.backward(dout, stream, timer)
+        self.forward(x, logits, bias, stream, timer, mask, seq_offsets)
+        self.backward(dout, stream, timer, dloss)
 
     def grouped_step(self, stream=None, timer=None, counts=None, x_perm=None, dy=None, y=None,
                      dx_perm=None):
@@ -528,7 +574,11 @@ class MoEExpertMLP:
         and two amax passes; fp32: the transposes of x_perm and dY), and for
         the routed layer top-k, group offsets + assignment (one launch),
         gather, combine, pad-row zeroing, combine backward, permute backward
-        and router backward."""
+        and router backward; the router's losses add two (one where a block
+        takes all tokens: up to 512, beyond 64 experts 128, in up to 8 sequences)."""
         n = (6 + int(self.has_b1) + int(self.has_b2) + (2 if self.mx else 0) + (6 if self.nv else 0)
              + (2 if self.f32 else 0))
+        if routed and self.loss_desc is not None:
+            alone = self.T <= (512 if self.E <= 64 else 128) and self.loss_desc.sequences <= 8
+            n += 1 if alone else 2
         return n + (8 if routed else 0)
