@@ -54,6 +54,7 @@ constexpr int kTmemCols = 2 * kTile;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kMirrorPitch = 40;               // halves from one mirrored row to the next
+constexpr int kOutPitch = 18;                  // the same for 32 x 16 of an unaligned result
 constexpr int kMirrorBytes = 16 * kMirrorPitch * 2;   // 16 x 32 of a tile, a warp
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
                          kEpiWarps * kMirrorBytes;
@@ -76,7 +77,8 @@ enum Product : int {
 
 struct OrthoArgs {
   CUtensorMap x_k[2], x_mn[2]; // both X buffers, 64 x 128 boxes and 64 x 64 boxes
-  CUtensorMap map_a, map_b;
+  CUtensorMap map_a, map_b;    // 64 x 128 boxes
+  CUtensorMap half_a, half_b;  // 64 x 64 boxes
   __half* x[2];                // [batch][rows][ld_x]
   float* state;                // [batch][blocks of 32 x 16], in place
   __half* mat_a;               // [batch][m][ld_a]
@@ -408,21 +410,28 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, cons
       }
     }
     if constexpr (OP == kLast) {
-      if (live) {
-        __nv_bfloat16* o = g.out + static_cast<long long>(w.z) * g.plane_out + row * g.ld_out + col;
+      __nv_bfloat16* o = g.out + static_cast<long long>(w.z) * g.plane_out + row0 * g.ld_out + col;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = parts(v[i]);
-          h[i] = pack_bf16x2(f.x, f.y);
-        }
-        if (g.out_vec && col + 16 <= N) {
-          store_words(o, h);
-        } else {
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = parts(v[i]);
+        h[i] = pack_bf16x2(f.x, f.y);
+      }
+      if (g.out_vec && col - col % 32 + 32 <= N) {
+        if (live) store_words(o + lane * g.ld_out, h);
+      } else {
+        // two rows of 16 at a time: by single elements of 32 rows it took eight
+        // times as long
+        uint32_t* mine = reinterpret_cast<uint32_t*>(mirror_buf) + lane * (kOutPitch / 2);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (col + i < N)
-              reinterpret_cast<uint16_t*>(o)[i] = static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1)));
-        }
+        for (int i = 0; i < 8; ++i) mine[i] = h[i];
+        __syncwarp();
+        const int c = lane & 15;
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(mirror_buf) + c;
+#pragma unroll 4
+        for (int r = lane >> 4; r < 32; r += 2)
+          if (row0 + r < M && col + c < N)
+            reinterpret_cast<uint16_t*>(o)[r * g.ld_out + c] = from[r * kOutPitch];
+        __syncwarp();
       }
     }
   };
@@ -501,19 +510,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Work w = work_at(g, p, t);
         const Shape sh = shape_of(g, w);
         const int now = w.step & 1;
+        // a CTA's half of the second operand in one or two boxes
+        const bool two = sh.n_eff > 128;
         const CUtensorMap* ta = &g.map_a;
-        const CUtensorMap* tb = &g.map_a;
+        const CUtensorMap* tb = two ? &g.map_a : &g.half_a;
         if (w.op == kGram) {
-          ta = tb = g.tall ? &g.x_mn[now] : &g.x_k[now];
+          ta = g.tall ? &g.x_mn[now] : &g.x_k[now];
+          tb = g.tall || !two ? &g.x_mn[now] : &g.x_k[now];
         } else if (w.op != kPoly) {
           ta = g.tall ? &g.x_k[now] : &g.map_b;
-          tb = g.tall ? &g.map_b : &g.x_mn[now];
+          tb = g.tall ? (two ? &g.map_b : &g.half_b) : &g.x_mn[now];
         }
         const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
         const int n0 = sh.col0 + (sh.n_eff / 2) * static_cast<int>(rank);
-        // a second box of the second operand's half, where it lies along its rows
-        const bool two = sh.n_eff > 128;
-        const uint32_t tx = 2 * kSub * (kHalfBytes + (sh.b_mn && !two ? kBoxBytes : kHalfBytes));
+        const uint32_t tx = 2 * kSub * (kHalfBytes + (two ? kHalfBytes : kBoxBytes));
         ok = wait_inputs(g, p, w, abort_flag);
         // what other SMs stored is now read by TMA
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -668,6 +678,7 @@ constexpr int kPrepUnits = 2;
 template <bool F32>
 __global__ void __launch_bounds__(256, 3) k_ortho_norm(const PrepArgs p) {
   __shared__ double s_sum[8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int z = blockIdx.y;
   if (blockIdx.x == 0 && threadIdx.x < 3) p.done[3 * z + threadIdx.x] = 0;
   const unsigned units = (p.cols + 7) / 8;
@@ -719,6 +730,7 @@ __global__ void __launch_bounds__(256, 4) k_ortho_start(const PrepArgs p) {
   __shared__ float s_mul;
   const int z = blockIdx.y;
   const int lane = threadIdx.x & 31;
+  wait_for_previous();
   if (threadIdx.x < 32) {          // fp64 for one warp only
     double sum = 0.0;
     for (int i = lane; i < p.parts; i += 32)
@@ -855,9 +867,10 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   return w;
 }
 
+// Boxes of 64 columns and 64 (half) or 128 rows.
 bool operand_map(CUtensorMap* map, const void* p, long long cols, long long rows, long long batch,
-                 long long ld, long long plane, bool mn) {
-  return encode_map_3d(map, p, cols, rows, batch, ld * 2, plane * 2, 64, mn ? 64 : 128,
+                 long long ld, long long plane, bool half) {
+  return encode_map_3d(map, p, cols, rows, batch, ld * 2, plane * 2, 64, half ? 64 : 128,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }
 
@@ -1013,12 +1026,21 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   const unsigned start_blocks = static_cast<unsigned>(
       (state_blocks + 7) / 8 < fill ? (state_blocks + 7) / 8 : fill);
   const dim3 norm_grid(p.parts, desc->batch), start_grid(start_blocks, desc->batch);
+  cudaLaunchAttribute early;       // placed while the first still runs
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = start_grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
   if (f32) {
     k_ortho_norm<true><<<norm_grid, 256, 0, stream>>>(p);
-    k_ortho_start<true><<<start_grid, 256, 0, stream>>>(p);
+    cudaLaunchKernelEx(&cfg, k_ortho_start<true>, p);
   } else {
     k_ortho_norm<false><<<norm_grid, 256, 0, stream>>>(p);
-    k_ortho_start<false><<<start_grid, 256, 0, stream>>>(p);
+    cudaLaunchKernelEx(&cfg, k_ortho_start<false>, p);
   }
   if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
 
@@ -1029,7 +1051,9 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
       !operand_map(&g.x_mn[0], x0, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true) ||
       !operand_map(&g.x_mn[1], x1, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true) ||
       !operand_map(&g.map_a, half_at(w.a), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
-      !operand_map(&g.map_b, half_at(w.b), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false))
+      !operand_map(&g.map_b, half_at(w.b), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
+      !operand_map(&g.half_a, half_at(w.a), w.m, w.m, desc->batch, w.ld_a, w.plane_a, true) ||
+      !operand_map(&g.half_b, half_at(w.b), w.m, w.m, desc->batch, w.ld_a, w.plane_a, true))
     return MOE_ERR_CUDA;
   g.x[0] = x0;
   g.x[1] = x1;
