@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kLossThreads, N <= 8 ? 4 : 2) k_loss_bwd(const
   fetch(t0 + group);
   for (int r = 0; r < ring.rounds; ++r) {
     const int t = t0 + r * kGroups + group;
-    const bool here = t < t1, counts = next_mask != 0;
+    const bool here = t < t1, marked = next_mask != 0;
     const long long at = static_cast<long long>(t) * a.k;
     float w = next_w, dw = next_dw;
     int idx = next_idx;
@@ -636,19 +636,26 @@ __global__ void __launch_bounds__(kLossThreads, N <= 8 ? 4 : 2) k_loss_bwd(const
         const int n = __ldg(a.tokens + s);
         const float per =
             static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n > 0 ? n : 1));
+        const int32_t* counts = a.counts + static_cast<long long>(s) * a.E;
 #pragma unroll
-        for (int j = 0; j < N / VEC; ++j)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const int e = expert_of<VEC>(lane, j) + i;
-            f[j * VEC + i] =
-                e < a.E ? __ldg(a.counts + static_cast<long long>(s) * a.E + e) * per - 1.0f : 0.0f;
+        for (int j = 0; j < N / VEC; ++j) {
+          const int e = expert_of<VEC>(lane, j);
+          if constexpr (VEC == 4) {
+            const int4 c = e < a.E ? __ldg(reinterpret_cast<const int4*>(counts + e))
+                                   : make_int4(0, 0, 0, 0);
+            f[4 * j] = fmaf(static_cast<float>(c.x), per, -1.0f);
+            f[4 * j + 1] = fmaf(static_cast<float>(c.y), per, -1.0f);
+            f[4 * j + 2] = fmaf(static_cast<float>(c.z), per, -1.0f);
+            f[4 * j + 3] = fmaf(static_cast<float>(c.w), per, -1.0f);
+          } else {
+            f[j] = e < a.E ? fmaf(static_cast<float>(__ldg(counts + e)), per, -1.0f) : 0.0f;
           }
+        }
       } else {
         begin = end = a.T;
       }
     }
-    const bool live = here && t >= begin && t < end && counts;
+    const bool live = here && t >= begin && t < end && marked;
     float* row = slots + group * a.E;
     if constexpr (VEC == 4) {
       ring.wait(r);
@@ -947,7 +954,8 @@ moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float
   a.dlogits = dlogits;
   a.chunk = chunk_tokens(a.T, (a.E <= 64 ? 4 : 2) * sms, kMostTokens);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
-  const bool vec = a.E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
+  const bool vec = a.E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16) &&
+                   aligned(counts, 16);
   return with_shape(a.E, vec, RunBwd{a, stream}) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
