@@ -12,29 +12,35 @@
 // where bf16's 8 would leave an error of one to several percent.  The powers of
 // two kOrthoScaleA and 2^x_exp keep A and X clear of fp16's subnormals.  The
 // state X is held in fp32 beside its operand: a X is exact, and the operand's
-// rounding E enters only through B E,
-// which lies in X's own column space -- a direction that X does not have stays
-// empty, where a rounded state would fill it and grow by a each step (3.44 by
-// default: 485 over five).  In the last two steps B is held as B - s I with
+// rounding E enters only through B E, which lies in X's own column space -- a
+// direction that X does not have stays empty, where a rounded state would fill it
+// and grow by a each step (3.44 by default: 485 over five).  In the last two steps B is held as B - s I with
 // s = tr(B)/m and X' = (a + s) X + (B - s I) X: near the end B's eigenvalues
 // crowd around s, so the rounded part is small.  Not earlier, where E would get
 // into the empty directions through s.
 //
 // All products of all steps are one launch.  Its work is a list of 256 x 256
 // tiles: group of matrices by group, step by step, in a step A's tiles of every
-// matrix, then B's, then X's, dealt out to the CTA pairs in turn.  A tile waits only for its own matrix's
-// tiles of the product before, by a counter: those stand earlier in the list, so
-// with every pair resident (a cooperative launch) each wait ends, and with a few
-// matrices they are done long before, so that no product ends in a wave that is
-// half empty (32 matrices of 7168 x 2048: 15 launches took 15.7 ms).
+// matrix, then B's, then X's, dealt out to the CTA pairs in turn.  A tile waits
+// only for its own matrix's tiles of the product before, by a counter: those stand
+// earlier in the list, so with every pair resident (a cooperative launch) each wait
+// ends, and with a few matrices they are done long before, so that no product ends
+// in a wave that is half empty (32 matrices of 7168 x 2048: 15 launches took 15.7
+// ms; all matrices a product at a time instead of in groups 16.2, in groups 14.5).
 //
 // A pair works as the weight gradients of moe_gemm.cu do (2-SM MMA): warp 0 of
-// each CTA feeds a ring of 32 KB stages by TMA, warp 1 of the lead issues the
-// MMAs, eight warps read the accumulators of the tile before.  What bounds it is
-// the tensor pipe with its operands' way through shared memory, which the
-// epilogue's accesses share: the state therefore lies in blocks of 32 rows by 16
-// columns in the order in which a warp's lanes take it, whole lines at a time,
-// where rows 4 KB apart took four times the passes.
+// each CTA feeds a ring of stages by TMA, warp 1 of the lead issues the MMAs, eight
+// warps read the accumulators of the tile before.  A stage costs its hand-offs as
+// much as its bytes, so it takes 128 of the contraction (867 cycles per 64 of it
+// with 64 a stage, 740 with 128; the MMAs alone take 512).  What bounds it then is
+// the operands' way from L2 (32 KB an SM for every 512 cycles of MMAs, the
+// epilogue's accesses on the same path) and, on large lists, the power limit (clocks
+// fall from 2.07 to about 1.6 GHz).  The epilogue keeps to whole lines where it can:
+// the state lies in blocks of 32 rows by 16 columns in the order in which a warp's
+// lanes take it (rows 4 KB apart took four times the passes through L1).  Measured
+// and not kept: sixteen epilogue warps (5 % slower: the tile's stores, not latency,
+// set the epilogue's pace), operand loads one stage deeper, accumulators fetched a
+// chunk ahead (spills).
 #include <math.h>
 
 #include "moe_ortho.cuh"
@@ -70,27 +76,27 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
 
 enum Product : int {
   kGram = 0,     // A = X X^T (or X^T X), upper tiles, mirrored
-  kPoly = 1,     // B = b A + c A A - s I, upper tiles, mirrored
+  kPoly = 1,     // B = b A + c A A - s I and such (term_of), upper tiles, mirrored
   kUpdate = 2,   // X' = (a + s) X + B X (or X B)
   kLast = 3      // the same into the caller's tensor
 };
 
 struct OrthoArgs {
   CUtensorMap x_k[2], x_mn[2]; // both X buffers, 64 x 128 boxes and 64 x 64 boxes
-  CUtensorMap map_a, map_b;    // 64 x 128 boxes
-  CUtensorMap half_a, half_b;  // 64 x 64 boxes
+  CUtensorMap mat_map[4], mat_half[4];   // the small matrices, 64 x 128 and 64 x 64 boxes
   __half* x[2];                // [batch][rows][ld_x]
   float* state;                // [batch][blocks of 32 x 16], in place
-  __half* mat_a;               // [batch][m][ld_a]
-  __half* mat_b;
+  __half* mat[4];              // [batch][m][ld_a]: A, B and, with joined, two more
   long long ld_x, plane_x, ld_a, plane_a, plane_s;
-  int batch, rows, cols, m, steps;
+  int batch, rows, cols, m;
+  int steps;                   // of the list: one less than asked for with joined
+  int joined;                  // the first of the list are two steps in one
   int groups;                  // of matrices that go through the steps together
   int sym_w, full_w;           // tiles' widths: of A and B, of X
   int tall;                    // more rows than columns: A = X^T X, X' = X B
   float* part;                 // [batch][tiles of A][2 CTAs][8 warps]: sums of A_ii, A_ij^2
   float* shift;                // [batch] s
-  unsigned int* done;          // [batch][3] finished warps' shares of A's, B's, X's tiles
+  unsigned int* done;          // [batch][2] finished warps' shares of small and of X's tiles
   float a, b, c;
   float x_scale, scale;
   __nv_bfloat16* out;
@@ -100,9 +106,9 @@ struct OrthoArgs {
 };
 
 // One tile of the list: rows mb*256 and on, columns nb*width and on; nr: its number
-// among its product's of the matrix.
+// among its product's of the matrix; q: the small product's number in the step.
 struct Work {
-  int op, step, z, mb, nb, nr;
+  int op, step, z, mb, nb, nr, q;
 };
 
 // The list's shape.
@@ -110,7 +116,7 @@ struct Plan {
   int r_tiles, c_tiles;            // of X's rows and columns
   int s_tiles, ratio;              // of A's columns, and how many of them are 256 wide
   int sym, full;                   // tiles of A (and B) and of X
-  int per_matrix, total;           // of one matrix in a step, of all
+  int per_step, per_matrix, total; // of one matrix in a step and in all, of all matrices
 };
 
 __host__ __device__ inline int tiles_of(int n, int width) { return (n + width - 1) / width; }
@@ -129,9 +135,48 @@ __device__ __forceinline__ Plan plan_of(const OrthoArgs& g) {
   p.ratio = kTile / g.sym_w;
   p.sym = sym_tiles(g.m, g.sym_w);
   p.full = p.r_tiles * p.c_tiles;
-  p.per_matrix = 2 * p.sym + p.full;
-  p.total = g.steps * g.batch * p.per_matrix;
+  p.per_step = 2 * p.sym + p.full;
+  p.per_matrix = g.steps * p.per_step + (g.joined ? 4 * p.sym : 0);
+  p.total = g.batch * p.per_matrix;
   return p;
+}
+
+// Small products of a step, and of all steps before it.
+__device__ __forceinline__ int terms_in(const OrthoArgs& g, int step) {
+  return g.joined && step == 0 ? 6 : 2;
+}
+__device__ __forceinline__ int terms_before(const OrthoArgs& g, int step) {
+  return step == 0 ? 0 : 2 * step + (g.joined ? 4 : 0);
+}
+
+// Two steps in one (with n >= 2 m the 3 m^2 n of a step's long products are more
+// than the 3 m^3 that take their place): from A = X X^T alone
+//     B = b A + c A A,  N = 2 a B + B B,  A' = a^2 A + N A,  B' = b A' + c A' A',
+//     Q = a (B + B') + B' B,  X <- a^2 X + Q X
+// as everything here is a polynomial of A, so that the products commute and are
+// symmetric.  Only the first two: there A's rounding costs no more than in two
+// steps, later it does (five steps, 256 x 900, full rank: 2e-3 of the result, with
+// the second and third joined 8e-3).
+struct Term {
+  int left, right, dst;        // which small matrices
+  int in, in2;                 // added times keep; in2 < 0: none
+  float scale, keep;           // dst = scale * left right + keep * (in + in2)
+};
+
+__device__ __forceinline__ Term term_of(const OrthoArgs& g, int q) {
+  const float square = g.c / (kOrthoScaleA * kOrthoScaleA), linear = g.b / kOrthoScaleA;
+  switch (q) {
+    case 1: return {0, 0, 1, 0, -1, square, linear};
+    case 2: return {1, 1, 2, 1, -1, 1.0f, 2.0f * g.a};
+    case 3: return {2, 0, 3, 0, -1, 1.0f, g.a * g.a};
+    case 4: return {3, 3, 2, 3, -1, square, linear};
+    default: return {2, 1, 0, 1, 2, 1.0f, g.a};
+  }
+}
+
+// The small matrix that X is multiplied by.
+__device__ __forceinline__ int factor_of(const OrthoArgs& g, int step) {
+  return g.joined && step == 0 ? 0 : 1;
 }
 
 // Symmetric products go row by row of 256; X with the small side inside, so that
@@ -139,19 +184,25 @@ __device__ __forceinline__ Plan plan_of(const OrthoArgs& g) {
 __device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t) {
   Work w;
   // group i holds the matrices floor(i batch / groups) and on
-  const int share = g.steps * p.per_matrix;
-  const int q = t / share;
-  const int i = static_cast<int>((static_cast<long long>(q + 1) * g.groups - 1) / g.batch);
+  const int i = static_cast<int>(
+      (static_cast<long long>(t / p.per_matrix + 1) * g.groups - 1) / g.batch);
   const int z0 = static_cast<int>(static_cast<long long>(i) * g.batch / g.groups);
   const int z1 = static_cast<int>(static_cast<long long>(i + 1) * g.batch / g.groups);
-  int r = t - z0 * share;
-  const int per_step = (z1 - z0) * p.per_matrix;
-  w.step = r / per_step;
-  r -= w.step * per_step;
-  const int sym = (z1 - z0) * p.sym;
-  if (r < 2 * sym) {
-    w.op = r < sym ? kGram : kPoly;
-    r -= w.op == kGram ? 0 : sym;
+  int r = t - z0 * p.per_matrix;
+  const int first = (z1 - z0) * (p.per_step + (g.joined ? 4 * p.sym : 0));
+  w.step = 0;
+  if (r >= first) {
+    r -= first;
+    const int per_step = (z1 - z0) * p.per_step;
+    w.step = 1 + r / per_step;
+    r -= (w.step - 1) * per_step;
+  }
+  const int sym = (z1 - z0) * p.sym, small = terms_in(g, w.step) * sym;
+  w.q = 0;
+  if (r < small) {
+    w.q = r / sym;
+    w.op = w.q == 0 ? kGram : kPoly;
+    r -= w.q * sym;
     const int z = r / p.sym;
     w.z = z0 + z;
     r -= z * p.sym;
@@ -164,7 +215,7 @@ __device__ __forceinline__ Work work_at(const OrthoArgs& g, const Plan& p, int t
     w.nb = w.mb * p.ratio + r;
   } else {
     w.op = w.step + 1 == g.steps ? kLast : kUpdate;
-    r -= 2 * sym;
+    r -= small;
     const int z = r / p.full;
     w.z = z0 + z;
     r -= z * p.full;
@@ -207,9 +258,12 @@ __device__ __forceinline__ bool wait_inputs(const OrthoArgs& g, const Plan& p, c
                                             volatile int* abort_flag) {
   if (w.op == kGram && w.step == 0) return true;
   const unsigned int share = 2 * kEpiWarps;
-  const unsigned int* ctr = g.done + 3 * w.z + (w.op == kGram ? 2 : w.op == kPoly ? 0 : 1);
-  const unsigned int target =
-      share * (w.op == kGram ? w.step * p.full : (w.step + 1) * p.sym);
+  const bool gram = w.op == kGram;
+  const unsigned int* ctr = g.done + 2 * w.z + (gram ? 1 : 0);
+  // a matrix's small products follow one another, so their tiles' count tells which
+  // of them are finished
+  const int before = terms_before(g, w.step) + (w.op == kPoly ? w.q : terms_in(g, w.step));
+  const unsigned int target = share * (gram ? w.step * p.full : before * p.sym);
   unsigned int v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
   if (v >= target) return true;
@@ -296,26 +350,31 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, cons
   const long long ld = kSym ? g.ld_a : g.ld_x;
   const long long at0 = static_cast<long long>(w.z) * (kSym ? g.plane_a : g.plane_x) + row * ld +
                         col0;
-  // v = keep * (what was loaded) + accumulator, where not kGram; then * scale
+  // v = keep * (what was loaded) + accumulator, where not kGram, and * scale
+  Term term = {};
+  if constexpr (OP == kPoly) term = term_of(g, w.q);
   float s = 0.0f, keep = 0.0f, scale = 1.0f;
   if constexpr (OP == kGram) {
     scale = kOrthoScaleA / (g.x_scale * g.x_scale);
   } else if constexpr (OP == kPoly) {
-    scale = g.c / (kOrthoScaleA * kOrthoScaleA);
-    keep = g.b / kOrthoScaleA;
+    scale = term.scale;
+    keep = term.keep;
     if (shifted && diagonal) {
       s = shift_of(g, w.z, p.sym * 2 * kEpiWarps, lane);
       if (w.nr == 0 && rank == 0 && ewarp == 0 && lane == 0) g.shift[w.z] = s;
     }
   } else {
-    keep = g.a + (shifted ? __ldcg(g.shift + w.z) : 0.0f);
+    keep = (g.joined && w.step == 0 ? g.a * g.a : g.a) +
+           (shifted ? __ldcg(g.shift + w.z) : 0.0f);
     if constexpr (OP == kLast) scale = g.scale / g.x_scale;
   }
   const F2 keep2 = f2(keep), scale2 = f2(scale);
-  const __half* src = g.mat_a;
-  __half* dst = OP == kGram ? g.mat_a : OP == kPoly ? g.mat_b : g.x[(w.step + 1) & 1];
+  const __half* src = g.mat[term.in];
+  const __half* src2 = term.in2 > 0 ? g.mat[term.in2] : nullptr;
+  __half* dst = OP == kGram ? g.mat[0] : OP == kPoly ? g.mat[term.dst] : g.x[(w.step + 1) & 1];
   constexpr int kBuf = OP == kGram ? 1 : kAhead;
-  uint32_t in[kBuf][kState ? 16 : 8] = {};   // kPoly: A as fp16; the state as fp32
+  // kPoly: one or two matrices' fp16; the state's fp32
+  uint32_t in[kBuf][OP == kGram ? 8 : 16] = {};
   float* state = nullptr;
   if constexpr (kState)
     state = g.state + w.z * g.plane_s + state_at((N + 15) / 16, row, col0);
@@ -329,6 +388,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, cons
           load_words(state + 1024 * j + 256, &in[b][8]);
         } else {
           load_words(src + at0 + 32 * j, &in[b][0]);
+          if (src2 != nullptr) load_words(src2 + at0 + 32 * j, &in[b][8]);
         }
       }
     }
@@ -343,7 +403,10 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, cons
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = f2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
-      if constexpr (OP == kPoly) v[i] = fma2(keep2, half_pair(in[b][i]), v[i] * scale2);
+      if constexpr (OP == kPoly) {
+        v[i] = fma2(keep2, half_pair(in[b][i]), v[i] * scale2);
+        if (src2 != nullptr) v[i] = fma2(keep2, half_pair(in[b][8 + i]), v[i]);
+      }
       if constexpr (kState)
         v[i] = fma2(keep2, f2(__uint_as_float(in[b][2 * i]), __uint_as_float(in[b][2 * i + 1])),
                     v[i]);
@@ -512,14 +575,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int now = w.step & 1;
         // a CTA's half of the second operand in one or two boxes
         const bool two = sh.n_eff > 128;
-        const CUtensorMap* ta = &g.map_a;
-        const CUtensorMap* tb = two ? &g.map_a : &g.half_a;
+        const CUtensorMap *ta, *tb;
         if (w.op == kGram) {
           ta = g.tall ? &g.x_mn[now] : &g.x_k[now];
           tb = g.tall || !two ? &g.x_mn[now] : &g.x_k[now];
-        } else if (w.op != kPoly) {
-          ta = g.tall ? &g.x_k[now] : &g.map_b;
-          tb = g.tall ? (two ? &g.map_b : &g.half_b) : &g.x_mn[now];
+        } else if (w.op == kPoly) {
+          const Term term = term_of(g, w.q);
+          ta = &g.mat_map[term.left];
+          tb = two ? &g.mat_map[term.right] : &g.mat_half[term.right];
+        } else {
+          const int f = factor_of(g, w.step);
+          ta = g.tall ? &g.x_k[now] : &g.mat_map[f];
+          tb = !g.tall ? &g.x_mn[now] : two ? &g.mat_map[f] : &g.mat_half[f];
         }
         const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
         const int n0 = sh.col0 + (sh.n_eff / 2) * static_cast<int>(rank);
@@ -654,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
         if (lane == 0)
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.done + 3 * w.z + w.op)
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.done + 2 * w.z + (w.op == kUpdate ? 1 : 0))
                        : "memory");
       }
     }
@@ -680,7 +747,7 @@ __global__ void __launch_bounds__(256, 3) k_ortho_norm(const PrepArgs p) {
   __shared__ double s_sum[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int z = blockIdx.y;
-  if (blockIdx.x == 0 && threadIdx.x < 3) p.done[3 * z + threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.done[2 * z + threadIdx.x] = 0;
   const unsigned units = (p.cols + 7) / 8;
   const unsigned count = p.rows * units;
   const unsigned stride = gridDim.x * 256;
@@ -828,11 +895,22 @@ moe_status_t check_ortho_desc(const moe_orthogonalize_desc_t* d) {
 }
 
 struct Layout {
+  bool joined;
   int m;                                   // the small side
   long long ld_x, plane_x, ld_a, plane_a, plane_s;  // elements
   int parts;                               // kGram's sums of a matrix
-  size_t x0, x1, state, a, b, part, norm, shift, done, bytes;
+  size_t x0, x1, state, mat[4], part, norm, shift, done, bytes;
 };
+
+// Whether the first two steps are taken as one: where that saves products (see
+// term_of), and there are tiles enough that products and not their sequence take the
+// time.  (32 matrices of 7168 x 2048: 13.9 -> 12.4 ms; 64 of 2048 x 1024: 2.94 ->
+// 2.80 ms.)
+bool joins_steps(const moe_orthogonalize_desc_t* d) {
+  const int m = d->rows < d->cols ? d->rows : d->cols, n = d->rows < d->cols ? d->cols : d->rows;
+  return d->steps >= 5 && n >= 2 * m &&
+         static_cast<long long>(d->batch) * sym_tiles(m, kTile) >= 128;
+}
 
 Layout layout_of(const moe_orthogonalize_desc_t* d) {
   Layout w = {};
@@ -857,12 +935,12 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   w.x0 = take(n * w.plane_x * 2);
   w.x1 = take(n * w.plane_x * 2);
   w.state = take(n * w.plane_s * 4);
-  w.a = take(n * w.plane_a * 2);
-  w.b = take(n * w.plane_a * 2);
+  w.joined = joins_steps(d);
+  for (int i = 0; i < 4; ++i) w.mat[i] = i < 2 || w.joined ? take(n * w.plane_a * 2) : w.mat[0];
   w.part = take(n * w.parts * 8);
   w.norm = take(n * kNormParts * 8);
   w.shift = take(n * 4);
-  w.done = take(n * 12);
+  w.done = take(n * 8);
   w.bytes = at > 0 ? at : 256;
   return w;
 }
@@ -881,7 +959,7 @@ cudaError_t launch_steps(OrthoArgs& g, int sms, cudaStream_t s) {
                                          static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
   // narrower tiles as long as they are one for each pair: a product of few tiles
-  // takes as long as one of them (8 matrices of 256 x 512: 150 -> WWW us)
+  // takes as long as one of them (8 matrices of 256 x 512: 149 -> 117 us)
   const int most = sms / 2;
   auto sym = [&](int width) { return static_cast<long long>(g.batch) * sym_tiles(g.m, width); };
   auto full = [&](int width) {
@@ -1049,18 +1127,18 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   if (!operand_map(&g.x_k[0], x0, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, false) ||
       !operand_map(&g.x_k[1], x1, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, false) ||
       !operand_map(&g.x_mn[0], x0, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true) ||
-      !operand_map(&g.x_mn[1], x1, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true) ||
-      !operand_map(&g.map_a, half_at(w.a), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
-      !operand_map(&g.map_b, half_at(w.b), w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
-      !operand_map(&g.half_a, half_at(w.a), w.m, w.m, desc->batch, w.ld_a, w.plane_a, true) ||
-      !operand_map(&g.half_b, half_at(w.b), w.m, w.m, desc->batch, w.ld_a, w.plane_a, true))
+      !operand_map(&g.x_mn[1], x1, desc->cols, desc->rows, desc->batch, w.ld_x, w.plane_x, true))
     return MOE_ERR_CUDA;
+  for (int i = 0; i < 4; ++i) {
+    g.mat[i] = half_at(w.mat[i]);
+    if (!operand_map(&g.mat_map[i], g.mat[i], w.m, w.m, desc->batch, w.ld_a, w.plane_a, false) ||
+        !operand_map(&g.mat_half[i], g.mat[i], w.m, w.m, desc->batch, w.ld_a, w.plane_a, true))
+      return MOE_ERR_CUDA;
+  }
   g.x[0] = x0;
   g.x[1] = x1;
   g.state = p.state;
   g.plane_s = w.plane_s;
-  g.mat_a = half_at(w.a);
-  g.mat_b = half_at(w.b);
   g.ld_x = w.ld_x;
   g.plane_x = w.plane_x;
   g.ld_a = w.ld_a;
@@ -1069,7 +1147,8 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   g.rows = desc->rows;
   g.cols = desc->cols;
   g.m = w.m;
-  g.steps = desc->steps;
+  g.joined = w.joined;
+  g.steps = desc->steps - (w.joined ? 1 : 0);
   g.tall = desc->rows > desc->cols;
   g.part = reinterpret_cast<float*>(base + w.part);
   g.shift = reinterpret_cast<float*>(base + w.shift);

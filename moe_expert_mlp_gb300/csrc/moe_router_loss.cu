@@ -4,9 +4,9 @@
 // of a group of 8 lanes, whose exchanges give its maximum, its sum of exponentials
 // and, in the backward, <f, p>; the next token's row is on its way meanwhile.  Four
 // tokens a warp: with a warp a token and 256 experts an exchange of five steps, the
-// reciprocal and the loop counted for 8 values a lane, not 32 (178 instructions a
-// token in the forward, and 22 us for 65536 tokens where this takes WW).  What they cannot do without is that read (and the backward's
-// write); the arithmetic, one exponential an element, is below it.
+// reciprocal and the loop count for 8 values a lane, not 32 (178 instructions a token
+// in the forward, where this takes 100).  What they cannot do without is that read
+// (and the backward's write); the arithmetic, one exponential an element, is below it.
 //
 // Forward: the tokens are cut into chunks of equal length, one block each, and
 // a chunk at the ends of sequences into segments.  Chunks and sequences both

@@ -109,9 +109,10 @@ def orthogonalize(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0):
     return scale * (x.T if tall else x)
 
 
-def orthogonalize_rounded(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0):
+def orthogonalize_rounded(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0, joined=False):
     """The same with the roundings that the kernels make: the products' operands as
-    fp16 of values times powers of two."""
+    fp16 of values times powers of two; joined: the first two steps as one, by
+    polynomials of A."""
     a, b, c = coefficients
 
     def half(v, by):
@@ -121,10 +122,17 @@ def orthogonalize_rounded(u, steps=5, coefficients=DEFAULT, eps=1e-7, scale=1.0)
     x = u / (np.linalg.norm(u) + eps)
     tall = x.shape[0] > x.shape[1]
     x = x.T if tall else x
-    for step in range(steps):
+    for step in range(1 if joined else 0, steps):
         hi = half(x, xs)
         A = half(hi @ hi.T, 4096.0)
         B = b * A + c * (A @ A)
+        if joined and step == 1:
+            B = half(B, 1.0)
+            N = half(2 * a * B + B @ B, 1.0)
+            A2 = half(a * a * A + N @ A, 4096.0)
+            B2 = half(b * A2 + c * (A2 @ A2), 1.0)
+            x = a * a * x + half(a * (B + B2) + B2 @ B, 1.0) @ hi
+            continue
         s = 0.0
         if step >= steps - 2:
             s = (b * np.trace(A) + c * (A * A).sum()) / len(A)

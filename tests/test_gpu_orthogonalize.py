@@ -97,6 +97,14 @@ def run(g, steps=5, scale=1.0, dtype=torch.bfloat16, mom=None, momentum=0.0, dam
         None if mo is None else f64(mo))
 
 
+def joined(shape, steps):
+    """Whether the kernels take the first two steps as one."""
+    b, r, c = shape
+    m, n = sorted((r, c))
+    tiles = -(-m // 256)
+    return m > 128 and steps >= 5 and n >= 2 * m and b * tiles * (tiles + 1) // 2 >= 128
+
+
 def check(grad, mom, out, mom_out, steps=5, scale=1.0, momentum=0.0, dampening=0.0, nesterov=False,
           coefficients=O.DEFAULT, eps=1e-7):
     for i in range(len(grad)):
@@ -106,7 +114,8 @@ def check(grad, mom, out, mom_out, steps=5, scale=1.0, momentum=0.0, dampening=0
             mag = abs(momentum) * np.abs(mom[i]) + abs(1 - dampening) * np.abs(grad[i])
             assert np.all(np.abs(mom_out[i] - m2) <= 6 * O.U32 * mag + 1e-44)
         ref = O.orthogonalize(u, steps, coefficients, eps, scale)
-        rounded = O.orthogonalize_rounded(u, steps, coefficients, eps, scale)
+        rounded = O.orthogonalize_rounded(u, steps, coefficients, eps, scale,
+                                          joined(grad.shape, steps))
         size = np.linalg.norm(ref)
         if size == 0:
             assert not out[i].any()
@@ -239,6 +248,13 @@ def test_graph_on_another_stream(shape):
         graph.replay()
         torch.cuda.synchronize()
         check(f64(g), before, f64(out), f64(mom), momentum=0.9, nesterov=True)
+
+
+@pytest.mark.parametrize("shape", [(43, 300, 640), (43, 610, 300), (130, 140, 300)])
+@pytest.mark.parametrize("kind,steps", [("full", 5), ("few tokens", 5), ("mixed", 6), ("falling", 5)])
+def test_first_two_steps_as_one(shape, kind, steps):
+    assert joined(shape, steps)
+    check(*run(values(shape, kind, 15), steps=steps, scale=0.3), steps=steps, scale=0.3)
 
 
 def test_many_small_matrices():

@@ -102,3 +102,15 @@ def test_what_fp16_operands_cost(shape, steps, bound):
             ref = O.orthogonalize(g, steps)
             off = np.linalg.norm(O.orthogonalize_rounded(g, steps) - ref) / np.linalg.norm(ref)
             assert off < np.sqrt(bound ** 2 - 2.0 ** -16), (name, off)
+
+
+@pytest.mark.parametrize("shape", [(64, 160), (300, 130), (200, 450)])
+def test_first_two_steps_as_one_cost_no_more(shape):
+    """Two steps by polynomials of A are the same update, and stay within what an
+    update of five steps may be off by."""
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        for name, g in spectra(rng, shape).items():
+            ref = O.orthogonalize(g, 5)
+            off = np.linalg.norm(O.orthogonalize_rounded(g, 5, joined=True) - ref) / np.linalg.norm(ref)
+            assert off < np.sqrt(5e-3 ** 2 - 2.0 ** -16), (name, off)
