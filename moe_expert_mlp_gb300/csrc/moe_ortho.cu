@@ -1084,7 +1084,7 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrice
   p.x_scale = x_scale;
   if (small_ortho(desc->rows, desc->cols)) {
     SmallOrthoArgs small = {p, static_cast<__nv_bfloat16*>(out.p), out.ld, out.plane, out_vec,
-                            desc->steps, desc->a, desc->b, desc->c, desc->scale};
+                            desc->steps, desc->a, desc->b, desc->c, desc->scale, status};
     return launch_small_ortho(small, sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   p.part = reinterpret_cast<double*>(base + w.norm);

@@ -93,11 +93,11 @@ __device__ __forceinline__ void direction(const PrepArgs& p, float (&g)[8], cons
   for (int i = 0; i < 8; ++i) g[i] = p.nesterov ? fmaf(p.mu, m[i], p.nu * g[i]) : m[i];
 }
 
-// Squares of 8 N values: in fp32, and in fp64 where their sum leaves fp32's middle
-// range.  (One fp64 addition for them all: this GPU's rate of those is 1/64.)
+// Squares of 8 N values in fp32; false where their sum is not in its middle range.
 template <int N>
-__device__ __forceinline__ double squares_of(const float (&u)[N][8]) {
-  float sq[N], all = 0.0f;
+__device__ __forceinline__ bool middle_squares(const float (&u)[N][8], float& all) {
+  float sq[N];
+  all = 0.0f;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     sq[q] = 0.0f;
@@ -105,14 +105,21 @@ __device__ __forceinline__ double squares_of(const float (&u)[N][8]) {
     for (int k = 0; k < 8; ++k) sq[q] = fmaf(u[q][k], u[q][k], sq[q]);
     all += sq[q];
   }
-  if ((all > 1e-30f && all < 1e30f) || all == 0.0f) {
-    bool zeros = true;             // a sum of 0 is one of zeros, or of squares below fp32's range
+  if (all > 1e-30f && all < 1e30f) return true;
+  bool zeros = all == 0.0f;          // a sum of 0 is one of zeros, or of squares below fp32's range
 #pragma unroll
-    for (int q = 0; q < N; ++q)
+  for (int q = 0; q < N; ++q)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) zeros = zeros && u[q][k] == 0.0f;
-    if (all != 0.0f || zeros) return all;
-  }
+    for (int k = 0; k < 8; ++k) zeros = zeros && u[q][k] == 0.0f;
+  return zeros;
+}
+
+// The same in fp64 where fp32 does not hold them.  (One fp64 addition for them all:
+// this GPU's rate of those is 1/64.)
+template <int N>
+__device__ __forceinline__ double squares_of(const float (&u)[N][8]) {
+  float all;
+  if (middle_squares(u, all)) return all;
   double sum = 0.0;
 #pragma unroll
   for (int q = 0; q < N; ++q)
@@ -135,6 +142,7 @@ struct SmallOrthoArgs {
   int out_vec;                 // out's rows may be written 8 elements at a time
   int steps;
   float a, b, c, scale;
+  int* status;
 };
 bool small_ortho(int rows, int cols);
 cudaError_t launch_small_ortho(const SmallOrthoArgs& args, int sms, cudaStream_t s);
