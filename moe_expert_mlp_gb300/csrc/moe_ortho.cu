@@ -421,7 +421,7 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, cons
         }
       }
     }
-    fetch(j + kAhead, b);
+    fetch(j + kBuf, b);
     uint32_t h[8];
     if constexpr (OP != kLast) {
 #pragma unroll
@@ -500,14 +500,14 @@ __device__ __forceinline__ bool epilogue(const OrthoArgs& g, const Plan& p, cons
   };
 
 #pragma unroll
-  for (int b = 0; b < kAhead; ++b) fetch(b, kBuf > 1 ? b : 0);
+  for (int b = 0; b < kBuf; ++b) fetch(b, b);
   if (!ready()) return false;
   if (nch <= 0) read();
 #pragma unroll 1
-  for (int j = 0; j < nch; j += kAhead) {
+  for (int j = 0; j < nch; j += kBuf) {
 #pragma unroll
-    for (int b = 0; b < kAhead; ++b)
-      if (j + b < nch) chunk(j + b, kBuf > 1 ? b : 0);
+    for (int b = 0; b < kBuf; ++b)
+      if (j + b < nch) chunk(j + b, b);
   }
   if constexpr (OP == kGram) {
     if (shifted) {
@@ -566,43 +566,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ====================== TMA producer (both CTAs) ======================
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      for (int t = pair; t < p.total && ok; t += npairs) {
-        const Work w = work_at(g, p, t);
-        const Shape sh = shape_of(g, w);
-        const int now = w.step & 1;
-        // a CTA's half of the second operand in one or two boxes
-        const bool two = sh.n_eff > 128;
-        const CUtensorMap *ta, *tb;
-        if (w.op == kGram) {
-          ta = g.tall ? &g.x_mn[now] : &g.x_k[now];
-          tb = g.tall || !two ? &g.x_mn[now] : &g.x_k[now];
-        } else if (w.op == kPoly) {
-          const Term term = term_of(g, w.q);
-          ta = &g.mat_map[term.left];
-          tb = two ? &g.mat_map[term.right] : &g.mat_half[term.right];
-        } else {
-          const int f = factor_of(g, w.step);
-          ta = g.tall ? &g.x_k[now] : &g.mat_map[f];
-          tb = !g.tall ? &g.x_mn[now] : two ? &g.mat_map[f] : &g.mat_half[f];
-        }
-        const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
-        const int n0 = sh.col0 + (sh.n_eff / 2) * static_cast<int>(rank);
-        const uint32_t tx = 2 * kSub * (kHalfBytes + (two ? kHalfBytes : kBoxBytes));
-        ok = wait_inputs(g, p, w, abort_flag);
-        // what other SMs stored is now read by TMA
-        asm volatile("fence.proxy.async;" ::: "memory");
-        for (int st = 0; st < sh.num_st && ok; ++st) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, g.status, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * kStageBytes;
-          uint8_t* sb = sa + kSub * kHalfBytes;
-          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          // boxes past a tensor's end are filled with zeros and count whole
+    // (the whole warp waits and one elected lane issues: of a single lane's branch
+    // each load took 250 cycles to issue and each MMA 95)
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int t = pair; t < p.total && ok; t += npairs) {
+      const Work w = work_at(g, p, t);
+      const Shape sh = shape_of(g, w);
+      const int now = w.step & 1;
+      // a CTA's half of the second operand in one or two boxes
+      const bool two = sh.n_eff > 128;
+      const CUtensorMap *ta, *tb;
+      if (w.op == kGram) {
+        ta = g.tall ? &g.x_mn[now] : &g.x_k[now];
+        tb = g.tall || !two ? &g.x_mn[now] : &g.x_k[now];
+      } else if (w.op == kPoly) {
+        const Term term = term_of(g, w.q);
+        ta = &g.mat_map[term.left];
+        tb = two ? &g.mat_map[term.right] : &g.mat_half[term.right];
+      } else {
+        const int f = factor_of(g, w.step);
+        ta = g.tall ? &g.x_k[now] : &g.mat_map[f];
+        tb = !g.tall ? &g.x_mn[now] : two ? &g.mat_map[f] : &g.mat_half[f];
+      }
+      const int m0 = w.mb * kTile + 128 * static_cast<int>(rank);
+      const int n0 = sh.col0 + (sh.n_eff / 2) * static_cast<int>(rank);
+      const uint32_t tx = 2 * kSub * (kHalfBytes + (two ? kHalfBytes : kBoxBytes));
+      ok = __all_sync(0xFFFFFFFFu, wait_inputs(g, p, w, abort_flag));
+      // what other SMs stored is now read by TMA: the one proxy fence on the way
+      // from their stores, here rather than at each of those
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      for (int st = 0; st < sh.num_st && ok; ++st) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait(&empty_bar[stage], phase ^ 1u, g.status, abort_flag));
+        if (!ok) break;
+        uint8_t* sa = smem + stage * kStageBytes;
+        uint8_t* sb = sa + kSub * kHalfBytes;
+        const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+        // boxes past a tensor's end are filled with zeros and count whole
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
@@ -620,16 +622,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(sb + u * kHalfBytes, tb, fb, k0, n0, w.z);
             }
           }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
   } else if (warp == 1) {
     // ====================== MMA issuer (lead CTA only) ====================
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       uint32_t stage = 0, phase = 0;
       int it = 0;
       bool ok = true;
@@ -639,34 +642,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t idesc = idesc_f16(kTile, sh.n_eff, sh.a_mn, sh.b_mn);
         const int acc = it & 1;
         const uint32_t acc_par = (it >> 1) & 1;
-        if (!mbar_wait(&tempty_bar[acc], acc_par ^ 1u, g.status, abort_flag)) break;
+        if (!__all_sync(0xFFFFFFFFu,
+                        mbar_wait(&tempty_bar[acc], acc_par ^ 1u, g.status, abort_flag)))
+          break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kTile;
         for (int st = 0; st < sh.num_st; ++st) {
-          if (!mbar_wait(&full_bar[stage], phase, g.status, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full_bar[stage], phase, g.status, abort_flag));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + stage * kStageBytes);
-          const uint32_t b_base = a_base + kSub * kHalfBytes;
+          if (elect_one()) {
+            const uint32_t a_base = smem_u32(smem + stage * kStageBytes);
+            const uint32_t b_base = a_base + kSub * kHalfBytes;
 #pragma unroll
-          for (int k = 0; k < kSub * kBK / 16; ++k) {
-            const uint32_t ab = a_base + (k / 4) * kHalfBytes, bb = b_base + (k / 4) * kHalfBytes;
-            const uint64_t ad = sh.a_mn ? sdesc_sw128(ab + k % 4 * 2048, kBoxBytes, 1024)
-                                        : sdesc_sw128(ab + k % 4 * 32, 16, 1024);
-            const uint64_t bd = sh.b_mn ? sdesc_sw128(bb + k % 4 * 2048, kBoxBytes, 1024)
-                                        : sdesc_sw128(bb + k % 4 * 32, 16, 1024);
-            umma_bf16_pair(d_tmem, ad, bd, idesc, (st > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kSub * kBK / 16; ++k) {
+              const uint32_t ab = a_base + (k / 4) * kHalfBytes, bb = b_base + (k / 4) * kHalfBytes;
+              const uint64_t ad = sh.a_mn ? sdesc_sw128(ab + k % 4 * 2048, kBoxBytes, 1024)
+                                          : sdesc_sw128(ab + k % 4 * 32, 16, 1024);
+              const uint64_t bd = sh.b_mn ? sdesc_sw128(bb + k % 4 * 2048, kBoxBytes, 1024)
+                                          : sdesc_sw128(bb + k % 4 * 32, 16, 1024);
+              umma_bf16_pair(d_tmem, ad, bd, idesc, (st > 0 || k > 0) ? 1u : 0u);
+            }
+            umma_commit_pair(&empty_bar[stage]);
+            if (st + 1 == sh.num_st) umma_commit_pair(&tfull_bar[acc]);
           }
-          umma_commit_pair(&empty_bar[stage]);
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair(&tfull_bar[acc]);
       }
     }
   } else {
@@ -700,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto read = [&]() {                    // the accumulator is free again
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+        if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
       };
       bool done;
       if (w.op == kGram)
@@ -716,9 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         done = epilogue<kLast>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
                                read);
       if (!done) break;
-      if (w.op != kLast) {
-        // the tile's stores, before the count that tells of them (TMA reads them)
-        asm volatile("fence.proxy.async;" ::: "memory");
+      if (w.op != kLast) {                   // (the readers fence before their TMA)
         __syncwarp();
         if (lane == 0)
           asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.done + 2 * w.z + (w.op == kUpdate ? 1 : 0))
