@@ -1014,10 +1014,13 @@ moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float
  * cores with fp16 operands and fp32 accumulation, the state X is kept in 32 bits
  * and out rounded once to bf16.  Up to eight of the default steps the 2-norm of
  * out's error is below 1e-2 of out's (sides below 16: 2e-2; 5 steps on matrices
- * with sides of 64 and more: 5e-3), rounding included.  (a, b, c) with which a singular value in
- * [0,1] could reach 2 within the steps, or |b| s^2 + |c| s^4 could pass 16, are
- * refused with MOE_ERR_UNSUPPORTED.  A zero matrix stays zero; an Inf or NaN
- * reaches its own matrix only. */
+ * with sides of 64 and more: 5e-3), rounding included.  (a, b, c) with which a
+ * singular value in [0,1] could reach 2 within the steps, or |b| s^2 + |c| s^4
+ * could pass 16, are refused with MOE_ERR_UNSUPPORTED.  A zero matrix stays zero;
+ * an Inf or NaN reaches its own matrix only.  With a short side above 128, or a long
+ * one that eight SMs' registers do not hold, the steps are one cooperative launch
+ * that takes as many SMs as there are tiles (MOE_ERR_CUDA where it cannot be
+ * resident). */
 typedef struct {
   void* p;        /* element (i, r, c) at p[i*plane + r*ld + c]; inputs are not written */
   int64_t ld;     /* elements from one row to the next */

@@ -259,3 +259,64 @@ def test_first_two_steps_as_one(shape, kind, steps):
 
 def test_many_small_matrices():
     check(*run(values((200, 24, 40), "mixed", 14)))
+
+
+# clusters of one to eight, whose shares of 64 or 128 rows are not all alike
+@pytest.mark.parametrize("shape", [(3, 50, 61), (3, 64, 100), (3, 50, 150), (2, 64, 250), (2, 64, 300),
+                                   (2, 33, 384), (2, 64, 448), (2, 17, 500), (2, 100, 80), (2, 128, 129),
+                                   (2, 128, 160), (2, 90, 190), (2, 128, 224), (2, 65, 256)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_small_matrices_of_every_cluster(shape, tall):
+    b, m, n = shape
+    check(*run(values((b, n, m) if tall else shape, "full", 21)))
+
+
+@pytest.mark.parametrize("shape", [(20, 64, 512), (6, 128, 900), (8, 256, 512), (3, 520, 700), (43, 300, 640)])
+def test_many_runs_give_equal_bits(shape):
+    import moe_expert_mlp_gb300 as m
+    g = torch.from_numpy(values(shape, "full", 22)).cuda().bfloat16()
+    desc = m.make_orthogonalize_desc(*shape)
+    ws = torch.empty(m.moe_orthogonalize_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    first, out = torch.empty_like(g), torch.empty_like(g)
+    m.moe_orthogonalize(desc, g, first, ws)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(40):
+        m.moe_orthogonalize(desc, g, out.zero_(), ws)
+        differ += (out != first).sum()
+    assert int(differ) == 0 and m.moe_read_device_status() == 0
+
+
+def test_two_calls_at_once_and_graphs_that_share_a_workspace():
+    """Calls on two streams with a workspace each, large (every SM) and small; then
+    two graphs over one workspace, replayed in turn."""
+    import moe_expert_mlp_gb300 as m
+    shapes = [(4, 300, 700), (2, 520, 400), (8, 64, 512)]
+    calls = []
+    for i, shape in enumerate(shapes):
+        g = torch.from_numpy(values(shape, "full", 30 + i)).cuda().bfloat16()
+        desc = m.make_orthogonalize_desc(*shape)
+        ws = torch.empty(m.moe_orthogonalize_workspace_size(desc), dtype=torch.uint8, device="cuda")
+        alone, out = torch.empty_like(g), torch.zeros_like(g)
+        m.moe_orthogonalize(desc, g, alone, ws)
+        calls.append((desc, g, out, ws, alone))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, (desc, g, out, ws, _) in zip(streams, calls):
+            m.moe_orthogonalize(desc, g, out, ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, alone) for _, _, out, _, alone in calls)
+    ws = max((c[3] for c in calls), key=lambda t: t.numel())
+    graphs = []
+    for desc, g, out, _, _ in calls:
+        out.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            m.moe_orthogonalize(desc, g, out, ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, alone) for _, _, out, _, alone in calls)
+    assert m.moe_read_device_status() == 0

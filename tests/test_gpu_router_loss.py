@@ -1,11 +1,12 @@
 """The router's losses and their gradient on the GPU against the fp64 oracle.
 
-Bounds.  An exponential by the hardware's base-2 form is off by 2 + 1.173 |x|
-steps of 2^-23 (the documented error of __expf), x a logit less the row's
-largest; so p, a quotient of one and a sum of E of them, by twice that (R below)
+Bounds.  An exponential is the hardware's base-2 one (off by two steps of 2^-23) of
+x log2(e), which log2(e)'s own rounding and the product's move by less than a
+step for each |x|, x a logit less the row's largest: less than 2 + 1.173 |x| steps
+of 2^-23; so p, a quotient of one and a sum of E of them, by twice that (R below)
 and the sum's and the quotient's own log2(32) + 8 + 3 half steps.  Means over
-tokens add positive terms in chains of at most 32 tokens, 32 groups, 16 segments
-a warp, 32 warps and one quotient: 128 half steps.  logsumexp is off by the sum's
+tokens add positive terms in chains of at most 32 tokens, 32 groups of a block,
+segments by halves and one quotient: 128 half steps.  logsumexp is off by the sum's
 relative error and two half steps of its own magnitude; squares and their sum
 twice that and the chain's.  A gradient is a handful of products and sums of the
 terms whose magnitudes the oracle adds up, each with p's and logsumexp's error."""
