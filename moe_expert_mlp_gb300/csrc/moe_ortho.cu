@@ -14,10 +14,10 @@
 // state X is held in fp32 beside its operand: a X is exact, and the operand's
 // rounding E enters only through B E, which lies in X's own column space -- a
 // direction that X does not have stays empty, where a rounded state would fill it
-// and grow by a each step (3.44 by default: 485 over five).  In the last two steps B is held as B - s I with
-// s = tr(B)/m and X' = (a + s) X + (B - s I) X: near the end B's eigenvalues
-// crowd around s, so the rounded part is small.  Not earlier, where E would get
-// into the empty directions through s.
+// and grow by a each step (3.44 by default: 485 over five).  In the last two steps
+// B is held as B - s I with s = tr(B)/m and X' = (a + s) X + (B - s I) X: near the
+// end B's eigenvalues crowd around s, so the rounded part is small.  Not earlier,
+// where E would get into the empty directions through s.
 //
 // All products of all steps are one launch.  Its work is a list of 256 x 256
 // tiles: group of matrices by group, step by step, in a step A's tiles of every
@@ -30,17 +30,20 @@
 //
 // A pair works as the weight gradients of moe_gemm.cu do (2-SM MMA): warp 0 of
 // each CTA feeds a ring of stages by TMA, warp 1 of the lead issues the MMAs, eight
-// warps read the accumulators of the tile before.  A stage costs its hand-offs as
-// much as its bytes, so it takes 128 of the contraction (867 cycles per 64 of it
-// with 64 a stage, 740 with 128; the MMAs alone take 512).  What bounds it then is
-// the operands' way from L2 (32 KB an SM for every 512 cycles of MMAs, the
-// epilogue's accesses on the same path) and, on large lists, the power limit (clocks
-// fall from 2.07 to about 1.6 GHz).  The epilogue keeps to whole lines where it can:
-// the state lies in blocks of 32 rows by 16 columns in the order in which a warp's
-// lanes take it (rows 4 KB apart took four times the passes through L1).  Measured
-// and not kept: sixteen epilogue warps (5 % slower: the tile's stores, not latency,
-// set the epilogue's pace), operand loads one stage deeper, accumulators fetched a
-// chunk ahead (spills).
+// warps read the accumulators of the tile before.  A stage takes 128 of the
+// contraction (six stages of 64: the same on long lists, 4 % slower on short ones).
+// Long lists are bound by the power limit (16 matrices of 2880 x 2880: 1.35 PFLOP/s
+// in the first 6 ms, 1.19 held, at 1.5 of 2.07 GHz) and below it by the operands' way
+// from L2, 32 KB an SM for every 512 cycles of MMAs.  Short ones are bound by the
+// sequence of products: of a 256 x 512 matrix's 4.6 us a product 0.75 are the loads'
+// latency, 0.2 the MMAs, 0.3 their signal, 1 the epilogue, 0.5 until its stores are
+// out and 0.75 until another SM has seen their count.
+// The epilogue keeps to whole lines where it can: the state lies in blocks of 32
+// rows by 16 columns in the order in which a warp's lanes take it (rows 4 KB apart
+// took four times the passes through L1).  Measured and not kept: sixteen epilogue
+// warps (5 % slower: the tile's stores, not latency, set the epilogue's pace), a
+// second producer warp, accumulators fetched a chunk ahead (spills), smaller groups
+// (one tile a pair instead of two: 64 of 2048 x 1408 4.8 -> 5.6 ms) and larger ones.
 #include <math.h>
 
 #include "moe_ortho.cuh"
@@ -909,7 +912,7 @@ struct Layout {
 // Whether the first two steps are taken as one: where that saves products (see
 // term_of), and there are tiles enough that products and not their sequence take the
 // time.  (32 matrices of 7168 x 2048: 13.9 -> 12.4 ms; 64 of 2048 x 1024: 2.94 ->
-// 2.80 ms.)
+// 2.80 ms, both in the state of this step.)
 bool joins_steps(const moe_orthogonalize_desc_t* d) {
   const int m = d->rows < d->cols ? d->rows : d->cols, n = d->rows < d->cols ? d->cols : d->rows;
   return d->steps >= 5 && n >= 2 * m &&
@@ -963,7 +966,8 @@ cudaError_t launch_steps(OrthoArgs& g, int sms, cudaStream_t s) {
                                          static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
   // narrower tiles as long as they are one for each pair: a product of few tiles
-  // takes as long as one of them (8 matrices of 256 x 512: 149 -> 117 us)
+  // takes as long as one of them (8 matrices of 256 x 512, in the state of this step:
+  // 149 -> 117 us)
   const int most = sms / 2;
   auto sym = [&](int width) { return static_cast<long long>(g.batch) * sym_tiles(g.m, width); };
   auto full = [&](int width) {
