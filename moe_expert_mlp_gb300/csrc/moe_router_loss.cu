@@ -296,13 +296,15 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, LossSha
     if (threadIdx.x == 0 && cur + kSlots < ring.rounds) ring.load(cur + kSlots);
     ++cur;
   };
+  int from = t0;                 // also of offsets that descend: a round never comes back
   for (int s = first_sequence<THREADS>(a, t0); s < a.S; ++s) {
     int begin, end;
     sequence_span(a, s, &begin, &end);
     if (begin >= t1) break;
-    begin = max(begin, t0);
+    begin = max(begin, from);
     end = min(end, t1);
     if (begin >= end) continue;
+    from = end;
     if (threadIdx.x < kMaxExperts) sh.count[threadIdx.x] = 0;
     __syncthreads();
     float acc[N], z = 0.0f;

@@ -244,6 +244,25 @@ def test_device_status():
     assert m.moe_read_device_status() == 0
 
 
+@pytest.mark.parametrize("T,E", [(300, 64), (9000, 64), (9000, 61), (40000, 256)])
+def test_offsets_that_descend_are_only_reported(T, E):
+    """Over many rounds of the rows' ring: neither a wait that runs out nor a trace in
+    the next call."""
+    import moe_expert_mlp_gb300 as m
+    k = 2
+    logits, idx, _, _ = make(T, E, k)
+    good = np.array([0, T // 3, T // 2, T], np.int32)
+    want = forward(logits, idx, 3, 1.0, 0.0, None, good)[1]
+    m.moe_read_device_status()
+    for bad in ([0, T, T // 2, T], [T // 2, T // 4, T, 7], [0, 200, 50, T - 1], [T, 0, T, 0]):
+        desc, _, out = forward(logits, idx, 3, 1.0, 0.0, None, np.array(bad, np.int32))
+        assert m.moe_read_device_status() == 1                  # MOE_DEV_BAD_OFFSETS
+        backward(desc, logits, idx, None, np.array(bad, np.int32), out, None, None)
+        assert m.moe_read_device_status() == 0
+    again = forward(logits, idx, 3, 1.0, 0.0, None, good)[1]
+    assert all(np.array_equal(want[n], again[n]) for n in want)
+
+
 def test_graph_and_other_stream():
     """Captured on a stream of its own and replayed on new values."""
     import moe_expert_mlp_gb300 as m
