@@ -16,10 +16,13 @@
 // exchanges and of chains of small products, which mma.sync starts and ends in tens
 // of cycles; a tcgen05 tile would be mostly empty at m = 64 and has to come back
 // from TMEM each time (64 x 2048 with a momentum: 15 products of the general kernel
-// took 139 us, this 27).  A step of it is 7,300 cycles: the first product 2,150 and
-// the last 1,450 (the operands' way out of shared memory), 850 for the second, 2,700
-// for the two exchanges.
+// took 139 us, this 22).  A step of it is 6,200 cycles: 900 for the first product and
+// 1,000 for the last (the operands' way out of shared memory), 800 for the second,
+// 3,300 for the two exchanges.  With sides of 65 to 128 the exchanges are most of a
+// step, as shared memory of other CTAs gives and takes some 10 bytes a cycle.
 #include <math.h>
+
+#include <atomic>
 
 #include "moe_ortho.cuh"
 
@@ -28,7 +31,8 @@ namespace {
 
 constexpr int kSmallThreads = 512;
 constexpr int kSmallWarps = 16;
-constexpr int kMaxCluster = 8;                 // what every GPC holds
+constexpr int kPortable = 8;                   // CTAs of a cluster that every GPC holds
+constexpr int kMaxCluster = 16;
 constexpr int kUnits = 4;                      // of 8 elements that a thread loads at once
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -140,9 +144,9 @@ struct SmallShape {
   static constexpr int kP = MP * kPitchP * 4;
   static constexpr int kR = (MP + kMaxCluster) * kPitchP * 4;   // a share of rows from each CTA
   // P's rows go to the CTA that adds them up, or that CTA reads them: 17 KB by copies
-  // and a barrier that counts them in 3,000 cycles until A is there, read after a
-  // barrier of the cluster in 3,600; 66 KB are faster read (32 matrices of 128 x 512:
-  // sent 61 us, read 52)
+  // and a barrier that counts them in 2,700 cycles until A is there, read after a
+  // barrier of the cluster in 4,000; 66 KB are faster read (32 matrices of 128 x 512:
+  // sent 61 us, read 50)
   static constexpr bool kSend = MP == 64;
   static constexpr int kBAt = kX + kA;
   static constexpr int kPAt = kBAt + kA;
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
   if (threadIdx.x < ctas) st_cluster_f64(mapa_shared(smem_u32(&s_norm[rank]), threadIdx.x), sum);
   cluster_sync();
   if (warp == 0) {
-    sum = lane < ctas ? s_norm[lane] : 0.0;
+    sum = lane < static_cast<int>(ctas) ? s_norm[lane] : 0.0;
 #pragma unroll
     for (int o = kMaxCluster / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) {
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
   const int ar0 = warp / 4 * (16 * MB), ac0 = warp % 4 * (16 * NB2);
   const int share = (MP + ctas - 1) / ctas;     // rows of A that a CTA adds up
   const int first = static_cast<int>(rank) * share;
-  const int rows = min(share, MP - first);
+  const int rows = max(0, min(share, MP - first));
   const uint32_t p_at = smem_u32(P), p_bar_at = smem_u32(&p_bar), a_bar_at = smem_u32(&a_bar);
   const float* received = reinterpret_cast<const float*>(smem + S::kRAt);
   for (int step = 0; step < g.steps; ++step) {
@@ -371,8 +375,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
       // rows to the CTA that adds them up
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
-      if (threadIdx.x < ctas) {
-        const int r = threadIdx.x * share;
+      const int r = threadIdx.x * share;
+      if (threadIdx.x < ctas && r < MP) {
         send(mapa_shared(smem_u32(received + rank * share * S::kPitchP), threadIdx.x),
              p_at + r * S::kPitchP * 4, min(share, MP - r) * S::kPitchP * 4,
              mapa_shared(p_bar_at, threadIdx.x));
@@ -518,59 +522,93 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
 }
 
 template <int MP, int NB>
+cudaLaunchConfig_t config_of(int batch, int ctas, cudaStream_t s, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = ctas;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch) * ctas);
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = SmallShape<MP, NB>::kBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int MP, int NB>
+cudaError_t prepare_shape() {
+  cudaError_t err = cudaFuncSetAttribute(k_ortho_small<MP, NB>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SmallShape<MP, NB>::kBytes);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(k_ortho_small<MP, NB>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                               1);
+  return err;
+}
+
+// Whether this GPU holds `batch` clusters of that many CTAs at once.  (GPCs differ in
+// their SMs from one GPU to the next, so it is asked, once a device.)
+template <int MP, int NB>
+bool holds(int batch, int ctas) {
+  if (ctas <= kPortable) return true;
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster - kPortable];   // clusters, and one
+  int dev;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::atomic<int>* have = dev < kDevices ? &known[dev][ctas - kPortable - 1] : nullptr;
+  int clusters = have != nullptr ? have->load(std::memory_order_relaxed) - 1 : -1;
+  if (clusters < 0) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config_of<MP, NB>(batch, ctas, nullptr, &attr);
+    if (prepare_shape<MP, NB>() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, k_ortho_small<MP, NB>, &cfg) != cudaSuccess) {
+      cudaGetLastError();        // the question's: fewer CTAs do
+      clusters = 0;
+    }
+    if (have != nullptr) have->store(clusters + 1, std::memory_order_relaxed);
+  }
+  return clusters >= batch;
+}
+
+template <int MP, int NB>
 cudaError_t launch_shape(const SmallOrthoArgs& g, int ctas, cudaStream_t s) {
-  using S = SmallShape<MP, NB>;
-  cudaError_t err = cudaFuncSetAttribute(
-      k_ortho_small<MP, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  const cudaError_t err = prepare_shape<MP, NB>();
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(g.in.batch) * ctas);
-  cfg.blockDim = dim3(kSmallThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = config_of<MP, NB>(g.in.batch, ctas, s, &attr);
   return cudaLaunchKernelEx(&cfg, k_ortho_small<MP, NB>, g);
 }
 
-// The fewest columns a CTA that leave a matrix in kMaxCluster CTAs, and all
-// matrices' CTAs on the GPU at once where that is to be had: more CTAs have
-// shorter products, fewer have less to exchange.
-template <int MP>
+// The fewest columns a CTA (8 NB for each of its warps along the columns) that leave a
+// matrix in one cluster and all clusters on the GPU at once: more CTAs have shorter
+// products, fewer have less to exchange.  More than eight where they keep 64 columns
+// (16 instead of 8: 64 x 2048 27 -> 22 us, 128 x 2048 72 -> 59, 128 x 1024 53 -> 52;
+// with 32 columns each 128 x 512 46 -> 50).
+template <int MP, int NB>
 cudaError_t launch_rows(const SmallOrthoArgs& g, int n, int sms, cudaStream_t s) {
-  constexpr int unit = SmallShape<MP, 1>::kCols;
-  int nb = 1;
-  while (nb < 8) {
-    const int ctas = (n + nb * unit - 1) / (nb * unit);
-    if (ctas <= kMaxCluster && static_cast<long long>(ctas) * g.in.batch <= sms) break;
-    if (ctas == 1) break;
-    nb *= 2;
+  const int ctas = (n + SmallShape<MP, NB>::kCols - 1) / SmallShape<MP, NB>::kCols;
+  if constexpr (NB < 8) {
+    const int most = SmallShape<MP, NB>::kCols >= 64 ? kMaxCluster : kPortable;
+    if (ctas > 1 && (ctas > most || static_cast<long long>(ctas) * g.in.batch > sms ||
+                     !holds<MP, NB>(g.in.batch, ctas)))
+      return launch_rows<MP, 2 * NB>(g, n, sms, s);
   }
-  const int ctas = (n + nb * unit - 1) / (nb * unit);
-  switch (nb) {
-    case 1: return launch_shape<MP, 1>(g, ctas, s);
-    case 2: return launch_shape<MP, 2>(g, ctas, s);
-    case 4: return launch_shape<MP, 4>(g, ctas, s);
-    default: return launch_shape<MP, 8>(g, ctas, s);
-  }
+  return launch_shape<MP, NB>(g, ctas, s);
 }
 
 }  // namespace
 
 bool small_ortho(int rows, int cols) {
   const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  if (m <= 64) return n <= kMaxCluster * SmallShape<64, 8>::kCols;
-  return m <= 128 && n <= kMaxCluster * SmallShape<128, 8>::kCols;
+  if (m <= 64) return n <= kPortable * SmallShape<64, 8>::kCols;
+  return m <= 128 && n <= kPortable * SmallShape<128, 8>::kCols;
 }
 
 cudaError_t launch_small_ortho(const SmallOrthoArgs& g, int sms, cudaStream_t s) {
   const int m = g.in.rows < g.in.cols ? g.in.rows : g.in.cols;
   const int n = g.in.rows < g.in.cols ? g.in.cols : g.in.rows;
-  return m <= 64 ? launch_rows<64>(g, n, sms, s) : launch_rows<128>(g, n, sms, s);
+  return m <= 64 ? launch_rows<64, 1>(g, n, sms, s) : launch_rows<128, 1>(g, n, sms, s);
 }
 
 }  // namespace moe

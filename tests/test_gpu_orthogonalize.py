@@ -320,3 +320,12 @@ def test_two_calls_at_once_and_graphs_that_share_a_workspace():
     torch.cuda.synchronize()
     assert all(torch.equal(out, alone) for _, _, out, _, alone in calls)
     assert m.moe_read_device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 600), (2, 40, 833), (1, 64, 1000), (2, 128, 900), (1, 70, 1900),
+                                   (1, 128, 2048), (3, 17, 4096)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_small_matrices_of_up_to_sixteen_ctas(shape, tall):
+    """Among them clusters in which the last CTAs have no rows of A to add up."""
+    b, m, n = shape
+    check(*run(values((b, n, m) if tall else shape, "full", 23)))
