@@ -99,7 +99,7 @@ struct OrthoArgs {
   int tall;                    // more rows than columns: A = X^T X, X' = X B
   float* part;                 // [batch][tiles of A][2 CTAs][8 warps]: sums of A_ii, A_ij^2
   float* shift;                // [batch] s
-  unsigned int* done;          // [batch][2] finished warps' shares of small and of X's tiles
+  unsigned int* done;          // finished halves of small and of X's tiles (counter_at)
   float a, b, c;
   float x_scale, scale;
   __nv_bfloat16* out;
@@ -255,18 +255,22 @@ __device__ __forceinline__ Shape shape_of(const OrthoArgs& g, const Work& w) {
   return s;
 }
 
+// Where matrix z has its two counts, of small and of X's tiles: a line each, as
+// every SM asks for them.
+__host__ __device__ inline int counter_at(int z, int which) { return 64 * z + 32 * which; }
+
 // Waits until the tiles that w reads are finished; false when that takes too long
 // or the CTA has given up.
 __device__ __forceinline__ bool wait_inputs(const OrthoArgs& g, const Plan& p, const Work& w,
                                             volatile int* abort_flag) {
   if (w.op == kGram && w.step == 0) return true;
-  const unsigned int share = 2 * kEpiWarps;
   const bool gram = w.op == kGram;
-  const unsigned int* ctr = g.done + 2 * w.z + (gram ? 1 : 0);
+  const unsigned int* ctr = g.done + counter_at(w.z, gram ? 1 : 0);
   // a matrix's small products follow one another, so their tiles' count tells which
   // of them are finished
   const int before = terms_before(g, w.step) + (w.op == kPoly ? w.q : terms_in(g, w.step));
-  const unsigned int target = share * (gram ? w.step * p.full : before * p.sym);
+  // (each of a tile's two CTAs counts)
+  const unsigned int target = 2 * (gram ? w.step * p.full : before * p.sym);
   unsigned int v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
   if (v >= target) return true;
@@ -281,6 +285,21 @@ __device__ __forceinline__ bool wait_inputs(const OrthoArgs& g, const Plan& p, c
       return false;
     }
   }
+}
+
+// Whether any thread of the epilogue's warps says so; all of them wait here.
+__device__ __forceinline__ bool any_of_epilogue(bool p) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(p ? 1u : 0u), "n"(32 * kEpiWarps)
+      : "memory");
+  return any != 0;
 }
 
 // Where the state has the first 8 of row r's 16 elements from column c (a
@@ -686,6 +705,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __half* mirror_buf = reinterpret_cast<__half*>(smem + kStages * kStageBytes) +
                          ewarp * (kMirrorBytes / 2);
     int it = 0;
+    bool failed = false;
     for (int t = pair; t < p.total; t += npairs, ++it) {
       const Work w = work_at(g, p, t);
       const int width = w.op >= kUpdate ? g.full_w : g.sym_w;
@@ -696,9 +716,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kTile + hc;
       // what the epilogue reads beside the accumulator is there
-      int ok = 1;
-      if (lane == 0 && w.op != kGram) ok = wait_inputs(g, p, w, abort_flag);
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      // (one thread asks, as one tells below: with each warp at it the counts' own
+      // traffic cost 12 % of 3 matrices of 1001 x 1441)
+      if (w.op != kGram) {
+        if (ewarp == 0 && lane == 0 && !failed) failed = !wait_inputs(g, p, w, abort_flag);
+        if (any_of_epilogue(failed)) break;
+      }
       auto ready = [&]() {
         int full = 1;
         if (lane == 0) full = mbar_wait(&tfull_bar[acc], acc_par, g.status, abort_flag);
@@ -711,24 +734,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
       };
-      bool done;
-      if (w.op == kGram)
-        done = epilogue<kGram>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
-                               read);
-      else if (w.op == kPoly)
-        done = epilogue<kPoly>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
-                               read);
-      else if (w.op == kUpdate)
-        done = epilogue<kUpdate>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
-                               read);
-      else
-        done = epilogue<kLast>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf, ready,
-                               read);
-      if (!done) break;
+      if (!failed) {
+        bool done;
+        if (w.op == kGram)
+          done = epilogue<kGram>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf,
+                                 ready, read);
+        else if (w.op == kPoly)
+          done = epilogue<kPoly>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf,
+                                 ready, read);
+        else if (w.op == kUpdate)
+          done = epilogue<kUpdate>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf,
+                                   ready, read);
+        else
+          done = epilogue<kLast>(g, p, w, width, tbase, row0, col0, lane, ewarp, rank, mirror_buf,
+                                 ready, read);
+        failed = !done;
+      }
       if (w.op != kLast) {                   // (the readers fence before their TMA)
-        __syncwarp();
-        if (lane == 0)
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.done + 2 * w.z + (w.op == kUpdate ? 1 : 0))
+        if (any_of_epilogue(failed)) break;
+        if (ewarp == 0 && lane == 0)
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(
+                           g.done + counter_at(w.z, w.op == kUpdate ? 1 : 0))
                        : "memory");
       }
     }
@@ -754,7 +780,7 @@ __global__ void __launch_bounds__(256, 3) k_ortho_norm(const PrepArgs p) {
   __shared__ double s_sum[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int z = blockIdx.y;
-  if (blockIdx.x == 0 && threadIdx.x < 2) p.done[2 * z + threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.done[counter_at(z, threadIdx.x)] = 0;
   const unsigned units = (p.cols + 7) / 8;
   const unsigned count = p.rows * units;
   const unsigned stride = gridDim.x * 256;
@@ -947,7 +973,7 @@ Layout layout_of(const moe_orthogonalize_desc_t* d) {
   w.part = take(n * w.parts * 8);
   w.norm = take(n * kNormParts * 8);
   w.shift = take(n * 4);
-  w.done = take(n * 8);
+  w.done = take(n * 256);
   w.bytes = at > 0 ? at : 256;
   return w;
 }

@@ -32,7 +32,7 @@ struct PrepArgs {
   __half* x_hi;
   float* state;
   long long ld_x, plane_x, plane_s;
-  unsigned int* done;          // [batch][3], set to zero
+  unsigned int* done;          // k_ortho_steps' counts, set to zero
 };
 
 // 8 floats of a row from c on, n of them where they are not aligned.
