@@ -94,9 +94,9 @@ class MoEResidualBlock:
     def forward(self, res, logits, bias=None, gate=None, stream=None, timer=None, mask=None,
                 seq_offsets=None):
         """res [T,d] (kept for the backward) -> res_out; logits, bias, mask and
-        seq_offsets: the router's, as MoEExpertMLP.forward; gate fp32 [T] with a token gate.  A
-        router that reads x calls forward_norm first; the norm runs again here,
-        with the same result."""
+        seq_offsets: the router's, as MoEExpertMLP.forward; gate fp32 [T] with a
+        token gate.  A router that reads x calls forward_norm first; the norm runs
+        again here, with the same result."""
         if self.token_gate and gate is None:
             raise ValueError("a token gate needs its values")
         layer, t = self.layer, self.layer._t

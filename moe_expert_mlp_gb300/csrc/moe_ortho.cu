@@ -35,9 +35,9 @@
 // Long lists are bound by the power limit (16 matrices of 2880 x 2880: 1.35 PFLOP/s
 // in the first 6 ms, 1.19 held, at 1.5 of 2.07 GHz) and below it by the operands' way
 // from L2, 32 KB an SM for every 512 cycles of MMAs.  Short ones are bound by the
-// sequence of products: of a 256 x 512 matrix's 4.6 us a product 0.75 are the loads'
+// sequence of products: of a 256 x 512 matrix's 4.4 us a product 0.75 are the loads'
 // latency, 0.2 the MMAs, 0.3 their signal, 1 the epilogue, 0.5 until its stores are
-// out and 0.75 until another SM has seen their count.
+// out and 0.7 until another SM has seen their count.
 // The epilogue keeps to whole lines where it can: the state lies in blocks of 32
 // rows by 16 columns in the order in which a warp's lanes take it (rows 4 KB apart
 // took four times the passes through L1).  Measured and not kept: sixteen epilogue
