@@ -98,12 +98,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // the reciprocal of their sum, and with DOT dot is <f, p>.  Returns logsumexp.  In
 // powers of two, exp(x) = 2^(x log2(e) - c) with c = top log2(e) as it is rounded:
 // the same for the whole row, so that it cancels in p and is added back in
-// logsumexp.  A row without a logit above -inf has p = 0 and gives 0; maxima pass
-// over NaN, which then reaches the sum.
+// logsumexp.  That holds while c is rounded by little: a top beyond kFar is taken off
+// the logits first (from 2^31 on c's rounding alone would make sums 0 or inf).  A row
+// without a logit above -inf has p = 0 and gives 0; maxima pass over NaN, which then
+// reaches the sum.
 template <int N, bool DOT>
 __device__ __forceinline__ float row_softmax(float (&x)[N], float& inv, const float* f, float& dot,
                                              uint32_t mask) {
   constexpr float kLog2E = 1.44269504088896f, kLn2 = 0.693147180559945f;
+  constexpr float kFar = 16777216.0f;      // up to it c is off by one at most
   constexpr int kChains = N < 4 ? 1 : 4;   // of maxima and sums, side by side
   float part[kChains], part_dot[kChains];
 #pragma unroll
@@ -116,7 +119,7 @@ __device__ __forceinline__ float row_softmax(float (&x)[N], float& inv, const fl
   top = group_max(top, mask);
   if (top == -INFINITY) top = 0.0f;
   float base = 0.0f;
-  if (!(fabsf(top) < 1e38f)) {     // c would leave fp32's range
+  if (!(fabsf(top) < kFar)) {      // (or NaN)
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] -= top;
     base = top;
