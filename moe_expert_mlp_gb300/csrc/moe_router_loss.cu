@@ -28,6 +28,9 @@ constexpr int kLossThreads = 256;
 constexpr int kAloneThreads = 1024;    // of a block that takes all tokens, up to 64 experts
 constexpr int kSlots = 3;              // of a block's ring: rounds in hand and on their way
 constexpr int kMostTokens = 1024;      // of a chunk: a group adds 32 up one by one
+// Squares are added up of values times this and their mean is multiplied back, so
+// that a sum over up to 2^28 tokens does not leave fp32's range before its mean does.
+constexpr float kSquareScale = 1.0f / 16384;
 
 struct LossArgs {
   const float* logits;
@@ -346,7 +349,8 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, LossSha
         const float lse = row_softmax<N, false>(x, inv, nullptr, unused, mask);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
-        z = fmaf(lse, lse, z);
+        const float q = lse * kSquareScale;
+        z = fmaf(q, q, z);
         ++n;
         for (int i = lane; i < a.k; i += kLanes) {
           const int e = i < kLanes ? mine : __ldg(a.topk_idx + static_cast<long long>(t) * a.k + i);
@@ -401,7 +405,7 @@ __device__ __forceinline__ void write_losses(const LossArgs& a, float terms, flo
   const float total = static_cast<float>(n > 0 ? n : 1);
   // N_s f P = E / k * count * P
   const float balance = terms * (static_cast<float>(a.E) / static_cast<float>(a.k)) / total;
-  const float z = squares / total;
+  const float z = squares / total * (1.0f / (kSquareScale * kSquareScale));
   a.loss[0] = fmaf(a.balance, balance, a.z * z);
   a.loss[1] = balance;
   a.loss[2] = z;

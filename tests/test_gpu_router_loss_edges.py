@@ -1,4 +1,5 @@
-"""Router's losses at the edges of what they take: rows of logits far from zero.
+"""Router's losses at the edges of what they take: rows of logits far from zero,
+squares whose sum is out of range.
 
 Bounds: those of test_gpu_router_loss.py."""
 import numpy as np
@@ -26,7 +27,7 @@ def far_rows(T, E, k, at):
     return logits, idx
 
 
-@pytest.mark.parametrize("at", [2.0 ** 20, 3e7, -3e7, 1e8, -1e9, 1e10, -1e10, 3e15])
+@pytest.mark.parametrize("at", [2.0 ** 20, 3e7, -3e7, 1e8, -1e9, 1e10, -1e10, 3e15, -1e18])
 @pytest.mark.parametrize("T,E,k", [(200, 64, 4), (200, 61, 4), (3000, 64, 4), (900, 256, 8)])
 def test_rows_far_from_zero(T, E, k, at):
     logits, idx = far_rows(T, E, k, at)
@@ -52,3 +53,12 @@ def test_rows_whose_squares_leave_the_range(T, E, k, at):
     assert got["loss"][1] == want["loss"][1]
     d = backward(desc, logits, idx, None, None, out)
     check_backward(logits, k, 1, 1.0, 0.0, None, None, got, d, 1.0, None)
+
+
+@pytest.mark.parametrize("T", [400, 5000, 200000])
+def test_mean_of_squares_whose_sum_leaves_the_range(T):
+    logits, idx, _, _ = make(T, 8, 2)
+    logits[:] = np.where(np.arange(8) == 3, 1.5e19, -np.inf)[None].astype(np.float32)
+    for S, offsets in ((1, None), (3, np.array([0, T // 3, T // 2, T], np.int32))):
+        _, got, _ = forward(logits, idx, S, 0.5, 0.25, None, offsets)
+        check_forward(logits, idx, S, 0.5, 0.25, None, offsets, got)
