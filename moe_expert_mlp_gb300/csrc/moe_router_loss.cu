@@ -806,13 +806,17 @@ void fill(LossArgs& a, const moe_router_loss_desc_t* d) {
   a.z = d->z_coef;
 }
 
-template <typename K>
-cudaError_t launch_rows(K kernel, const LossArgs& a, int blocks, int threads, bool vec,
+// K's rows in shared memory: `slots` rounds of a row of at most N kLanes experts for
+// each group.  The limit is the kernel's, not the call's: it is set for the most
+// experts that K takes, so that calls at once do not lower it under one another.
+template <int N, typename K>
+cudaError_t launch_rows(K kernel, const LossArgs& a, int blocks, int threads, int slots,
                         cudaStream_t s) {
-  const size_t bytes = static_cast<size_t>(threads / kLanes) * a.E * 4 * (vec ? kSlots : 1);
+  const int column = threads / kLanes * slots * 4, bytes = column * a.E;   // of an expert, of all
   if (bytes > 8 * 1024) {        // with the static part possibly over 48 KB
-    const cudaError_t err = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    const int most = column * (N * kLanes < kMaxExperts ? N * kLanes : kMaxExperts);
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (err != cudaSuccess) return err;
   }
   kernel<<<blocks, threads, bytes, s>>>(a);
@@ -825,16 +829,13 @@ struct RunChunks {
   cudaStream_t s;
   template <int N, int VEC>
   cudaError_t operator()() const {
+    constexpr int kSlotsOf = VEC == 4 ? kSlots : 1;
     if (alone) {
-      if constexpr (N <= 8)
-        return launch_rows(k_loss_chunks<N, VEC, true, kAloneThreads>, a, 1, kAloneThreads,
-                           VEC == 4, s);
-      else
-        return launch_rows(k_loss_chunks<N, VEC, true, kLossThreads>, a, 1, kLossThreads, VEC == 4,
-                           s);
+      constexpr int kThreads = N <= 8 ? kAloneThreads : kLossThreads;
+      return launch_rows<N>(k_loss_chunks<N, VEC, true, kThreads>, a, 1, kThreads, kSlotsOf, s);
     }
-    return launch_rows(k_loss_chunks<N, VEC, false, kLossThreads>, a, a.chunks, kLossThreads,
-                       VEC == 4, s);
+    return launch_rows<N>(k_loss_chunks<N, VEC, false, kLossThreads>, a, a.chunks, kLossThreads,
+                          kSlotsOf, s);
   }
 };
 
@@ -843,7 +844,7 @@ struct RunBwd {
   cudaStream_t s;
   template <int N, int VEC>
   cudaError_t operator()() const {
-    return launch_rows(k_loss_bwd<N, VEC>, a, a.chunks, kLossThreads, VEC == 4, s);
+    return launch_rows<N>(k_loss_bwd<N, VEC>, a, a.chunks, kLossThreads, VEC == 4 ? kSlots : 1, s);
   }
 };
 

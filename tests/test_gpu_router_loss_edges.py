@@ -1,7 +1,9 @@
 """Router's losses at the edges of what they take: rows of logits far from zero,
-squares whose sum is out of range.
+squares whose sum is out of range, calls from two host threads at once.
 
 Bounds: those of test_gpu_router_loss.py."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -62,3 +64,53 @@ def test_mean_of_squares_whose_sum_leaves_the_range(T):
     for S, offsets in ((1, None), (3, np.array([0, T // 3, T // 2, T], np.int32))):
         _, got, _ = forward(logits, idx, S, 0.5, 0.25, None, offsets)
         check_forward(logits, idx, S, 0.5, 0.25, None, offsets, got)
+
+
+def test_two_host_threads_with_layers_of_different_experts():
+    """Calls of 132 and of 256 experts run in one kernel; each thread has its own
+    stream, workspace and results."""
+    import moe_expert_mlp_gb300 as m
+    calls = []
+    for T, E, k in ((600, 132, 4), (500, 256, 8)):
+        logits, idx, _, _ = make(T, E, k, seed=E)
+        desc = m.make_router_loss_desc(T, E, k, 1, 1.0, 1e-3)
+        t = dict(logits=torch.from_numpy(logits).cuda(), idx=torch.from_numpy(idx).cuda(),
+                 counts=torch.zeros((1, E), dtype=torch.int32, device="cuda"),
+                 tokens=torch.zeros(2, dtype=torch.int32, device="cuda"),
+                 probs=torch.zeros((1, E), device="cuda"), loss=torch.zeros(3, device="cuda"),
+                 dlogits=torch.zeros((T, E), device="cuda"),
+                 ws=torch.empty(m.moe_router_loss_workspace_size(desc), dtype=torch.uint8,
+                                device="cuda"))
+        calls.append((desc, t, torch.cuda.Stream()))
+
+    def step(desc, t, stream):
+        m.moe_router_loss_fwd(desc, t["logits"], t["idx"], None, None, t["counts"], t["tokens"],
+                              t["probs"], t["loss"], t["ws"], stream)
+        m.moe_router_loss_bwd(desc, t["logits"], None, None, t["counts"], t["tokens"], None, None,
+                              t["dlogits"], stream)
+
+    results = ("counts", "tokens", "probs", "loss", "dlogits")
+    torch.cuda.synchronize()
+    want = []
+    for desc, t, stream in calls:
+        step(desc, t, stream)
+        torch.cuda.synchronize()
+        want.append({n: t[n].clone() for n in results})
+    failures = []
+
+    def work(call):
+        try:
+            for _ in range(4000):
+                step(*call)
+        except Exception as e:          # reported by the test's own thread
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not failures
+    for (_, t, _), w in zip(calls, want):
+        assert all(torch.equal(t[n], w[n]) for n in results)
