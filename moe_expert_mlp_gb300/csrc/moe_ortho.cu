@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(256, 3) k_ortho_norm(const PrepArgs p) {
 // by 16 columns, a row a lane: whole sectors of the rows, whole lines of the state.
 template <bool F32>
 __global__ void __launch_bounds__(256, 4) k_ortho_start(const PrepArgs p) {
-  __shared__ float s_mul;
+  __shared__ float2 s_mul;
   const int z = blockIdx.y;
   const int lane = threadIdx.x & 31;
   wait_for_previous();
@@ -837,10 +837,10 @@ __global__ void __launch_bounds__(256, 4) k_ortho_start(const PrepArgs p) {
       sum += p.part[static_cast<long long>(z) * kNormParts + i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) s_mul = static_cast<float>(p.x_scale / (sqrt(sum) + p.eps));
+    if (lane == 0) s_mul = norm_factors(sum, p.x_scale, p.eps);
   }
   __syncthreads();
-  const float mul = s_mul;
+  const float2 mul = s_mul;
   const int col_blocks = (p.cols + 15) / 16;
   const int blocks = (p.rows + 31) / 32 * col_blocks;
   const bool reads_grad = p.mom == nullptr || p.nesterov;
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(256, 4) k_ortho_start(const PrepArgs p) {
       for (int k = 0; k < 8; ++k) u[k] = reads_grad ? g[q][k] : 0.0f;
       if (p.mom != nullptr) direction(p, u, m[q]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] *= mul;
+      for (int k = 0; k < 8; ++k) u[k] = u[k] * mul.x * mul.y;
       *reinterpret_cast<uint4*>(p.x_hi + z * p.plane_x + r * p.ld_x + c) =
           make_uint4(pack_half2(u[0], u[1]), pack_half2(u[2], u[3]), pack_half2(u[4], u[5]),
                      pack_half2(u[6], u[7]));

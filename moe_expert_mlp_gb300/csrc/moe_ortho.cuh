@@ -128,6 +128,14 @@ __device__ __forceinline__ double squares_of(const float (&u)[N][8]) {
   return sum;
 }
 
+// What U is multiplied by, x_scale / (|U| + eps), as two factors: with a norm and an
+// eps near fp32's smallest the one number would be inf, and a zero matrix NaN.
+__device__ __forceinline__ float2 norm_factors(double squares, float x_scale, float eps) {
+  const double f = x_scale / (sqrt(squares) + eps);     // at most 2^14 / 2^-149
+  return f > 1e38 ? make_float2(static_cast<float>(f * 0x1p-64), 0x1p64f)
+                  : make_float2(static_cast<float>(f), 1.0f);
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
   __shared__ double s_norm[kMaxCluster];
   __shared__ double s_part[kSmallThreads];
   __shared__ float s_warp[kSmallWarps];
-  __shared__ float s_mul;
+  __shared__ float2 s_mul;
   __shared__ float s_diag[MP];
   __shared__ volatile int s_abort;
   __half* X = reinterpret_cast<__half*>(smem);
@@ -305,12 +305,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
     if (lane == 0) {
       const float f = static_cast<float>(sum);
       s_mul = f > 1e-28f && f < 1e36f
-                  ? static_cast<float>(p.x_scale) / (sqrtf(f) + static_cast<float>(p.eps))
-                  : static_cast<float>(p.x_scale / (sqrt(sum) + p.eps));
+                  ? make_float2(p.x_scale / (sqrtf(f) + p.eps), 1.0f)
+                  : norm_factors(sum, p.x_scale, p.eps);
     }
   }
   __syncthreads();
-  const float mul = s_mul;
+  const float2 mul = s_mul;
 
   // ---- X in the accumulators: 32 rows, 8 NB columns a warp
   const int xr0 = warp / S::kColWarps * 32, xc0 = warp % S::kColWarps * (8 * NB);
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_ortho_small(const __grid_c
           v = make_float2(U[c * S::kPitchT + r], U[(c + 1) * S::kPitchT + r]);
         else
           v = *reinterpret_cast<const float2*>(U + r * S::kPitchU + c);
-        x[i][j][2 * h] = v.x * mul;
-        x[i][j][2 * h + 1] = v.y * mul;
+        x[i][j][2 * h] = v.x * mul.x * mul.y;
+        x[i][j][2 * h + 1] = v.y * mul.x * mul.y;
       }
   cluster_arrive();                          // U may be written over, by other CTAs too
   __syncthreads();
