@@ -952,7 +952,7 @@ moe_status_t moe_clip_grads(const moe_grad_t* grads, int32_t n, const float* nor
  *   f[s,e] = E c[s,e] / (k N_s)      P[s,e] = 1/N_s sum_t p[t,e]
  *   balance = sum_s N_s/N sum_e f[s,e] P[s,e]          (1 where all is even)
  *   z       = 1/N sum_t logsumexp(logits[t])^2
- *   loss    = balance_coef*balance + z_coef*z
+ *   loss    = balance_coef*balance + z_coef*z      (a coefficient of 0 leaves its out)
  * and, f held fixed as it is not differentiable,
  *   dlogits[t,e] = dloss/N * p[t,e] * (balance_coef*(f[s,e] - sum_j f[s,j] p[t,j])
  *                                      + 2*z_coef*logsumexp(logits[t])).

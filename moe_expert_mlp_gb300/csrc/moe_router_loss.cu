@@ -406,7 +406,8 @@ __device__ __forceinline__ void write_losses(const LossArgs& a, float terms, flo
   // N_s f P = E / k * count * P
   const float balance = terms * (static_cast<float>(a.E) / static_cast<float>(a.k)) / total;
   const float z = squares / total * (1.0f / (kSquareScale * kSquareScale));
-  a.loss[0] = fmaf(a.balance, balance, a.z * z);
+  // (0 times a loss out of range is not 0)
+  a.loss[0] = fmaf(a.balance, a.balance != 0.0f ? balance : 0.0f, a.z != 0.0f ? a.z * z : 0.0f);
   a.loss[1] = balance;
   a.loss[2] = z;
   a.tokens[a.S] = n;

@@ -1,5 +1,6 @@
 """Router's losses at the edges of what they take: rows of logits far from zero,
-squares whose sum is out of range, calls from two host threads at once.
+squares whose sum is out of range, losses without a coefficient, calls from two host
+threads at once.
 
 Bounds: those of test_gpu_router_loss.py."""
 import threading
@@ -114,3 +115,22 @@ def test_two_host_threads_with_layers_of_different_experts():
     assert not failures
     for (_, t, _), w in zip(calls, want):
         assert all(torch.equal(t[n], w[n]) for n in results)
+
+
+@pytest.mark.parametrize("T", [60, 700])
+def test_a_loss_without_a_coefficient_is_left_out(T):
+    """A row masked with the most negative finite number: its square leaves fp32's range,
+    which is no part of a loss that does not ask for it."""
+    E, k = 40, 4
+    logits, idx, _, _ = make(T, E, k)
+    logits[9] = np.finfo(np.float32).min
+    _, got, _ = forward(logits, idx, 1, 0.5, 0.0)
+    assert np.isposinf(got["loss"][2]) and np.isfinite(got["loss"][1])
+    assert got["loss"][0] == np.float32(0.5) * got["loss"][1]
+    _, got, _ = forward(logits, idx, 1, 0.0, 0.0)
+    assert got["loss"][0] == 0
+    _, got, _ = forward(logits, idx, 1, 0.0, 1e-3)
+    assert np.isposinf(got["loss"][0])
+    logits[9, 3] = np.nan
+    for coefficients in ((0.5, 0.0), (0.0, 1e-3), (0.5, 1e-3)):
+        assert np.isnan(forward(logits, idx, 1, *coefficients)[1]["loss"]).all()
