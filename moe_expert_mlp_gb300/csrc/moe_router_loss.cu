@@ -150,23 +150,13 @@ __device__ __forceinline__ float row_softmax(float (&x)[N], float& inv, const fl
   return sum == 0.0f ? 0.0f : fmaf(c + log2_approx(sum), kLn2, base);
 }
 
-// A lane's share of a row of floats; `fill` past the experts.
-template <int N, int VEC>
-__device__ __forceinline__ void load_row(const float* row, int E, int lane, float fill,
-                                         float (&x)[N]) {
+// A lane's share of a row in global memory, by single floats.
+template <int N>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&x)[N]) {
 #pragma unroll
-  for (int j = 0; j < N / VEC; ++j) {
-    const int e = expert_of<VEC>(lane, j);
-    if constexpr (VEC == 4) {
-      const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
-                             : make_float4(fill, fill, fill, fill);
-      x[4 * j] = v.x;
-      x[4 * j + 1] = v.y;
-      x[4 * j + 2] = v.z;
-      x[4 * j + 3] = v.w;
-    } else {
-      x[j] = e < E ? __ldg(row + e) : fill;
-    }
+  for (int j = 0; j < N; ++j) {
+    const int e = expert_of<1>(lane, j);
+    x[j] = e < E ? __ldg(row + e) : -INFINITY;
   }
 }
 
@@ -210,22 +200,18 @@ struct RowRing {
   }
 };
 
-// A lane's share of a row in shared memory.
-template <int N, int VEC>
+// A lane's share of a row in shared memory, four floats at a time.
+template <int N>
 __device__ __forceinline__ void load_shared_row(const float* row, int E, int lane, float (&x)[N]) {
 #pragma unroll
-  for (int j = 0; j < N / VEC; ++j) {
-    const int e = expert_of<VEC>(lane, j);
-    if constexpr (VEC == 4) {
-      const float4 v = e < E ? *reinterpret_cast<const float4*>(row + e)
-                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      x[4 * j] = v.x;
-      x[4 * j + 1] = v.y;
-      x[4 * j + 2] = v.z;
-      x[4 * j + 3] = v.w;
-    } else {
-      x[j] = e < E ? row[e] : -INFINITY;
-    }
+  for (int j = 0; j < N / 4; ++j) {
+    const int e = expert_of<4>(lane, j);
+    const float4 v = e < E ? *reinterpret_cast<const float4*>(row + e)
+                           : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    x[4 * j] = v.x;
+    x[4 * j + 1] = v.y;
+    x[4 * j + 2] = v.z;
+    x[4 * j + 3] = v.w;
   }
 }
 
@@ -343,9 +329,9 @@ __device__ __forceinline__ void chunk_segments(const LossArgs& a, int c, LossSha
       if (live) {
         float x[N], inv, unused;
         if constexpr (VEC == 4)
-          load_shared_row<N, VEC>(ring.round(r) + group * a.E, a.E, lane, x);
+          load_shared_row(ring.round(r) + group * a.E, a.E, lane, x);
         else
-          load_row<N, VEC>(a.logits + static_cast<long long>(t) * a.E, a.E, lane, -INFINITY, x);
+          load_row(a.logits + static_cast<long long>(t) * a.E, a.E, lane, x);
         const float lse = row_softmax<N, false>(x, inv, nullptr, unused, mask);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
@@ -675,9 +661,9 @@ __global__ void __launch_bounds__(kLossThreads, N <= 8 ? 4 : 2) k_loss_bwd(const
       float x[N];
       if (live) {
         if constexpr (VEC == 4)
-          load_shared_row<N, VEC>(row, a.E, lane, x);
+          load_shared_row(row, a.E, lane, x);
         else
-          load_row<N, VEC>(a.logits + static_cast<long long>(t) * a.E, a.E, lane, -INFINITY, x);
+          load_row(a.logits + static_cast<long long>(t) * a.E, a.E, lane, x);
         float inv, dot;
         const float lse = row_softmax<N, true>(x, inv, f, dot, mask);
         const float b = scale * inv * a.balance;

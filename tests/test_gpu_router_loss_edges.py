@@ -1,6 +1,6 @@
 """Router's losses at the edges of what they take: rows of logits far from zero,
-squares whose sum is out of range, losses without a coefficient, calls from two host
-threads at once.
+squares whose sum is out of range, losses without a coefficient, arrays off 16-byte
+boundaries, chunks of the most tokens, calls from two host threads at once.
 
 Bounds: those of test_gpu_router_loss.py."""
 import threading
@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_router_loss import backward, check_backward, check_forward, forward, make
+from tests.test_gpu_router_loss import backward, check_backward, check_forward, forward, gpu, make
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -134,3 +134,55 @@ def test_a_loss_without_a_coefficient_is_left_out(T):
     logits[9, 3] = np.nan
     for coefficients in ((0.5, 0.0), (0.0, 1e-3), (0.5, 1e-3)):
         assert np.isnan(forward(logits, idx, 1, *coefficients)[1]["loss"]).all()
+
+
+def apart(v, by):
+    """v on the GPU, `by` elements past a 16-byte boundary."""
+    v = np.ascontiguousarray(v)
+    t = torch.from_numpy(v)
+    room = torch.zeros(v.size + 4, dtype=t.dtype, device="cuda")
+    view = room[by:by + v.size].view(v.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 32, 4), (300, 64, 6), (300, 128, 4), (1100, 32, 2),
+                                   (1100, 64, 6), (1100, 128, 8), (1100, 256, 8)])
+@pytest.mark.parametrize("which,by", [("logits", 1), ("logits", 2), ("dlogits", 3), ("counts", 1),
+                                      ("all", 1)])
+def test_arrays_that_no_vector_load_reaches(T, E, k, which, by):
+    """Rows of whole 16 bytes in arrays that do not start on such a boundary."""
+    import moe_expert_mlp_gb300 as m
+    S = 3
+    logits, idx, mask, offsets = make(T, E, k, S, T + E, masked=True)
+    rng = np.random.default_rng(4)
+    w = rng.random((T, k)).astype(np.float32)
+    dw = (rng.standard_normal((T, k)) / T).astype(np.float32)
+    at = {n: by if which in (n, "all") else 0 for n in ("logits", "dlogits", "counts")}
+    x = apart(logits, at["logits"])
+    desc = m.make_router_loss_desc(T, E, k, S, 0.5, 0.25)
+    ws = torch.empty(m.moe_router_loss_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    out = dict(counts=apart(np.full((S, E), -9, np.int32), at["counts"]),
+               tokens=torch.full((S + 1,), -9, dtype=torch.int32, device="cuda"),
+               probs=torch.full((S, E), -9.0, device="cuda"), loss=torch.full((3,), -9.0, device="cuda"))
+    dlogits = apart(np.full((T, E), -9, np.float32), at["dlogits"])
+    on = dict(idx=gpu(idx), mask=gpu(mask), offsets=gpu(offsets), w=gpu(w), dw=gpu(dw))
+    m.moe_router_loss_fwd(desc, x, on["idx"], on["mask"], on["offsets"], out["counts"],
+                          out["tokens"], out["probs"], out["loss"], ws)
+    m.moe_router_loss_bwd(desc, x, on["mask"], on["offsets"], out["counts"], out["tokens"], None,
+                          dict(dw=on["dw"], topk_w=on["w"], topk_idx=on["idx"]), dlogits)
+    got = {n: t.cpu().numpy() for n, t in out.items()}
+    check_forward(logits, idx, S, 0.5, 0.25, mask, offsets, got)
+    check_backward(logits, k, S, 0.5, 0.25, mask, offsets, got,
+                   dlogits.cpu().numpy().astype(np.float64), 1.0, (dw, w, idx))
+    assert m.moe_read_device_status() == 0
+
+
+@pytest.mark.parametrize("T,E,k", [(640_001, 8, 2), (320_003, 68, 4)])
+def test_chunks_of_the_most_tokens(T, E, k):
+    """More tokens than blocks of 1024 hold in one wave."""
+    logits, idx, mask, offsets = make(T, E, k, 3, 9, masked=True)
+    desc, got, out = forward(logits, idx, 3, 0.5, 0.25, mask, offsets)
+    check_forward(logits, idx, 3, 0.5, 0.25, mask, offsets, got)
+    d = backward(desc, logits, idx, mask, offsets, out)
+    check_backward(logits, k, 3, 0.5, 0.25, mask, offsets, got, d, 1.0, None)
