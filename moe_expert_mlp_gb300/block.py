@@ -100,6 +100,7 @@ class MoEResidualBlock:
         if self.token_gate and gate is None:
             raise ValueError("a token gate needs its values")
         layer, t = self.layer, self.layer._t
+        layer._check_loss_inputs(mask, seq_offsets)
         self.gate = gate if self.token_gate else self.params.get("gate")
         with t(timer, "pre_norm"):
             self.forward_norm(res, stream)

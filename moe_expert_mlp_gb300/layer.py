@@ -229,6 +229,7 @@ class MoEExpertMLP:
         """Routing and permutation; mask (bool or uint8 [T]) and seq_offsets (int32
         [sequences+1]) are the router's losses' (which keep them, and the logits,
         for the backward)."""
+        self._check_loss_inputs(mask, seq_offsets)
         with self._t(timer, "route_permute"):
             if self.mx:          # x_perm's rowwise MXFP8 copy written by the gather
                 L.moe_route_permute_mx(self.desc, logits, bias, x, self.topk_idx, self.topk_w,
@@ -243,11 +244,13 @@ class MoEExpertMLP:
                                     self.ws, stream)
         self._router_losses(logits, mask, seq_offsets, stream, timer)
 
+    def _check_loss_inputs(self, mask, seq_offsets):
+        if self.loss_desc is None and (mask is not None or seq_offsets is not None):
+            raise ValueError("a mask and sequences belong to the router's losses, whose "
+                             "coefficients are 0")
+
     def _router_losses(self, logits, mask, seq_offsets, stream, timer):
         if self.loss_desc is None:
-            if mask is not None or seq_offsets is not None:
-                raise ValueError("a mask and sequences belong to the router's losses, whose "
-                                 "coefficients are 0")
             return
         self._loss_inputs = (logits, mask, seq_offsets)
         with self._t(timer, "router_loss"):
@@ -269,6 +272,7 @@ class MoEExpertMLP:
         (x W_r^T) with the top-k in its epilogue, then the same permutation
         as route(); w_router bf16 [E,d]; logits_out fp32 [T,E] or None (the
         router's losses need them); mask, seq_offsets as route()."""
+        self._check_loss_inputs(mask, seq_offsets)
         if self.loss_desc is not None and logits_out is None:
             raise ValueError("the router's losses read the logits: give logits_out")
         self._x_row_fused = False
