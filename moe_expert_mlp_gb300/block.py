@@ -76,12 +76,17 @@ class MoEResidualBlock:
         self.norm_ws = torch.empty(L.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=dev)
         self.updates = None            # the experts', see orthogonal_updates
 
-    def orthogonal_updates(self, **kw):
+    def orthogonal_updates(self, padding=True, **kw):
         """From now on step() ends with the orthogonalised updates of the experts'
         weights, self.updates.outs for layer.w1p and layer.w2 (their clipped
-        gradients' matrices, one an expert; the packed FC1's padding rows stay
-        zero); kw: as OrthogonalUpdates."""
-        self.updates = OrthogonalUpdates([self.layer.dw1p, self.layer.dw2], **kw)
+        gradients' matrices, one an expert: gate and linear half of FC1 together;
+        the packed FC1's padding rows stay zero); kw: as OrthogonalUpdates.  The scale
+        goes by the packed rows, 2*Fp, which with F not a multiple of 128 makes FC1's
+        update larger by up to sqrt(Fp/F); with padding=False by the weights' own."""
+        layer = self.layer
+        if not padding:
+            kw["sizes"] = [(2 * layer.F if layer.gated else layer.F, layer.d), (layer.d, layer.F)]
+        self.updates = OrthogonalUpdates([layer.dw1p, layer.dw2], **kw)
         return self.updates
 
     def forward_norm(self, res, stream=None):
