@@ -1,5 +1,6 @@
-"""Orthogonalised updates of matrices that are zero or next to it, with an eps as
-small as fp32 has one.  Bounds: those of test_gpu_orthogonalize.py."""
+"""Orthogonalised updates of long thin matrices, and of matrices that are zero or
+next to it, with an eps as small as fp32 has one.  Bounds: those of
+test_gpu_orthogonalize.py."""
 import numpy as np
 import pytest
 import torch
@@ -39,3 +40,11 @@ def test_matrices_of_the_smallest_numbers(shape, size, eps):
 def test_matrices_of_the_largest_numbers(shape):
     g = np.clip(values(shape, "full", 3), -3, 3) * 1.1e38
     check(*run(g, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 4104), (3, 64, 7168), (2, 1, 5000), (1, 9, 16384),
+                                   (2, 33, 4500), (1, 128, 2056), (2, 100, 7168), (1, 256, 7168)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_long_thin_matrices_that_no_cluster_holds(shape, tall):
+    b, m, n = shape
+    check(*run(values((b, n, m) if tall else shape, "full", 4)))
