@@ -1020,7 +1020,7 @@ moe_status_t moe_router_loss_bwd(const moe_router_loss_desc_t* desc, const float
  * an Inf or NaN reaches its own matrix only.  With a short side above 128, or a long
  * one that eight SMs' registers do not hold, the steps are one cooperative launch
  * that takes as many SMs as there are tiles (MOE_ERR_CUDA where it cannot be
- * resident). */
+ * resident; the momentum has then been stepped). */
 typedef struct {
   void* p;        /* element (i, r, c) at p[i*plane + r*ld + c]; inputs are not written */
   int64_t ld;     /* elements from one row to the next */
@@ -1045,8 +1045,9 @@ moe_status_t moe_orthogonalize_workspace_size(const moe_orthogonalize_desc_t* de
 
 /* grad (grad_dtype), mom and mom_out (fp32; all NULL with momentum 0: no
  * momentum is kept) -> out (bf16).  Any strides with ld >= cols and, of what is
- * written, matrices apart.  mom_out may be mom, and out may be grad of the same
- * strides; otherwise a written tensor shares no memory with another. */
+ * written, matrices apart.  mom_out may be mom and, where grad is bf16, out may be
+ * grad, of the same strides; otherwise a written tensor shares no memory with
+ * another. */
 moe_status_t moe_orthogonalize(const moe_orthogonalize_desc_t* desc, moe_matrices_t grad,
                                moe_matrices_t mom, moe_matrices_t mom_out, moe_matrices_t out,
                                void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -1005,8 +1005,10 @@ cudaError_t launch_steps(OrthoArgs& g, int sms, cudaStream_t s) {
   const long long tiles = sym(g.sym_w) > full(g.full_w) ? sym(g.sym_w) : full(g.full_w);
   const long long pairs = tiles < most ? tiles : most;
   // together as many matrices as give A's product two tiles a pair: then a
-  // product's inputs are done by the time the list comes to it, and no more
-  // matrices than that take turns in L2
+  // product's inputs are done by the time the list comes to it.  (Not for L2: 8
+  // matrices of 2048 x 1408 are 248 MB of operands and state, of which 80 bytes an
+  // element pass through DRAM in five steps; but half as many, one tile a pair, took
+  // 5.6 ms for 64 instead of 4.8, as each wait stands bare then.)
   const int each = sym_tiles(g.m, g.sym_w);
   const long long together = (2 * pairs + each - 1) / each;
   g.groups = static_cast<int>(g.batch > together ? g.batch / together : 1);

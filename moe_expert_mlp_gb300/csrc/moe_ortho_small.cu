@@ -16,7 +16,7 @@
 // exchanges and of chains of small products, which mma.sync starts and ends in tens
 // of cycles; a tcgen05 tile would be mostly empty at m = 64 and has to come back
 // from TMEM each time (64 x 2048 with a momentum: 15 products of the general kernel
-// took 139 us, this 22).  A step of it is 6,200 cycles: 900 for the first product and
+// took 139 us, this 24.6).  A step of it is 6,200 cycles: 900 for the first product and
 // 1,000 for the last (the operands' way out of shared memory), 800 for the second,
 // 3,300 for the two exchanges.  With sides of 65 to 128 the exchanges are most of a
 // step, as shared memory of other CTAs gives and takes some 10 bytes a cycle.
@@ -583,8 +583,8 @@ cudaError_t launch_shape(const SmallOrthoArgs& g, int ctas, cudaStream_t s) {
 // The fewest columns a CTA (8 NB for each of its warps along the columns) that leave a
 // matrix in one cluster and all clusters on the GPU at once: more CTAs have shorter
 // products, fewer have less to exchange.  More than eight where they keep 64 columns
-// (16 instead of 8: 64 x 2048 27 -> 22 us, 128 x 2048 72 -> 59, 128 x 1024 53 -> 52;
-// with 32 columns each 128 x 512 46 -> 50).
+// (16 instead of 8: 64 x 2048 with a momentum 29.2 -> 24.6 us, 128 x 2048 72 -> 59,
+// 128 x 1024 53 -> 52; with 32 columns each 128 x 512 46 -> 50).
 template <int MP, int NB>
 cudaError_t launch_rows(const SmallOrthoArgs& g, int n, int sms, cudaStream_t s) {
   const int ctas = (n + SmallShape<MP, NB>::kCols - 1) / SmallShape<MP, NB>::kCols;
